@@ -20,7 +20,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpctree.so")
 
-PCT_F32, PCT_BF16 = 0, 1
+PCT_F32, PCT_BF16, PCT_F16 = 0, 1, 2
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration",
            3: "workspace too small", 4: "HIP error"}
 
@@ -40,6 +40,13 @@ class TreeShape(C.Structure):
 class CostModel(C.Structure):
     _fields_ = [("C_d", C.c_double), ("c0", C.c_double), ("c1", C.c_double),
                 ("c2", C.c_double), ("c_ell", C.c_double)]
+
+
+class CacheShape(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("N", C.c_int32),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages", C.c_int32), ("Hq", C.c_int32),
+                ("Hkv", C.c_int32), ("D", C.c_int32), ("dtype", C.c_int32)]
 
 
 _lib = None
@@ -85,6 +92,18 @@ def lib():
                                     sz, P]
     L.pct_verify_sample_workspace.argtypes = [i32, i32, i32]
     L.pct_verify_sample_workspace.restype = sz
+    shape = C.POINTER(CacheShape)
+    L.pct_cache_plan_workspace.argtypes = [i32]
+    L.pct_cache_plan_workspace.restype = sz
+    L.pct_cache_plan.argtypes = [shape, P, P, P, P, P, P, P, P, P, P, P, sz,
+                                 P]
+    L.pct_cache_write.argtypes = [shape, P, i64, P, i64, P, P, P, P]
+    L.pct_tree_attention_workspace.argtypes = [shape]
+    L.pct_tree_attention_workspace.restype = sz
+    L.pct_tree_attention.argtypes = [shape, C.c_float, P, i64, P, P, P, P, P,
+                                     P, P, P, P, sz, P]
+    L.pct_cache_commit.argtypes = [shape, i32, i64, i32, P, P, P, P, P, P, P,
+                                   P, P]
     L.pct_profile_enable.argtypes = [i32]
     L.pct_profile_reset.argtypes = []
     L.pct_profile_read.argtypes = [i32, i64, C.POINTER(C.c_double),
@@ -104,14 +123,18 @@ def exported_symbols():
             "pct_build_tree_adaptive_pc_workspace", "pct_throughput_curve",
             "pct_build_tree_noalloc", "pct_verify_sample",
             "pct_verify_sample_workspace",
-            "pct_tree_mask", "pct_verify_accept", "pct_profile_enable",
+            "pct_tree_mask", "pct_verify_accept",
+            "pct_cache_plan", "pct_cache_plan_workspace", "pct_cache_write",
+            "pct_tree_attention", "pct_tree_attention_workspace",
+            "pct_cache_commit", "pct_profile_enable",
             "pct_profile_reset", "pct_profile_read", "pct_status_string",
             "pct_last_error"]
 
 
 PROF_MARKOV, PROF_EXPAND, PROF_TOPN, PROF_MASK, PROF_ACCEPT, PROF_ROWTOP, \
     PROF_INIT, PROF_ROWSTATS, PROF_BESTFIRST, PROF_FINALIZE, PROF_STOP, \
-    PROF_SAMPLE = range(12)
+    PROF_SAMPLE, PROF_PLAN, PROF_CACHE_WRITE, PROF_ATTEND, PROF_JOIN, \
+    PROF_COMMIT = range(17)
 
 
 def profile_enable(on: bool = True):
@@ -474,6 +497,298 @@ def verify_sample(tok, parent, depth, n_nodes, target_logits, B: int,
         int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(sm), _ptr(tau), _ptr(an),
         _ptr(at), _ptr(workspace), workspace.numel(), _stream(dev)))
     return sm, tau, an, at
+
+
+# ---------------------------------------------------------------------------
+# paged key-value cache: pct_cache_plan / pct_cache_write /
+# pct_tree_attention / pct_cache_commit
+
+_CACHE_TYPES = {torch.bfloat16: PCT_BF16, torch.float16: PCT_F16}
+
+
+def _cache_dtype(dtype) -> int:
+    if dtype not in _CACHE_TYPES:
+        raise ValueError("the cache holds bfloat16 or float16")
+    return _CACHE_TYPES[dtype]
+
+
+def _want(name, t, dtype, shape, device):
+    """Check one tensor of a cache call and return its address."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of "
+                         f"shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, device):
+    """Check rows [batch][R][heads][D] whose heads are contiguous and whose
+    rows are evenly spaced (a joint projection's view); returns the address
+    and the row stride."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape "
+                         f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    b, R, H, D = shape
+    sb, sr, sh, sd = t.stride()
+    if R == 1:
+        sr = sb if b > 1 else H * D
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (b > 1 and
+                                                      sb != R * sr):
+        raise ValueError(f"{name} needs contiguous heads and evenly spaced "
+                         f"rows, got strides {t.stride()}")
+    return t.data_ptr(), sr
+
+
+class _on:
+    """Makes a device current for a call when it is not."""
+
+    def __init__(self, device):
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _device(device) -> torch.device:
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+@dataclass
+class CacheRows:
+    """Where a round's rows go: slot [batch][N+1] int64 (-1: none), pos
+    [batch][N+1] int32 (place in the sequence, -1 for unused rows), missing
+    [batch] int32 (pages that the free ring could not give)."""
+    slot: torch.Tensor
+    pos: torch.Tensor
+    missing: torch.Tensor
+
+
+class CachePlan:
+    """Page plan of fixed shape with its workspace and outputs allocated
+    once; run() only enqueues kernels."""
+
+    def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
+                 max_pages: int, device="cuda"):
+        self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, 1, 1,
+                                16, PCT_BF16)
+        self.device = _device(device)
+        dev = self.device
+        self.ws = _workspace(lib().pct_cache_plan_workspace(batch), dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.out = CacheRows(
+            slot=torch.empty(batch, N + 1, dtype=torch.int64, device=dev),
+            pos=torch.empty(batch, N + 1, **i32),
+            missing=torch.empty(batch, **i32))
+
+    def run(self, ctx_len, n_nodes, block_table, n_held, ring, ring_state,
+            depth=None) -> CacheRows:
+        """n_nodes None = N everywhere; depth [batch][N] gives nodes their
+        place in the sequence and is required unless N = 0."""
+        sh, o, dev, i32 = self.shape, self.out, self.device, torch.int32
+        one = (sh.batch,)
+        if depth is None and sh.N > 0:
+            raise ValueError("depth is required when N > 0")
+        args = (_want("ctx_len", ctx_len, i32, one, dev),
+                None if n_nodes is None else
+                _want("n_nodes", n_nodes, i32, one, dev),
+                None if sh.N == 0 else
+                _want("depth", depth, i32, (sh.batch, sh.N), dev),
+                _want("block_table", block_table, i32,
+                      (sh.batch, sh.max_pages), dev),
+                _want("n_held", n_held, i32, one, dev),
+                _want("ring", ring, i32, (sh.n_pages,), dev),
+                _want("ring_state", ring_state, i32, (2,), dev))
+        with _on(dev):
+            _check(lib().pct_cache_plan(
+                C.byref(sh), *args, o.slot.data_ptr(), o.pos.data_ptr(),
+                o.missing.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                _stream(dev)))
+        return o
+
+
+def cache_write(k, v, slot, k_cache, v_cache):
+    """Write the rows k, v [batch][R][Hkv][D] (views with evenly spaced rows
+    allowed) into slots slot [batch][R] of k_cache, v_cache
+    [n_pages][Hkv][page_size][D]; a slot outside the cache is left out."""
+    dev = _dev(k_cache)
+    n_pages, Hkv, page, D = k_cache.shape
+    batch, R = slot.shape
+    dt = k_cache.dtype
+    sh = CacheShape(batch, R - 1, n_pages, page, 1, Hkv, Hkv, D,
+                    _cache_dtype(dt))
+    kp, ks = _rows("k", k, dt, (batch, R, Hkv, D), dev)
+    vp, vs = _rows("v", v, dt, (batch, R, Hkv, D), dev)
+    sp = _want("slot", slot, torch.int64, slot.shape, dev)
+    kc = _want("k_cache", k_cache, dt, k_cache.shape, dev)
+    vc = _want("v_cache", v_cache, dt, k_cache.shape, dev)
+    with _on(dev):
+        _check(lib().pct_cache_write(C.byref(sh), kp, ks, vp, vs, sp, kc, vc,
+                                     _stream(dev)))
+
+
+class TreeAttention:
+    """Attention of a round's rows over a paged cache, fixed shape, with its
+    workspace and outputs allocated once; run() only enqueues kernels."""
+
+    def __init__(self, batch: int, N: int, Hq: int, Hkv: int, D: int,
+                 n_pages: int, page_size: int, max_pages: int,
+                 dtype=torch.bfloat16, lse: bool = False, device="cuda"):
+        self.dtype = dtype
+        self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, Hq,
+                                Hkv, D, _cache_dtype(dtype))
+        self.device = _device(device)
+        dev = self.device
+        nbytes = lib().pct_tree_attention_workspace(C.byref(self.shape))
+        if nbytes == 0:
+            raise PCTError(1, lib().pct_last_error().decode())
+        self.ws = _workspace(nbytes, dev)
+        # unused rows are never written: they stay zero
+        self.out = torch.zeros(batch, N + 1, Hq, D, dtype=dtype, device=dev)
+        self.lse = (torch.zeros(batch, N + 1, Hq, dtype=torch.float32,
+                                device=dev) if lse else None)
+
+    def run(self, q, k_cache, v_cache, block_table, ctx_len, n_nodes=None,
+            mask=None, scale=None, out=None):
+        """q [batch][N+1][Hq][D] (a view with evenly spaced rows allowed),
+        mask [batch][N][ceil(N/64)] int64 or None (straight drafts); scale
+        defaults to 1/sqrt(D).  Returns (out, lse), lse None unless the
+        handle keeps it; out: another tensor for the outputs."""
+        sh, dev, dt, i32 = self.shape, self.device, self.dtype, torch.int32
+        rows = (sh.batch, sh.N + 1, sh.Hq, sh.D)
+        cache = (sh.n_pages, sh.Hkv, sh.page_size, sh.D)
+        if out is None:
+            out = self.out
+            op = out.data_ptr()
+        else:
+            op = _want("out", out, dt, rows, dev)
+        qp, qs = _rows("q", q, dt, rows, dev)
+        args = (qp, qs, _want("k_cache", k_cache, dt, cache, dev),
+                _want("v_cache", v_cache, dt, cache, dev),
+                _want("block_table", block_table, i32,
+                      (sh.batch, sh.max_pages), dev),
+                _want("ctx_len", ctx_len, i32, (sh.batch,), dev),
+                None if n_nodes is None else
+                _want("n_nodes", n_nodes, i32, (sh.batch,), dev),
+                None if mask is None or sh.N == 0 else
+                _want("mask", mask, torch.int64,
+                      (sh.batch, sh.N, (sh.N + 63) // 64), dev))
+        with _on(dev):
+            _check(lib().pct_tree_attention(
+                C.byref(sh), sh.D ** -0.5 if scale is None else scale, *args,
+                op, None if self.lse is None else self.lse.data_ptr(),
+                self.ws.data_ptr(), self.ws.numel(), _stream(dev)))
+        return out, self.lse
+
+
+def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes=None,
+                   mask=None, scale=None, lse: bool = False):
+    """One call of TreeAttention: q [batch][N+1][Hq][D] over k_cache, v_cache
+    [n_pages][Hkv][page_size][D].  Returns (out, lse or None)."""
+    batch, R, Hq, D = q.shape
+    n_pages, Hkv, page, _ = k_cache.shape
+    h = TreeAttention(batch, R - 1, Hq, Hkv, D, n_pages, page,
+                      block_table.shape[1], dtype=k_cache.dtype, lse=lse,
+                      device=_dev(k_cache))
+    return h.run(q, k_cache, v_cache, block_table, ctx_len, n_nodes, mask,
+                 scale)
+
+
+def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
+                 v_cache, out=None):
+    """Keep the accepted paths: tau [batch] and accept_node [batch][B] as
+    verify_accept returns them, n_nodes [batch] or None (no padded request),
+    k_cache, v_cache [layers][n_pages][Hkv][page_size][D] (or one layer).
+    Returns the new context lengths, in `out` when given (which may be
+    ctx_len itself)."""
+    dev = _dev(k_cache)
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    n_pages, Hkv, page, D = k_cache.shape[-4:]
+    batch, B = accept_node.shape
+    dt, i32 = k_cache.dtype, torch.int32
+    if out is None:
+        out = torch.empty_like(ctx_len)
+    # the rows are not read: any number of nodes up to the largest may be
+    # accepted
+    sh = CacheShape(batch, 8192, n_pages, page, block_table.shape[1], Hkv,
+                    Hkv, D, _cache_dtype(dt))
+    args = (_want("tau", tau, i32, (batch,), dev),
+            _want("accept_node", accept_node, i32, (batch, B), dev),
+            None if n_nodes is None else
+            _want("n_nodes", n_nodes, i32, (batch,), dev),
+            _want("block_table", block_table, i32,
+                  (batch, block_table.shape[1]), dev),
+            _want("ctx_len", ctx_len, i32, (batch,), dev),
+            _want("k_cache", k_cache, dt, k_cache.shape, dev),
+            _want("v_cache", v_cache, dt, k_cache.shape, dev),
+            _want("out", out, i32, (batch,), dev))
+    with _on(dev):
+        _check(lib().pct_cache_commit(
+            C.byref(sh), layers, n_pages * Hkv * page * D, B, *args,
+            _stream(dev)))
+    return out
+
+
+class PagedCache:
+    """A paged key-value cache of a serving batch: k, v
+    [layers][n_pages][Hkv][page_size][D], the block table, the pages held,
+    the free ring and the context lengths of `batch` places.
+
+    A round: rows = plan(n_nodes, depth); in each layer write(layer, k, v)
+    and attend(layer, q, mask); then commit(tau, accept_node).  A place is
+    emptied by setting its ctx_len to 0 and its n_nodes to -1 for one plan.
+    """
+
+    def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
+                 max_pages: int, Hq: int, Hkv: int, D: int, layers: int = 1,
+                 dtype=torch.bfloat16, device="cuda"):
+        dev = _device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.k = torch.zeros(layers, n_pages, Hkv, page_size, D, dtype=dtype,
+                             device=dev)
+        self.v = torch.zeros_like(self.k)
+        self.block_table = torch.full((batch, max_pages), -1, **i32)
+        self.n_held = torch.zeros(batch, **i32)
+        self.ring = torch.arange(n_pages, **i32)
+        self.ring_state = torch.tensor([0, n_pages], **i32)
+        self.ctx_len = torch.zeros(batch, **i32)
+        self.n_nodes = None
+        self._plan = CachePlan(batch, N, n_pages, page_size, max_pages,
+                               device=dev)
+        self._attend = TreeAttention(batch, N, Hq, Hkv, D, n_pages, page_size,
+                                     max_pages, dtype=dtype, device=dev)
+
+    def plan(self, n_nodes=None, depth=None) -> CacheRows:
+        self.n_nodes = n_nodes
+        return self._plan.run(self.ctx_len, n_nodes, self.block_table,
+                              self.n_held, self.ring, self.ring_state,
+                              depth=depth)
+
+    def write(self, layer: int, k, v):
+        cache_write(k, v, self._plan.out.slot, self.k[layer], self.v[layer])
+
+    def attend(self, layer: int, q, mask=None, scale=None, out=None):
+        return self._attend.run(q, self.k[layer], self.v[layer],
+                                self.block_table, self.ctx_len, self.n_nodes,
+                                mask=mask, scale=scale, out=out)[0]
+
+    def commit(self, tau, accept_node):
+        return cache_commit(tau, accept_node, self.ctx_len, self.n_nodes,
+                            self.block_table, self.k, self.v,
+                            out=self.ctx_len)
 
 
 def bf16_tensor(bits, device="cuda") -> torch.Tensor:

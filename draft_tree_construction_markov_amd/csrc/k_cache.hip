@@ -1,0 +1,287 @@
+// k_cache.hip -- the paged key-value cache of the target's side of a round:
+// block tables and slots from the requests' lengths, the rows' keys and
+// values into their slots, and the accepted path's rows to their places
+// behind the context.
+#include "pct_cache.h"
+#include "pct_device.h"
+
+namespace pct {
+
+// ---------------------------------------------------------------------
+// Page plan.  With need_b = ceil((ctx_b + n_b + 1) / page), want_b =
+// max(need_b - held_b, 0) and back_b = max(held_b - need_b, 0), request b
+// takes want_b pages from the free ring at offset sum_{b' < b} want_b' when
+// sum_{b' <= b} want_b' is at most the ring's count, and gives back_b pages
+// to its tail at offset sum_{b' < b} back_b'.  The free part and the part
+// behind it never meet (free and held pages together are at most n_pages),
+// so takes and gives of different requests need no order between them.
+//
+// plan_scan: one workgroup computes both prefix sums and the new state;
+// plan_apply: block tables, ring entries, slots and places, a workgroup for
+// each piece of a request's rows.
+
+constexpr int kScanThreads = 1024;
+constexpr int kApplyThreads = 256;
+constexpr int kApplyRows = 1024;  // rows per workgroup of plan_apply
+
+__device__ __forceinline__ int64_t pages_for(int64_t tokens, int shift) {
+  return (tokens + ((1 << shift) - 1)) >> shift;
+}
+
+// inclusive prefix sums of two values over the workgroup
+__device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b,
+                                            int64_t (*sum)[2], int tid) {
+  const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int64_t x = __shfl_up(a, d, kWave), y = __shfl_up(b, d, kWave);
+    if (lane >= d) {
+      a += x;
+      b += y;
+    }
+  }
+  if (lane == kWave - 1) {
+    sum[wave][0] = a;
+    sum[wave][1] = b;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    a += sum[w][0];
+    b += sum[w][1];
+  }
+}
+
+__global__ __launch_bounds__(kScanThreads) void plan_scan_kernel(PlanArgs a) {
+  __shared__ int64_t sum[kScanThreads / kWave][2];
+  __shared__ int64_t total[3];  // wanted, given back, taken
+  const int tid = threadIdx.x;
+  const PageGeom& g = a.g;
+  const int head0 = a.ring_state[0], count0 = a.ring_state[1];
+  const int head = ((head0 % g.n_pages) + g.n_pages) % g.n_pages;
+  const int count = min(max(count0, 0), g.n_pages);
+  if (tid == 0) total[0] = total[1] = total[2] = 0;
+  for (int b0 = 0; b0 < g.batch; b0 += kScanThreads) {
+    __syncthreads();
+    const int b = b0 + tid;
+    const bool in = b < g.batch;
+    int held = 0;
+    int64_t need = 0;
+    if (in) {
+      held = min(max(a.held[b], 0), g.max_pages);
+      const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+      need = pages_for((int64_t)clamp_ctx(g.ctx_len[b]) + n + 1, g.shift);
+    }
+    const int to = (int)min(need, (int64_t)g.max_pages);
+    const int64_t want = max(to - held, 0), back = max(held - to, 0);
+    int64_t wi = want, bi = back;
+    block_scan2(wi, bi, sum, tid);
+    wi += total[0];
+    bi += total[1];
+    const bool fits = wi <= count;
+    __syncthreads();
+    if (in) {
+      const int after = fits ? to : min(held, to);
+      // (offsets into the ring; the first is used only where it fits)
+      a.req[b] = make_int4((int)(wi - want), (int)((bi - back) % g.n_pages),
+                           held, after);
+      a.held[b] = after;
+      a.missing[b] = (int)(need - after);
+      // the last request that is served has the largest sum
+      if (fits) atomicMax((unsigned long long*)&total[2],
+                          (unsigned long long)wi);
+      if (b == g.batch - 1 || tid == kScanThreads - 1) {
+        total[0] = wi;
+        total[1] = bi;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    a.ring0[0] = make_int2(head, count);
+    a.ring_state[0] = (int)((head + total[2]) % g.n_pages);
+    a.ring_state[1] = (int)min(count - total[2] + total[1],
+                               (int64_t)g.n_pages);
+  }
+}
+
+__global__ __launch_bounds__(kApplyThreads) void plan_apply_kernel(
+    PlanArgs a) {
+  const PageGeom& g = a.g;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int4 rq = a.req[b];
+  const int2 ring0 = a.ring0[0];
+  const int held = rq.z, after = rq.w;
+  const int P = g.n_pages;
+  int32_t* table = a.table + (int64_t)b * g.max_pages;
+  if (blockIdx.y == 0) {
+    for (int j = held + tid; j < after; j += kApplyThreads)
+      table[j] = a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
+    for (int j = after + tid; j < held; j += kApplyThreads) {
+      a.ring[((int64_t)ring0.x + ring0.y + rq.y + j - after) % P] = table[j];
+      table[j] = -1;
+    }
+  }
+  const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+  const int ctx = clamp_ctx(g.ctx_len[b]);
+  const int R = g.N + 1;
+  const int r1 = min((int)(blockIdx.y + 1) * kApplyRows, R);
+  const int page_mask = (1 << g.shift) - 1;
+  for (int i = blockIdx.y * kApplyRows + tid; i < r1; i += kApplyThreads) {
+    int64_t s = -1;
+    int place = -1;
+    if (i <= n) {
+      const int p = ctx + i, j = p >> g.shift;
+      if (j < after) {
+        // pages taken by this call are read where they come from: another
+        // workgroup may not have written them to the table yet
+        const int page =
+            j < held ? table[j]
+                     : a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
+        if (page >= 0 && page < P)
+          s = ((int64_t)page << g.shift) + (p & page_mask);
+      }
+      if (a.pos) place = ctx + (i > 0 ? a.depth[(int64_t)b * g.N + i - 1] : 0);
+    }
+    a.slot[(int64_t)b * R + i] = s;
+    if (a.pos) a.pos[(int64_t)b * R + i] = place;
+  }
+}
+
+hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int pieces = (a.g.N + kApplyRows) / kApplyRows;
+  hipLaunchKernelGGL(plan_apply_kernel, dim3(a.g.batch, pieces),
+                     dim3(kApplyThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------
+// Row writes: one thread copies a 16-byte piece of a row's key and of its
+// value; consecutive threads take consecutive pieces of a row.
+__global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
+  const int hc = a.D / 8, rc = a.Hkv * hc;  // pieces of a head, of a row
+  const int64_t total = a.rows * rc;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / rc;
+    const int c = (int)(i - row * rc);
+    const int64_t slot = a.slot[row];
+    if (slot < 0 || slot >= a.n_slots) continue;
+    const int h = c / hc;
+    const int64_t page = slot >> a.shift;
+    const int64_t off = slot & ((1 << a.shift) - 1);
+    const int64_t to =
+        (((page * a.Hkv + h) << a.shift) + off) * hc + (c - h * hc);
+    a.kc[to] = a.k[row * a.ks + c];
+    a.vc[to] = a.v[row * a.vs + c];
+  }
+}
+
+hipError_t launch_cache_write(const WriteArgs& a, hipStream_t s) {
+  const int64_t total = a.rows * a.Hkv * (a.D / 8);
+  const int64_t blocks = (total + 255) / 256;
+  hipLaunchKernelGGL(cache_write_kernel,
+                     dim3((unsigned)(blocks < 65536 ? blocks : 65536)),
+                     dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------
+// Commit: node a_j of the accepted path moves to the place of node j.  The
+// path is ascending, so a_j >= j: a thread that moves one 16-byte column of
+// its request in ascending j, kMove sources loaded before their stores,
+// reads every source before anything overwrites it (a later source a_j is
+// at least j, past every place written so far), and columns do not touch
+// each other.  Moves onto themselves are left out.
+constexpr int kMove = 8;
+constexpr int kMoveList = 128;  // moves resolved to slots at a time
+
+__global__ __launch_bounds__(256) void cache_commit_kernel(CommitArgs a,
+                                                           int write_len) {
+  __shared__ int64_t from[kMoveList], to[kMoveList];
+  __shared__ int s_end;
+  const PageGeom& g = a.g;
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+  const int ctx = clamp_ctx(g.ctx_len[b]);
+  const int tau = min(max(a.tau[b], 0), a.B + 1);
+  if (write_len && blockIdx.x == 0 && tid == 0)
+    a.ctx_out[b] = n < 0 ? g.ctx_len[b] : ctx + tau;
+  const int moves = n < 0 ? 0 : min(min(tau - 1, a.B), n);
+  const int hc = g.D / 8;
+  const int cols = a.layers * g.Hkv * hc * 2;
+  const int col = blockIdx.x * 256 + tid;
+  const bool live = col < cols;
+  // column = ((layer * Hkv + head) * 2 + value) * hc + piece
+  const int c = live ? col % hc : 0, hkv = live ? col / hc : 0;
+  const int lh = hkv >> 1, h = lh % g.Hkv;
+  uint4* cache = (hkv & 1) ? a.vc : a.kc;
+  cache += (int64_t)(lh / g.Hkv) * a.layer_stride +
+           ((int64_t)h << g.shift) * hc + c;
+  const int32_t* table = g.table + (int64_t)b * g.max_pages;
+  const int32_t* acc = a.accept + (int64_t)b * a.B;
+  const int64_t page_chunks = ((int64_t)g.Hkv << g.shift) * hc;
+  auto place = [&](int64_t p) -> int64_t {  // chunk of a position, -1: none
+    const int64_t j = p >> g.shift;
+    const int page = j < g.max_pages ? table[j] : -1;
+    if (page < 0 || page >= g.n_pages) return -1;
+    return page * page_chunks + (p & ((1 << g.shift) - 1)) * hc;
+  };
+  for (int j0 = 0; j0 < moves; j0 += kMoveList) {
+    if (tid == 0) s_end = min(moves - j0, kMoveList);
+    __syncthreads();
+    const int j = j0 + tid;
+    if (tid < kMoveList && j < moves) {
+      const int nd = acc[j];
+      if (nd < 0 || nd >= n) {
+        atomicMin(&s_end, tid);
+      } else {
+        const int64_t f = place((int64_t)ctx + 1 + nd);
+        const int64_t t = place((int64_t)ctx + 1 + j);
+        from[tid] = nd == j || t < 0 ? -1 : f;
+        to[tid] = t;
+      }
+    }
+    __syncthreads();
+    const int end = s_end;
+    if (live) {
+      for (int i0 = 0; i0 < end; i0 += kMove) {
+        uint4 x[kMove];
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+          if (i0 + u < end && from[i0 + u] >= 0) x[u] = cache[from[i0 + u]];
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+          if (i0 + u < end && from[i0 + u] >= 0) cache[to[i0 + u]] = x[u];
+      }
+    }
+    if (end < min(moves - j0, kMoveList)) break;
+    __syncthreads();
+  }
+}
+
+// new lengths in place, once every workgroup of the moves has read them
+__global__ __launch_bounds__(256) void cache_length_kernel(CommitArgs a) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= a.g.batch) return;
+  const int n = a.g.n_nodes ? a.g.n_nodes[b] : a.g.N;
+  const int32_t c = a.g.ctx_len[b];
+  a.ctx_out[b] = n < 0 ? c : clamp_ctx(c) + min(max(a.tau[b], 0), a.B + 1);
+}
+
+hipError_t launch_cache_commit(const CommitArgs& a, hipStream_t s) {
+  const bool alias = a.ctx_out == a.g.ctx_len;
+  const int64_t cols = (int64_t)a.layers * a.g.Hkv * (a.g.D / 8) * 2;
+  hipLaunchKernelGGL(cache_commit_kernel,
+                     dim3((unsigned)((cols + 255) / 256), a.g.batch),
+                     dim3(256), 0, s, a, alias ? 0 : 1);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !alias) return e;
+  hipLaunchKernelGGL(cache_length_kernel, dim3((a.g.batch + 255) / 256),
+                     dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace pct

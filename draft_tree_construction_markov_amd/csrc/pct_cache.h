@@ -1,0 +1,82 @@
+// pct_cache.h -- kernel arguments and launchers of the paged key-value
+// cache: page plan, row writes, tree attention, commit of accepted paths.
+#pragma once
+
+#include "pct_internal.h"
+
+namespace pct {
+
+// profiler kinds after those of ProfKind
+constexpr int PROF_PLAN = 12, PROF_CACHE_WRITE = 13, PROF_ATTEND = 14,
+              PROF_JOIN = 15, PROF_COMMIT = 16;
+
+constexpr int kMaxTokens = 1 << 30;  // positions of a request at most
+
+// Paged cache geometry shared by the kernels.
+struct PageGeom {
+  int batch, N, n_pages, max_pages;
+  int shift;  // log2 of the page size
+  int Hkv, D;
+  const int32_t* table;    // [batch][max_pages]
+  const int32_t* ctx_len;  // [batch]
+  const int32_t* n_nodes;  // [batch] or null (N in every request)
+};
+
+struct PlanArgs {
+  PageGeom g;  // table unused
+  const int32_t* depth;
+  int32_t *table, *held, *ring, *ring_state;
+  int64_t* slot;
+  int32_t *pos, *missing;
+  int4* req;   // [batch] {first taken, first given back, held before, after}
+  int2* ring0; // ring head and count before the call
+};
+hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s);
+
+struct WriteArgs {
+  int64_t rows;
+  int64_t n_slots;
+  int shift, Hkv, D;
+  const uint4 *k, *v;      // 8 elements each
+  int64_t ks, vs;          // row strides in 8-element chunks
+  const int64_t* slot;
+  uint4 *kc, *vc;
+};
+hipError_t launch_cache_write(const WriteArgs& a, hipStream_t s);
+
+struct CommitArgs {
+  PageGeom g;
+  int layers, B;
+  int64_t layer_stride;  // in 8-element chunks
+  const int32_t *tau, *accept;
+  uint4 *kc, *vc;
+  int32_t* ctx_out;
+};
+hipError_t launch_cache_commit(const CommitArgs& a, hipStream_t s);
+
+struct AttendArgs {
+  PageGeom g;
+  int Hq, G;        // query heads, query heads per key-value head
+  int bf16;         // element type: 1 bf16, 0 fp16
+  float scale;
+  const void* q;
+  int64_t qs;       // row stride in elements
+  const void *kc, *vc;
+  const uint64_t* mask;
+  int words;        // 64-bit words of a mask row
+  void* out;
+  float* lse;
+};
+hipError_t launch_tree_attention(const AttendArgs& a, void* ws,
+                                 hipStream_t s);
+size_t tree_attention_workspace(const pct_cache_shape& sh);
+
+// A request's lengths, clamped to what the calls accept.
+__host__ __device__ inline int clamp_ctx(int c) {
+  return c < 0 ? 0 : (c > kMaxTokens ? kMaxTokens : c);
+}
+__host__ __device__ inline int clamp_nodes(int n, int N) {
+  return n < -1 ? -1 : (n > N ? N : n);
+}
+
+}  // namespace pct

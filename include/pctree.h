@@ -50,7 +50,8 @@ typedef enum {
   PCT_ERR_HIP = 4
 } pct_status;
 
-typedef enum { PCT_F32 = 0, PCT_BF16 = 1 } pct_dtype;
+/* PCT_F16 is an element type of key-value caches only. */
+typedef enum { PCT_F32 = 0, PCT_BF16 = 1, PCT_F16 = 2 } pct_dtype;
 
 /* Shape of a parent-conditioned build.
  *  batch   independent requests
@@ -334,6 +335,159 @@ pct_status pct_build_tree_noalloc(const pct_tree_shape* shape /*host*/,
                                   void* stream);
 
 /* ------------------------------------------------------------------------
+ * The target's side of a round ([PCT] "straight draft": the whole tree is
+ * verified in one target forward) on a paged key-value cache.  The calls
+ * below keep the cache's pages, write the tree's keys and values, attend
+ * from the tree's rows and keep the rows that were accepted:
+ *
+ *   pct_build_tree (mask) -> pct_cache_plan -> per layer of the target
+ *   { pct_cache_write, pct_tree_attention } -> pct_verify_accept or
+ *   pct_verify_sample -> pct_cache_commit -> the next round
+ *
+ * Positions of a request: its ctx_len committed tokens, then the root (the
+ * last token the target supplied, not yet in the cache) at position
+ * ctx_len, then node i at position ctx_len + 1 + i.  Rows: row 0 of a
+ * request is its root, row 1 + i its node i, R = N + 1 rows per request, of
+ * which the first n_nodes + 1 are used; n_nodes = -1 marks a padded request
+ * (no row).  N = 0 is plain decoding, one new token per request.  The
+ * values of ctx_len are taken as at least 0 and at most 2^30, those of
+ * n_nodes as at least -1 and at most N.
+ *
+ * Shape of a paged cache and its rows
+ *  batch      requests
+ *  N          drafted nodes per request at most (0 <= N <= 8192)
+ *  n_pages    pages of the cache
+ *  page_size  tokens of a page, a power of two up to 1024
+ *  max_pages  entries of a request's block table row;
+ *             max_pages * page_size <= 2^30
+ *  Hq, Hkv    query heads and key-value heads; query head h reads
+ *             key-value head h / (Hq / Hkv); Hq <= 1024
+ *  D          elements of a head, a multiple of 16 up to 256
+ *  dtype      PCT_BF16 or PCT_F16: queries, cache and outputs
+ * A cache is [n_pages][Hkv][page_size][D], keys and values apart.  The
+ * block table [batch][max_pages] gives the page of each page_size
+ * positions; an entry outside [0, n_pages) stands for no page: its
+ * positions are not written, attended or moved. */
+typedef struct {
+  int32_t batch, N, n_pages, page_size, max_pages, Hq, Hkv, D, dtype;
+} pct_cache_shape;
+
+/* ------------------------------------------------------------------------
+ * pct_cache_plan -- block tables and slots from the requests' lengths.
+ * Every request is given ceil((ctx_len + n_nodes + 1) / page_size) pages
+ * (at most max_pages), so a request of n_nodes = -1 keeps the pages of its
+ * context and one of ctx_len = 0 and n_nodes = -1 gives all of them back.
+ * Free pages are a ring: ring_state = {head, count}, the free pages are
+ * ring[(head + i) % n_pages], i < count.  Pages that are needed come from
+ * the head, request by request in order; from the first request that the
+ * free pages of before the call do not satisfy, no request gets more.  Pages
+ * past a request's need go to the tail, in the order of requests and
+ * positions (they are handed out from the next call on).
+ *
+ *  ctx_len [batch], n_nodes [batch] (NULL = N in every request)
+ *  depth   [batch][N] depth of each node (as the builds write it; needed
+ *          with pos unless N = 0)
+ *  block_table [batch][max_pages] in/out; entries past a request's pages
+ *          that held one become -1, others there are not touched
+ *  n_held  [batch] in/out: pages held (0 at first)
+ *  ring    [n_pages] in/out, ring_state [2] in/out
+ *  slot    [batch][R] out: page * page_size + offset of each used row; -1
+ *          for unused rows and for rows whose position has no page
+ *  pos     [batch][R] out, optional: the row's place in its sequence,
+ *          ctx_len + its depth (the root's is 0), -1 for unused rows
+ *  missing [batch] out: pages needed and not held
+ *  workspace  pct_cache_plan_workspace(batch) bytes
+ * Only batch, N, n_pages, page_size and max_pages of the shape are read.
+ * Precondition (not checked): ring and block_table hold every page once.
+ * Errors: PCT_ERR_INVALID_ARG for a size outside its range or null required
+ * pointers; PCT_ERR_UNSUPPORTED for batch > 65535; PCT_ERR_WORKSPACE. */
+size_t pct_cache_plan_workspace(int32_t batch);
+pct_status pct_cache_plan(const pct_cache_shape* shape /*host*/,
+                          const int32_t* ctx_len, const int32_t* n_nodes,
+                          const int32_t* depth, int32_t* block_table,
+                          int32_t* n_held, int32_t* ring,
+                          int32_t* ring_state, int64_t* slot, int32_t* pos,
+                          int32_t* missing, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pct_cache_write -- a layer's keys and values of the round's rows into
+ * their slots.
+ *  k, v    [batch * R] rows of [Hkv][D], k_row_stride and v_row_stride
+ *          elements from row to row (views of a joint projection)
+ *  slot    [batch * R]; a slot outside [0, n_pages * page_size) is left
+ *          out.  The slots of one call are distinct.
+ *  k_cache, v_cache  [n_pages][Hkv][page_size][D]
+ * Only batch, N, n_pages, page_size, Hkv, D and dtype of the shape are read.
+ * Errors: PCT_ERR_INVALID_ARG for sizes, null pointers, strides below
+ * Hkv * D or not a multiple of 8, pointers that are not 16-byte aligned. */
+pct_status pct_cache_write(const pct_cache_shape* shape /*host*/,
+                           const void* k, int64_t k_row_stride,
+                           const void* v, int64_t v_row_stride,
+                           const int64_t* slot, void* k_cache, void* v_cache,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * pct_tree_attention -- softmax attention of the round's rows over the
+ * cache.  A row sees the request's context, the root and, of the nodes,
+ * those of its mask row (itself and its ancestors); without a mask node i
+ * sees nodes 0..i (a straight draft, or a piece of a prompt).  With S the
+ * set of seen positions that have a page,
+ *   out = sum_{t in S} softmax_S(scale * q . k_t) v_t,
+ *   lse = ln sum_{t in S} exp(scale * q . k_t);
+ * an empty S gives out = 0 and lse = -inf.  Positions outside a row's S have
+ * no influence on it, whatever the cache holds there (NaN included).
+ * Scores, normalisers and sums are fp32; a probability is rounded to the
+ * cache's type before it meets a value.
+ *
+ *  q       rows of [Hq][D], q_row_stride elements from row to row
+ *  k_cache, v_cache, block_table, ctx_len, n_nodes (NULL = N)  as above
+ *  mask    [batch][N][ceil(N/64)] as pct_tree_mask writes it, or NULL
+ *  out     [batch][R][Hq][D]; lse [batch][R][Hq] optional.  Unused rows
+ *          are left as they were.
+ *  workspace  pct_tree_attention_workspace(shape) bytes
+ * Errors: PCT_ERR_INVALID_ARG for sizes, null pointers, a scale that is not
+ * finite, a stride below Hq * D or not a multiple of 8, pointers that are
+ * not 16-byte aligned; PCT_ERR_UNSUPPORTED for batch > 65535;
+ * PCT_ERR_WORKSPACE. */
+size_t pct_tree_attention_workspace(const pct_cache_shape* shape /*host*/);
+pct_status pct_tree_attention(const pct_cache_shape* shape /*host*/,
+                              float scale, const void* q,
+                              int64_t q_row_stride, const void* k_cache,
+                              const void* v_cache,
+                              const int32_t* block_table,
+                              const int32_t* ctx_len, const int32_t* n_nodes,
+                              const uint64_t* mask, void* out, float* lse,
+                              void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * pct_cache_commit -- after the acceptance walk: the accepted path's keys
+ * and values move, in every layer, to the positions behind the root, and
+ * the context grows by the root and the accepted nodes: node accept_node[j]
+ * moves to position ctx_len + 1 + j, j < tau - 1, and ctx_out = ctx_len +
+ * tau.  A padded request keeps its length and its cache.
+ *  layers, layer_stride  caches of `layers` layers, layer_stride elements
+ *          apart (at least n_pages * Hkv * page_size * D)
+ *  B       entries of accept_node per request
+ *  tau [batch], accept_node [batch][B]  as pct_verify_accept writes them
+ *          (nodes in ascending order); the first entry outside
+ *          [0, n_nodes) ends the moves
+ *  ctx_len [batch]; ctx_out [batch], which may be ctx_len itself
+ * Needs no workspace.
+ * Errors: PCT_ERR_INVALID_ARG for sizes, null pointers, caches that are not
+ * 16-byte aligned, a layer_stride that is too short or not a multiple of 8,
+ * a ctx_out that overlaps ctx_len without being it; PCT_ERR_UNSUPPORTED for
+ * batch > 65535. */
+pct_status pct_cache_commit(const pct_cache_shape* shape /*host*/,
+                            int32_t layers, int64_t layer_stride, int32_t B,
+                            const int32_t* tau, const int32_t* accept_node,
+                            const int32_t* n_nodes,
+                            const int32_t* block_table,
+                            const int32_t* ctx_len, void* k_cache,
+                            void* v_cache, int32_t* ctx_out, void* stream);
+
+/* ------------------------------------------------------------------------
  * Profiling (not from the pages; for measuring kernels against the
  * hardware roofline).  When enabled, every kernel launch of the calls above
  * is bracketed by two HIP events recorded on its stream, tagged with a kind
@@ -342,7 +496,8 @@ pct_status pct_build_tree_noalloc(const pct_tree_shape* shape /*host*/,
  * 3 mask, 4 acceptance walk, 5 seed pre-pass (units = rows), 6 depth-1
  * init, 7 adaptive row statistics (units = rows), 8 adaptive best-first +
  * stop, 9 standalone per-parent results, 10 throughput stop / curve scan,
- * 11 sampled target tokens.
+ * 11 sampled target tokens, 12 cache plan, 13 cache write, 14 tree
+ * attention (units = rows), 15 its join, 16 cache commit.
  *  pct_profile_enable  turns recording on or off (the event pool, 8192
  *                      launches, is created on the first enable)
  *  pct_profile_reset   forgets recorded launches
