@@ -17,7 +17,9 @@ SOURCES = ["api.hip", "k_markov.hip",
            "k_markov_r4d.hip", "k_markov_r8s.hip", "k_markov_r8d.hip",
            "k_markov_r16s.hip", "k_markov_r16d.hip", "k_select.hip",
            "k_verify.hip", "k_adaptive.hip", "profile.hip", "noalloc.hip",
-           "api_cache.hip", "k_cache.hip", "k_attend.hip"]
+           "api_cache.hip", "k_cache.hip", "k_attend.hip", "k_attend_d64.hip",
+           "k_attend_d96.hip", "k_attend_d128.hip", "k_attend_d192.hip",
+           "k_attend_d256.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

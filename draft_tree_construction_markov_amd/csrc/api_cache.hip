@@ -211,7 +211,9 @@ pct_status pct_tree_attention(const pct_cache_shape* shape, float scale,
   a.Hq = shape->Hq;
   a.G = shape->Hq / shape->Hkv;
   a.bf16 = shape->dtype == PCT_BF16;
-  a.scale = scale;
+  a.c = scale == 0.f ? 1.f : fabsf(scale) * 1.44269504f;
+  a.qand = scale == 0.f ? 0u : ~0u;
+  a.qxor = scale < 0.f ? 0x80008000u : 0u;
   a.q = q;
   a.qs = q_row_stride;
   a.kc = k_cache;

@@ -1,0 +1,9 @@
+// k_attend_d96.hip -- tree attention for heads padded to 96 elements.
+#include "k_attend_impl.h"
+
+namespace pct {
+hipError_t launch_attend_d96(const AttendArgs& a, const AttendPlan& p,
+                           const AttendWs& ws, hipStream_t s) {
+  return launch_attend_dp<96>(a, p, ws, s);
+}
+}  // namespace pct

@@ -58,7 +58,8 @@ struct AttendArgs {
   PageGeom g;
   int Hq, G;        // query heads, query heads per key-value head
   int bf16;         // element type: 1 bf16, 0 fp16
-  float scale;
+  float c;          // |scale| * log2(e); 1 for a scale of zero
+  uint32_t qand, qxor;  // bits that carry the scale's sign into two elements
   const void* q;
   int64_t qs;       // row stride in elements
   const void *kc, *vc;
@@ -67,6 +68,29 @@ struct AttendArgs {
   void* out;
   float* lse;
 };
+// Tile of a call: NT 16-row blocks per wave, RG waves per key tile, mt rows
+// per workgroup, n_wg runs, heads padded to dp elements.
+struct AttendPlan {
+  int dp, nt, rg, mt, n_wg;
+};
+// Per run two row tiles of sums that other runs continue: slot 0 of a tile
+// that an earlier run began, slot 1 of one that this run began and did not
+// end; meta {request, head, row tile, last run} of the latter, w < 0: none.
+struct AttendWs {
+  float* o;    // [2 n_wg][mt][dp]
+  float2* ml;  // [2 n_wg][mt] {m, sum}
+  int4* meta;  // [n_wg]
+};
+hipError_t launch_attend_d64(const AttendArgs&, const AttendPlan&,
+                             const AttendWs&, hipStream_t);
+hipError_t launch_attend_d96(const AttendArgs&, const AttendPlan&,
+                             const AttendWs&, hipStream_t);
+hipError_t launch_attend_d128(const AttendArgs&, const AttendPlan&,
+                              const AttendWs&, hipStream_t);
+hipError_t launch_attend_d192(const AttendArgs&, const AttendPlan&,
+                              const AttendWs&, hipStream_t);
+hipError_t launch_attend_d256(const AttendArgs&, const AttendPlan&,
+                              const AttendWs&, hipStream_t);
 hipError_t launch_tree_attention(const AttendArgs& a, void* ws,
                                  hipStream_t s);
 size_t tree_attention_workspace(const pct_cache_shape& sh);
