@@ -22,9 +22,9 @@ AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   p.dp = padded(D);
   // the smallest row tile that holds a request's rows of one head
   const int64_t M = (int64_t)(N + 1) * (Hq / Hkv);
-  p.nt = M <= 16 ? 1 : 2;
-  p.rg = M <= 32 ? 1 : M <= 64 ? 2 : 4;
-  p.mt = 16 * p.nt * p.rg;
+  p.shared = M > 32;
+  p.nt = M <= 16 || (p.shared && M <= 64) ? 1 : 2;
+  p.mt = 16 * p.nt * (p.shared ? 4 : 1);
   p.n_wg = kCus * (p.dp <= 128 ? 2 : 1);
   return p;
 }

@@ -68,10 +68,11 @@ struct AttendArgs {
   void* out;
   float* lse;
 };
-// Tile of a call: NT 16-row blocks per wave, RG waves per key tile, mt rows
-// per workgroup, n_wg runs, heads padded to dp elements.
+// Tile of a call: heads padded to dp elements, nt 16-row blocks per wave, the
+// waves share their keys (and hold different rows) or not, mt rows per
+// workgroup, n_wg runs.
 struct AttendPlan {
-  int dp, nt, rg, mt, n_wg;
+  int dp, nt, shared, mt, n_wg;
 };
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
