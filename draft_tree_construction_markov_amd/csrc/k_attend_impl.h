@@ -102,6 +102,13 @@ __device__ __forceinline__ float row_sum(float x) {
   return row_reduce(x, [](float p, float q) { return p + q; });
 }
 
+// x as a value that the compiler cannot trace: what is derived from it inside
+// a loop is computed there instead of held in registers across the loop.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // the lowest n bits (n clamped to [0, 64])
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0 : (n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1);
@@ -281,19 +288,20 @@ struct AttendState {
   }
 };
 
-// Probabilities of a tile of scores, rounded to the type of the values they
-// meet, as B operands; raises m where a score asks for it.
+// Probabilities of the scores of 32 keys, rounded to the type of the values
+// they meet, as B operands; raises m where a score asks for it.
 template <class C>
-__device__ __forceinline__ void probabilities(
-    float c, const f32x4 (&s)[C::NT][C::KT16], AttendState<C>& st,
-    s16x8 (&pf)[C::NT][C::KT16 / 2]) {
+__device__ __forceinline__ void probabilities(float c,
+                                              const f32x4 (&s)[C::NT][2],
+                                              AttendState<C>& st,
+                                              s16x8 (&pf)[C::NT]) {
   bool up = false;
   float tm[C::NT];
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
     tm[nt] = s[nt][0][0];
 #pragma unroll
-    for (int x = 0; x < C::KT16; ++x)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) tm[nt] = fmaxf(tm[nt], s[nt][x][e]);
     tm[nt] *= c;
@@ -314,30 +322,45 @@ __device__ __forceinline__ void probabilities(
   }
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
+    f32x8 p;
 #pragma unroll
-    for (int y = 0; y < C::KT16 / 2; ++y) {
-      f32x8 p;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(
-            __builtin_fmaf(s[nt][2 * y + e / 4][e & 3], c, -st.ms[nt]));
-        st.l[nt] += p[e];
-      }
-      pf[nt][y] = round8<C::BF16>(p);
-    }
+    for (int e = 0; e < 8; ++e)
+      p[e] = __builtin_amdgcn_exp2f(
+          __builtin_fmaf(s[nt][e / 4][e & 3], c, -st.ms[nt]));
+    st.l[nt] += ((p[0] + p[1]) + (p[2] + p[3])) +
+                ((p[4] + p[5]) + (p[6] + p[7]));
+    pf[nt] = round8<C::BF16>(p);
   }
 }
 
-// Adds the values of the given keys of a tile that are not finite to the
-// rows that see them (the tile holds 0 in their place).
+// Leaves the scores of 32 keys that a row sees (bits of `see`, one word per
+// 16-row block) and -inf in place of the others.
+template <class C>
+__device__ __forceinline__ void mask_scores(const uint32_t (&see)[C::NT],
+                                            f32x4 (&s)[C::NT][2]) {
+  const int quad = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int nt = 0; nt < C::NT; ++nt) {
+    const uint32_t w = see[nt] >> (4 * quad);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!((w >> (16 * x + e)) & 1)) s[nt][x][e] = neg_inf();
+  }
+}
+
+// Adds the values of the given keys of the 32 from t0 on that are not finite
+// to the rows that see them (the tile holds 0 in their place).
 template <class C>
 __device__ __forceinline__ void add_odd_values(
-    const AttendArgs& a, const int32_t* table, int h, int t0, uint64_t keys,
-    const f32x4 (&s)[C::NT][C::KT16], AttendState<C>& st) {
+    const AttendArgs& a, const int32_t* table, int h, int t0, uint32_t keys,
+    const f32x4 (&s)[C::NT][2], AttendState<C>& st) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const PageGeom& g = a.g;
+  const int D = opaque(g.D);
   while (keys) {
-    const int key = __builtin_ctzll(keys);
+    const int key = __builtin_ctz(keys);
     keys &= keys - 1;
     const int t = t0 + key;
     const int p = table[t >> g.shift];
@@ -349,7 +372,7 @@ __device__ __forceinline__ void add_odd_values(
     for (int nt = 0; nt < C::NT; ++nt) {
       float sk = 0.f;
 #pragma unroll
-      for (int x = 0; x < C::KT16; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (key >> 4 == x && (key & 3) == e) sk = s[nt][x][e];
@@ -358,7 +381,7 @@ __device__ __forceinline__ void add_odd_values(
           __builtin_amdgcn_exp2f(__builtin_fmaf(sk, a.c, -st.ms[nt]));
 #pragma unroll
       for (int d = 0; d < C::DT; ++d) {
-        if (16 * d >= g.D) continue;
+        if (16 * d >= D) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float x = elem<C::BF16>(v[16 * d + 4 * quad + e]);

@@ -16,7 +16,7 @@ struct RowsCfg {
   static constexpr int NT = NT_;  // 16-row blocks
   static constexpr bool BF16 = BF16_;
   static constexpr int KB = 32;  // keys of a wave's tile
-  static constexpr int KT16 = KB / 16, DT = DP / 16, KSTEP = DP / 32;
+  static constexpr int DT = DP / 16, KSTEP = DP / 32;
   static constexpr int CH = DP / 8;  // 16-byte pieces of a row
   static constexpr int KS = 4 * KB;
   static constexpr int MT = 16 * NT;
@@ -38,7 +38,7 @@ template <class C>
 __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     AttendArgs a, AttendWs ws) {
   constexpr int NT = C::NT, KB = C::KB, CH = C::CH, NL = C::NL;
-  constexpr int KT16 = C::KT16, DT = C::DT, KSTEP = C::KSTEP;
+  constexpr int DT = C::DT, KSTEP = C::KSTEP;
   __shared__ __align__(16) uint4 lds[C::LDS / 16];
   __shared__ float dump_m[4][C::MT], dump_l[4][C::MT];
 
@@ -152,9 +152,9 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
       __builtin_amdgcn_wave_barrier();
 
       // ---- scores
-      f32x4 s[NT][KT16];
+      f32x4 s[NT][2];
 #pragma unroll
-      for (int x = 0; x < KT16; ++x) {
+      for (int x = 0; x < 2; ++x) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -166,47 +166,35 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
             s[nt][x] = mfma16<C::BF16>(kf, qf[nt][z], s[nt][x]);
         }
       }
-
-      // ---- mask of a tile with nodes, with missing pages or past the end
+      // a tile with nodes, with missing pages or past the end
       if (tail || dead_keys != 0) {
         const uint64_t all = low_bits(L - t0) & ~dead_keys;
+        uint32_t see[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint64_t see =
-              (seen_keys(a, b, irow[nt], rq.n, ctx, t0) & all) >> (4 * quad);
-#pragma unroll
-          for (int x = 0; x < KT16; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!((see >> (16 * x + e)) & 1)) s[nt][x][e] = neg_inf();
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          see[nt] = (uint32_t)(seen_keys(a, b, irow[nt], rq.n, ctx, t0) & all);
+        mask_scores<C>(see, s);
       }
-
-      s16x8 pf[NT][KT16 / 2];
+      s16x8 pf[NT];
       probabilities<C>(a.c, s, st, pf);
 
       // ---- O^T += V^T P^T
 #pragma unroll
-      for (int y = 0; y < KT16 / 2; ++y) {
+      for (int d = 0; d < DT; ++d) {
+        const uint16_t* vb = reinterpret_cast<const uint16_t*>(vt) +
+                             (4 * quad + (col >> 2)) * (8 * C::VROW) + 16 * d +
+                             4 * (col & 3);
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4)(const_cast<uint16_t*>(vb)));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4)(const_cast<uint16_t*>(vb + 16 * 8 * C::VROW)));
+        const s16x8 vf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6,
+                                                 7);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const uint16_t* vb = reinterpret_cast<const uint16_t*>(vt) +
-                               (32 * y + 4 * quad + (col >> 2)) *
-                                   (8 * C::VROW) +
-                               16 * d + 4 * (col & 3);
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4)(const_cast<uint16_t*>(vb)));
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4)(const_cast<uint16_t*>(vb + 16 * 8 * C::VROW)));
-          const s16x8 vf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5,
-                                                   6, 7);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            st.o[nt][d] = mfma16<C::BF16>(vf, pf[nt][y], st.o[nt][d]);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          st.o[nt][d] = mfma16<C::BF16>(vf, pf[nt], st.o[nt][d]);
       }
-
-      add_odd_values<C>(a, table, h, t0, odd_keys, s, st);
+      add_odd_values<C>(a, table, h, t0, (uint32_t)odd_keys, s, st);
     }
 
     // ---- sums to LDS, joined over the waves

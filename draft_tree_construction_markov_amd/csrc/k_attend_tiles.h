@@ -9,7 +9,7 @@
 // LDS layout: rows of SL 16-byte slots without padding (direct loads write
 // 64 consecutive slots per wave instruction), swizzled by the choice of the
 // piece that a lane loads: slot s of key r holds piece s ^ fK(r) of K, and
-// s ^ 2 fV(r) of V, so that the 16 keys of an operand read, and the 8 keys of
+// s ^ fV(r) of V, so that the 16 keys of an operand read, and the 8 keys of
 // half a transposing read, fall on all banks.  Slots past the head size are
 // never loaded and stay zero.
 #pragma once
@@ -18,7 +18,6 @@
 namespace pct {
 
 typedef __attribute__((address_space(3))) void* lds_any;
-typedef const __attribute__((address_space(1))) void* gbl_any;
 
 template <int DP_, int NT_, bool BF16_>
 struct TilesCfg {
@@ -27,7 +26,7 @@ struct TilesCfg {
   static constexpr bool BF16 = BF16_;
   static constexpr int SL = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;
   static constexpr int KB = DP <= 128 ? 64 : 32;  // keys of a tile
-  static constexpr int KT16 = KB / 16, DT = DP / 16, KSTEP = DP / 32;
+  static constexpr int DT = DP / 16, KSTEP = DP / 32;
   static constexpr int KS = KB;
   static constexpr int MT = 64 * NT;
   static constexpr int RPI = 64 / SL;       // rows per direct load
@@ -35,13 +34,31 @@ struct TilesCfg {
   static constexpr int GPS = KB / 8;        // 8-key groups of a tile
   static constexpr int TPV = 64 / GPS;      // tiles whose pages fit a wave
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
+  static __device__ __forceinline__ int swizzle_k(int r) {
+    return SL == 8 ? (r >> 1) & 7 : r & 15;
+  }
+  static __device__ __forceinline__ int swizzle_v(int r) {
+    return 2 * (SL == 8 ? (r >> 1) & 3 : r & 7);
+  }
 };
+
+// 16 bytes per lane from base + off straight to LDS slots to[lane]; base,
+// bytes and to are the same in every lane, off + 16 past `bytes` reads
+// nothing.
+__device__ __forceinline__ void load_to_lds(const uint4* base, int bytes,
+                                            int off, uint4* to) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the buffer type exists there only
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint4*>(base),
+                                                   0, bytes, 0x00027000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_any)to, 16, off, 0, 0, 0);
+#endif
+}
 
 template <class C>
 __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     AttendArgs a, AttendWs ws) {
   constexpr int NT = C::NT, KB = C::KB, SL = C::SL, NI = C::NI;
-  constexpr int KT16 = C::KT16, DT = C::DT, KSTEP = C::KSTEP;
+  constexpr int DT = C::DT, KSTEP = C::KSTEP;
   __shared__ __align__(16) uint4 k_a[KB * SL];
   __shared__ __align__(16) uint4 v_a[KB * SL];
   __shared__ __align__(16) uint4 k_b[KB * SL];
@@ -69,26 +86,19 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
       k_a[i] = v_a[i] = k_b[i] = v_b[i] = zero;
   }
 
-  // direct loads: this lane's row within its 8-key group and its pieces
-  const int row0 = wave * (KB / 4) + lane / SL;  // row of load 0 in the tile
-  int koff[NI], voff[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = row0 + i * C::RPI, s = lane % SL;
-    const int fk = SL == 8 ? (r >> 1) & 7 : r & 15;
-    const int fv = SL == 8 ? (r >> 1) & 3 : r & 7;
-    const int kp = s ^ fk, vp = s ^ (2 * fv);
-    koff[i] = kp < chd ? (r & 7) * chd + kp : -1;
-    voff[i] = vp < chd ? (r & 7) * chd + vp : -1;
-  }
-  // operand reads: slots of K per 32 elements, bytes of V per 16
-  const int fk = SL == 8 ? (col >> 1) & 7 : col;
+  // direct loads: this lane's row of load 0 and its pieces there.  Load i
+  // reads rows i RPI further; the bits of a row and of i RPI are distinct, so
+  // its swizzle differs by that of i RPI.
+  const int row0 = wave * (KB / 4) + lane / SL;
+  const int kp0 = (lane % SL) ^ C::swizzle_k(row0);
+  const int vp0 = (lane % SL) ^ C::swizzle_v(row0);
+  const int row_bytes = chd * 16, group_bytes = 8 * row_bytes;
+
+  // operand reads: bytes of K for the first 32 elements, of V for the first
+  // 16; later ones differ in bits of the swizzled slot only
+  const int kx = (col * SL + (quad ^ C::swizzle_k(col))) * 16;
   const int vkey = 4 * quad + (col >> 2);
-  const int fv = SL == 8 ? (vkey >> 1) & 3 : vkey & 7;
-  int kx[KSTEP];
-#pragma unroll
-  for (int z = 0; z < KSTEP; ++z) kx[z] = col * SL + ((4 * z + quad) ^ fk);
-  const int vx = vkey * SL * 16 + fv * 32 + (col & 3) * 8;
+  const int vx = (vkey * SL + C::swizzle_v(vkey)) * 16 + (col & 3) * 8;
 
   while (u < run.end) {
     while (u >= b_off + rq.units) {
@@ -123,26 +133,19 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     // issues the loads of tile k; returns whether a group has no page
     auto issue = [&](int k, uint4* kd, uint4* vd)
         __attribute__((always_inline)) -> bool {
-      const uint4* kc = static_cast<const uint4*>(a.kc);
-      const uint4* vc = static_cast<const uint4*>(a.vc);
       if (small) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int r = row0 + i * C::RPI;
+        // a page of its own for every row: through registers
+#pragma unroll 1
+        for (int x = tid; x < KB * SL; x += 256) {
+          const int r = x / SL, sl = x % SL;
           const int t = min(k * KB + r, L - 1);
           int p = table[t >> g.shift];
           p = (unsigned)p < (unsigned)g.n_pages ? p : 0;
           const int64_t at =
-              ((((int64_t)p * g.Hkv + h) << g.shift) + (t & page_mask) -
-               (r & 7)) * chd;
-          uint4* kl = kd + (wave * NI + i) * 64;
-          uint4* vl = vd + (wave * NI + i) * 64;
-          if (koff[i] >= 0)
-            __builtin_amdgcn_global_load_lds((gbl_any)(kc + (at + koff[i])),
-                                             (lds_any)kl, 16, 0, 0);
-          if (voff[i] >= 0)
-            __builtin_amdgcn_global_load_lds((gbl_any)(vc + (at + voff[i])),
-                                             (lds_any)vl, 16, 0, 0);
+              ((((int64_t)p * g.Hkv + h) << g.shift) + (t & page_mask)) * chd;
+          const int kp = sl ^ C::swizzle_k(r), vp = sl ^ C::swizzle_v(r);
+          if (kp < chd) kd[x] = static_cast<const uint4*>(a.kc)[at + kp];
+          if (vp < chd) vd[x] = static_cast<const uint4*>(a.vc)[at + vp];
         }
         return true;
       }
@@ -153,6 +156,15 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
         pv_next = group_pages(kv + C::TPV);
       }
       const int first = (k - kv) * C::GPS;
+      const int lr = opaque((lane / SL) * row_bytes);
+      const int kp = opaque(kp0), vp = opaque(vp0);
+      // bytes of a piece from its 8-key group on; a slot past the head size
+      // gets an offset past the group, which the bound of the buffer
+      // descriptor keeps from being read
+      auto bytes = [&](int piece, int i) {
+        const int off = lr + (i * C::RPI & 7) * row_bytes + piece * 16;
+        return piece < chd ? off : group_bytes;
+      };
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int grp = (wave * (KB / 4) + i * C::RPI) >> 3;
@@ -160,105 +172,134 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
         p = (unsigned)p < (unsigned)g.n_pages ? p : 0;
         const int64_t at = ((((int64_t)p * g.Hkv + h) << g.shift) +
                             ((k * KB + 8 * grp) & page_mask)) * chd;
-        uint4* kl = kd + (wave * NI + i) * 64;
-        uint4* vl = vd + (wave * NI + i) * 64;
-        if (koff[i] >= 0)
-          __builtin_amdgcn_global_load_lds((gbl_any)(kc + at + koff[i]),
-                                           (lds_any)kl, 16, 0, 0);
-        if (voff[i] >= 0)
-          __builtin_amdgcn_global_load_lds((gbl_any)(vc + at + voff[i]),
-                                           (lds_any)vl, 16, 0, 0);
+        load_to_lds(static_cast<const uint4*>(a.kc) + at, group_bytes,
+                    bytes(kp ^ C::swizzle_k(i * C::RPI), i),
+                    kd + (wave * NI + i) * 64);
+        load_to_lds(static_cast<const uint4*>(a.vc) + at, group_bytes,
+                    bytes(vp ^ C::swizzle_v(i * C::RPI), i),
+                    vd + (wave * NI + i) * 64);
       }
       return ((no_page >> first) & low_bits(C::GPS)) != 0;
     };
 
-    // one tile: wait for its loads, start the next tile's, multiply
-    auto tile = [&](int k, const uint4* kt, uint4* vt, uint4* kn, uint4* vn,
-                    bool& holes) __attribute__((always_inline)) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      const int t0 = k * KB;
-      const bool edge = holes || t0 + KB > ctx + 1;
-      if (k + 1 < k1) holes = issue(k + 1, kn, vn);
-
-      uint64_t odd_keys = 0, all = 0;
-      if (edge) {
-        // keys that exist and have a page
-        const int t = t0 + lane;
-        bool on = lane < KB && t < L;
-        if (on) on = (unsigned)table[t >> g.shift] < (unsigned)g.n_pages;
-        all = __ballot(on);
-        // Values of other keys become 0.  A node's value that is not finite
-        // must not meet the probability 0 of a row that does not see it:
-        // it is taken out here and added to the rows that see it below.
-        for (int x = tid; x < KB * SL; x += 256) {
-          const int r = x / SL;
-          const bool live = (all >> r) & 1;
-          uint4 v = vt[x];
-          if (!live) vt[x] = make_uint4(0, 0, 0, 0);
-          const bool odd = live && t0 + r > ctx && drop_odd<C::BF16>(v);
-          if (odd) vt[x] = v;
-          odd_keys |= key_bits(odd, r);
-        }
-        if (lane == 0) odd_s[wave] = odd_keys;
-        __syncthreads();
-        odd_keys = odd_s[0] | odd_s[1] | odd_s[2] | odd_s[3];
-      }
-
-      f32x4 s[NT][KT16];
+    // S^T of keys 32 y .. of the tile in kt
+    auto scores = [&](const uint4* kt, int y, f32x4(&s)[NT][2])
+        __attribute__((always_inline)) {
+      const char* kb =
+          reinterpret_cast<const char*>(kt) + 32 * y * SL * 16;
+      const int kx0 = opaque(kx);
 #pragma unroll
-      for (int x = 0; x < KT16; ++x) {
+      for (int x = 0; x < 2; ++x) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int z = 0; z < KSTEP; ++z) {
-          const s16x8 kf = __builtin_bit_cast(s16x8, kt[16 * SL * x + kx[z]]);
+          const s16x8 kf = *reinterpret_cast<const s16x8*>(
+              kb + 16 * SL * 16 * x + (kx0 ^ (64 * z)));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             s[nt][x] = mfma16<C::BF16>(kf, qf[nt][z], s[nt][x]);
         }
       }
-      if (edge) {
+    };
+    // O^T += V^T P^T for keys 32 y .. of the tile in vt
+    auto values = [&](const uint4* vt, int y, const s16x8(&pf)[NT])
+        __attribute__((always_inline)) {
+      const int vx0 = opaque(vx);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint64_t see =
-              (seen_keys(a, b, irow[nt], rq.n, ctx, t0) & all) >> (4 * quad);
+      for (int d = 0; d < DT; ++d) {
+        char* vb = const_cast<char*>(reinterpret_cast<const char*>(vt)) +
+                   (vx0 ^ (32 * d)) + 32 * y * SL * 16;
+        const s16x4 lo =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)vb);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4)(vb + 16 * SL * 16));
+        const s16x8 vf =
+            __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-          for (int x = 0; x < KT16; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!((see >> (16 * x + e)) & 1)) s[nt][x][e] = neg_inf();
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          st.o[nt][d] = mfma16<C::BF16>(vf, pf[nt], st.o[nt][d]);
       }
-      s16x8 pf[NT][KT16 / 2];
-      probabilities<C>(a.c, s, st, pf);
+    };
+    // every wave's loads of the current tile have arrived, and every wave is
+    // done with the other buffer
+    auto arrived = [&]() __attribute__((always_inline)) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+    };
+
+    bool holes = false;  // the next tile has keys without a page
+    // a tile of context whose keys all have pages
+    auto tile = [&](int k, const uint4* kt, const uint4* vt, uint4* kn,
+                    uint4* vn) __attribute__((always_inline)) {
+      arrived();
+      if (k + 1 < k1) holes = issue(k + 1, kn, vn);
 #pragma unroll
-      for (int y = 0; y < KT16 / 2; ++y) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          char* vb = reinterpret_cast<char*>(vt) + (vx ^ (32 * d)) +
-                     32 * y * SL * 16;
-          const s16x4 lo =
-              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)vb);
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4)(vb + 16 * SL * 16));
-          const s16x8 vf =
-              __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            st.o[nt][d] = mfma16<C::BF16>(vf, pf[nt][y], st.o[nt][d]);
-        }
+      for (int y = 0; y < KB / 32; ++y) {
+        f32x4 s[NT][2];
+        s16x8 pf[NT];
+        scores(kt, y, s);
+        probabilities<C>(a.c, s, st, pf);
+        values(vt, y, pf);
       }
-      if (edge) add_odd_values<C>(a, table, h, t0, odd_keys, s, st);
+    };
+    // any other tile
+    auto edge_tile = [&](int k, const uint4* kt, uint4* vt, uint4* kn,
+                         uint4* vn) __attribute__((always_inline)) {
+      arrived();
+      if (k + 1 < k1) holes = issue(k + 1, kn, vn);
+      // keys that exist and have a page
+      const int t0 = k * KB;
+      bool on = lane < KB && t0 + lane < L;
+      if (on)
+        on = (unsigned)table[(t0 + lane) >> g.shift] < (unsigned)g.n_pages;
+      const uint64_t all = __ballot(on);
+      // Values of other keys become 0.  A node's value that is not finite
+      // must not meet the probability 0 of a row that does not see it: it is
+      // taken out here and added to the rows that see it below.
+      uint64_t odd_keys = 0;
+#pragma unroll 1
+      for (int x = tid; x < KB * SL; x += 256) {
+        const int r = x / SL;
+        const bool live = (all >> r) & 1;
+        uint4 v = vt[x];
+        if (!live) vt[x] = make_uint4(0, 0, 0, 0);
+        const bool odd = live && t0 + r > ctx && drop_odd<C::BF16>(v);
+        if (odd) vt[x] = v;
+        odd_keys |= key_bits(odd, r);
+      }
+      if (lane == 0) odd_s[wave] = odd_keys;
+      __syncthreads();
+      odd_keys = odd_s[0] | odd_s[1] | odd_s[2] | odd_s[3];
+
+#pragma unroll 1
+      for (int y = 0; y < KB / 32; ++y) {
+        f32x4 s[NT][2];
+        s16x8 pf[NT];
+        uint32_t see[NT];
+        scores(kt, y, s);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          see[nt] = (uint32_t)(seen_keys(a, b, irow[nt], rq.n, ctx,
+                                         t0 + 32 * y) & (all >> (32 * y)));
+        mask_scores<C>(see, s);
+        probabilities<C>(a.c, s, st, pf);
+        values(vt, y, pf);
+        add_odd_values<C>(a, table, h, t0 + 32 * y,
+                          (uint32_t)(odd_keys >> (32 * y)), s, st);
+      }
     };
 
     __syncthreads();  // the previous run's last tile has been read
-    bool holes = issue(k0, k_a, v_a);
-    for (int k = k0;;) {
-      tile(k, k_a, v_a, k_b, v_b, holes);
-      if (++k >= k1) break;
-      tile(k, k_b, v_b, k_a, v_a, holes);
-      if (++k >= k1) break;
+    holes = issue(k0, k_a, v_a);
+    for (int k = k0, par = 0; k < k1; ++k, par ^= 1) {
+      if (holes || (k + 1) * KB > ctx + 1)
+        edge_tile(k, par ? k_b : k_a, par ? v_b : v_a, par ? k_a : k_b,
+                  par ? v_a : v_b);
+      else if (par)
+        tile(k, k_b, v_b, k_a, v_a);
+      else
+        tile(k, k_a, v_a, k_b, v_b);
     }
 
     // ---- finished rows, or sums for the join
