@@ -288,20 +288,19 @@ struct AttendState {
   }
 };
 
-// Probabilities of the scores of 32 keys, rounded to the type of the values
-// they meet, as B operands; raises m where a score asks for it.
-template <class C>
-__device__ __forceinline__ void probabilities(float c,
-                                              const f32x4 (&s)[C::NT][2],
-                                              AttendState<C>& st,
-                                              s16x8 (&pf)[C::NT]) {
+// Raises the reference m of a wave's rows where one of the scores of NX
+// 16-key blocks asks for it.
+template <class C, int NX>
+__device__ __forceinline__ void raise_reference(float c,
+                                                const f32x4 (&s)[C::NT][NX],
+                                                AttendState<C>& st) {
   bool up = false;
   float tm[C::NT];
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
     tm[nt] = s[nt][0][0];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < NX; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) tm[nt] = fmaxf(tm[nt], s[nt][x][e]);
     tm[nt] *= c;
@@ -320,13 +319,22 @@ __device__ __forceinline__ void probabilities(float c,
       for (int d = 0; d < C::DT; ++d) st.o[nt][d] *= f;
     }
   }
+}
+
+// Probabilities of 32 keys (the 16-key blocks x0 and x0 + 1 of s), rounded to
+// the type of the values they meet, as B operands.
+template <class C, int NX>
+__device__ __forceinline__ void probabilities(float c,
+                                              const f32x4 (&s)[C::NT][NX],
+                                              int x0, AttendState<C>& st,
+                                              s16x8 (&pf)[C::NT]) {
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
     f32x8 p;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       p[e] = __builtin_amdgcn_exp2f(
-          __builtin_fmaf(s[nt][e / 4][e & 3], c, -st.ms[nt]));
+          __builtin_fmaf(s[nt][x0 + e / 4][e & 3], c, -st.ms[nt]));
     st.l[nt] += ((p[0] + p[1]) + (p[2] + p[3])) +
                 ((p[4] + p[5]) + (p[6] + p[7]));
     pf[nt] = round8<C::BF16>(p);
@@ -393,25 +401,27 @@ __device__ __forceinline__ void add_odd_values(
   }
 }
 
-// Takes the elements of a 16-byte piece that are not finite out of it.
+// Takes the elements of a 16-byte piece that are not finite out of it;
+// returns whether there were any.
 template <bool BF16>
 __device__ __forceinline__ bool drop_odd(uint4& v) {
-  constexpr uint32_t ex = BF16 ? 0x7f80u : 0x7c00u;
+  // without its sign an element that is not finite is at least inf's bits:
+  // adding what is missing to 0x8000 carries into the sign bit
+  constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
+  constexpr uint32_t add = (0x8000u - inf) * 0x10001u;
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool odd = false;
+  const uint32_t any = ((w[0] & 0x7fff7fffu) + add) |
+                       ((w[1] & 0x7fff7fffu) + add) |
+                       ((w[2] & 0x7fff7fffu) + add) |
+                       ((w[3] & 0x7fff7fffu) + add);
+  if (!(any & 0x80008000u)) return false;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if ((w[e] & ex) == ex) {
-      odd = true;
-      w[e] &= 0xffff0000u;
-    }
-    if ((w[e] & (ex << 16)) == (ex << 16)) {
-      odd = true;
-      w[e] &= 0xffffu;
-    }
+    if ((w[e] & inf) == inf) w[e] &= 0xffff0000u;
+    if ((w[e] & (inf << 16)) == (inf << 16)) w[e] &= 0xffffu;
   }
-  if (odd) v = make_uint4(w[0], w[1], w[2], w[3]);
-  return odd;
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  return true;
 }
 
 // bits of the keys (lane values) of the lanes with `on`

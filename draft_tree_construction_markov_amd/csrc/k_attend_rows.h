@@ -176,7 +176,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
         mask_scores<C>(see, s);
       }
       s16x8 pf[NT];
-      probabilities<C>(a.c, s, st, pf);
+      raise_reference<C, 2>(a.c, s, st);
+      probabilities<C, 2>(a.c, s, 0, st, pf);
 
       // ---- O^T += V^T P^T
 #pragma unroll

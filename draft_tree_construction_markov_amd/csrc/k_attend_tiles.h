@@ -27,6 +27,7 @@ struct TilesCfg {
   static constexpr int SL = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;
   static constexpr int KB = DP <= 128 ? 64 : 32;  // keys of a tile
   static constexpr int DT = DP / 16, KSTEP = DP / 32;
+  static constexpr int GD = DT % 4 == 0 ? 4 : 2;  // V operands of a group
   static constexpr int KS = KB;
   static constexpr int MT = 64 * NT;
   static constexpr int RPI = 64 / SL;       // rows per direct load
@@ -58,7 +59,7 @@ template <class C>
 __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     AttendArgs a, AttendWs ws) {
   constexpr int NT = C::NT, KB = C::KB, SL = C::SL, NI = C::NI;
-  constexpr int DT = C::DT, KSTEP = C::KSTEP;
+  constexpr int DT = C::DT, KSTEP = C::KSTEP, GD = C::GD;
   __shared__ __align__(16) uint4 k_a[KB * SL];
   __shared__ __align__(16) uint4 v_a[KB * SL];
   __shared__ __align__(16) uint4 k_b[KB * SL];
@@ -182,44 +183,46 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
       return ((no_page >> first) & low_bits(C::GPS)) != 0;
     };
 
-    // S^T of keys 32 y .. of the tile in kt
-    auto scores = [&](const uint4* kt, int y, f32x4(&s)[NT][2])
+    // operands of the 16-key block x of the tile in kt, and their products
+    auto read_k = [&](const uint4* kt, int x, int kx0, s16x8(&kf)[KSTEP])
         __attribute__((always_inline)) {
       const char* kb =
-          reinterpret_cast<const char*>(kt) + 32 * y * SL * 16;
-      const int kx0 = opaque(kx);
+          reinterpret_cast<const char*>(kt) + 16 * x * SL * 16;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int z = 0; z < KSTEP; ++z) {
-          const s16x8 kf = *reinterpret_cast<const s16x8*>(
-              kb + 16 * SL * 16 * x + (kx0 ^ (64 * z)));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            s[nt][x] = mfma16<C::BF16>(kf, qf[nt][z], s[nt][x]);
-        }
-      }
+      for (int z = 0; z < KSTEP; ++z)
+        kf[z] = *reinterpret_cast<const s16x8*>(kb + (kx0 ^ (64 * z)));
     };
-    // O^T += V^T P^T for keys 32 y .. of the tile in vt
-    auto values = [&](const uint4* vt, int y, const s16x8(&pf)[NT])
+    auto scores = [&](const s16x8(&kf)[KSTEP], int nt)
         __attribute__((always_inline)) {
-      const int vx0 = opaque(vx);
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
+      for (int z = 0; z < KSTEP; ++z)
+        s = mfma16<C::BF16>(kf[z], qf[nt][z], s);
+      return s;
+    };
+    // operands of keys 32 y .. and elements 16 GD d0 .. of the tile in vt, and
+    // their products
+    auto read_v = [&](const uint4* vt, int y, int d0, int vx0,
+                      s16x8(&vf)[GD]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int d = 0; d < GD; ++d) {
         char* vb = const_cast<char*>(reinterpret_cast<const char*>(vt)) +
-                   (vx0 ^ (32 * d)) + 32 * y * SL * 16;
+                   (vx0 ^ (32 * (GD * d0 + d))) + 32 * y * SL * 16;
         const s16x4 lo =
             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)vb);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (lds_s16x4)(vb + 16 * SL * 16));
-        const s16x8 vf =
-            __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        vf[d] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+    };
+    auto values = [&](const s16x8(&vf)[GD], int d0, const s16x8(&pf)[NT])
+        __attribute__((always_inline)) {
+#pragma unroll
+      for (int d = 0; d < GD; ++d)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          st.o[nt][d] = mfma16<C::BF16>(vf, pf[nt], st.o[nt][d]);
-      }
+          st.o[nt][GD * d0 + d] =
+              mfma16<C::BF16>(vf[d], pf[nt], st.o[nt][GD * d0 + d]);
     };
     // every wave's loads of the current tile have arrived, and every wave is
     // done with the other buffer
@@ -234,13 +237,33 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
                     uint4* vn) __attribute__((always_inline)) {
       arrived();
       if (k + 1 < k1) holes = issue(k + 1, kn, vn);
+      // Operands are read one group of products ahead; the barriers keep the
+      // compiler from moving a group's reads back to its products.
+      constexpr int NX = KB / 16, NG = DT / GD, NV = KB / 32 * NG;
+      f32x4 s[NT][NX];
+      s16x8 kf[2][KSTEP], vf[2][GD], pf[NT];
+      const int kx0 = opaque(kx), vx0 = opaque(vx);
+      read_k(kt, 0, kx0, kf[0]);
 #pragma unroll
-      for (int y = 0; y < KB / 32; ++y) {
-        f32x4 s[NT][2];
-        s16x8 pf[NT];
-        scores(kt, y, s);
-        probabilities<C>(a.c, s, st, pf);
-        values(vt, y, pf);
+      for (int x = 0; x < NX; ++x) {
+        if (x + 1 < NX)
+          read_k(kt, x + 1, kx0, kf[(x + 1) & 1]);
+        else
+          read_v(vt, 0, 0, vx0, vf[0]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][x] = scores(kf[x & 1], nt);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      raise_reference<C, NX>(a.c, s, st);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (i % NG == 0) probabilities<C, NX>(a.c, s, 2 * (i / NG), st, pf);
+        if (i + 1 < NV)
+          read_v(vt, (i + 1) / NG, (i + 1) % NG, vx0, vf[(i + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        values(vf[i & 1], i % NG, pf);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
     // any other tile
@@ -277,14 +300,28 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
         f32x4 s[NT][2];
         s16x8 pf[NT];
         uint32_t see[NT];
-        scores(kt, y, s);
+        const int kx0 = opaque(kx);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          s16x8 kf[KSTEP];
+          read_k(kt, 2 * y + x, kx0, kf);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][x] = scores(kf, nt);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           see[nt] = (uint32_t)(seen_keys(a, b, irow[nt], rq.n, ctx,
                                          t0 + 32 * y) & (all >> (32 * y)));
         mask_scores<C>(see, s);
-        probabilities<C>(a.c, s, st, pf);
-        values(vt, y, pf);
+        raise_reference<C, 2>(a.c, s, st);
+        probabilities<C, 2>(a.c, s, 0, st, pf);
+        const int vx0 = opaque(vx);
+#pragma unroll
+        for (int i = 0; i < DT / GD; ++i) {
+          s16x8 vf[GD];
+          read_v(vt, y, i, vx0, vf);
+          values(vf, i, pf);
+        }
         add_odd_values<C>(a, table, h, t0 + 32 * y,
                           (uint32_t)(odd_keys >> (32 * y)), s, st);
       }
@@ -292,14 +329,26 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
 
     __syncthreads();  // the previous run's last tile has been read
     holes = issue(k0, k_a, v_a);
+    // Tiles of context go in pairs through the fast path (its loop names the
+    // buffers); an odd one, nodes and holes take the other path.
+    auto clean = [&](int k) {
+      return k < k1 && !holes && (k + 1) * KB <= ctx + 1;
+    };
     for (int k = k0, par = 0; k < k1; ++k, par ^= 1) {
-      if (holes || (k + 1) * KB > ctx + 1)
-        edge_tile(k, par ? k_b : k_a, par ? v_b : v_a, par ? k_a : k_b,
-                  par ? v_a : v_b);
-      else if (par)
-        tile(k, k_b, v_b, k_a, v_a);
-      else
-        tile(k, k_a, v_a, k_b, v_b);
+      if (par == 0) {
+        while (clean(k)) {
+          tile(k, k_a, v_a, k_b, v_b);
+          ++k;
+          par = 1;
+          if (!clean(k)) break;
+          tile(k, k_b, v_b, k_a, v_a);
+          ++k;
+          par = 0;
+        }
+        if (k >= k1) break;
+      }
+      edge_tile(k, par ? k_b : k_a, par ? v_b : v_a, par ? k_a : k_b,
+                par ? v_a : v_b);
     }
 
     // ---- finished rows, or sums for the join
