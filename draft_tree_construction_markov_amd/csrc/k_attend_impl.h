@@ -23,8 +23,8 @@
 // into tiles whose waves share the keys (k_attend_tiles.h, bound by the
 // matrix units and the exponentials).
 //
-// Work is the list of all (request, head, row tile, step of KS keys),
-// cut into equal contiguous runs, one per workgroup, whatever the lengths
+// Work is the list of all (request, head, row tile, step of KS keys), cut
+// into contiguous runs of equal work, one per workgroup, whatever the lengths
 // of the requests (known on the device only).  A row tile whose steps lie in
 // one run is finished there; otherwise each run leaves its unnormalised
 // sums in the workspace and the join kernel adds them up in order of runs,
@@ -114,93 +114,236 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0 : (n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1);
 }
 
-// Steps of one request.
+// Work of one request in units: a step of a row tile counts W units, one of
+// a row tile that fills at most half of it 1 unit (W = 2 where the kernel
+// has a form for such tiles, else 1).
 struct AttendReq {
-  int ctx, n, L;  // context, nodes, positions
-  int M, RT, KT;  // packed rows, row tiles, steps of a row tile
-  int64_t units;  // steps of all heads and row tiles
+  int ctx, n, L;    // context, nodes, positions
+  int M, KT;        // packed rows, steps of a row tile
+  int full, light;  // row tiles that count W units, 1 unit
+  int64_t head;     // units of a head
+  int64_t units;
 };
-template <int MT, int KS>
-__device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b) {
+template <int MT, int KS, int W>
+__device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
+                                                bool uniform = false) {
   const PageGeom& g = a.g;
   AttendReq r;
   r.n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
   r.ctx = clamp_ctx(g.ctx_len[b]);
   r.L = min(r.ctx + r.n + 1, g.max_pages << g.shift);
+  // the same in every lane when b is: held in scalar registers
+  if (uniform) {
+    r.n = __builtin_amdgcn_readfirstlane(r.n);
+    r.ctx = __builtin_amdgcn_readfirstlane(r.ctx);
+    r.L = __builtin_amdgcn_readfirstlane(r.L);
+  }
   r.M = (r.n + 1) * a.G;
-  r.RT = (r.M + MT - 1) / MT;
   r.KT = (r.L + KS - 1) / KS;
-  r.units = (int64_t)g.Hkv * r.RT * r.KT;
+  r.full = (r.M + MT - 1) / MT;
+  r.light = W > 1 && r.M - (r.full - 1) * MT <= MT / 2 ? 1 : 0;
+  r.full -= r.light;
+  r.head = (int64_t)(W * r.full + r.light) * r.KT;
+  r.units = g.Hkv * r.head;
   return r;
 }
 
-// A workgroup's run of steps [u, end) of the `total` steps of all requests,
-// and where it begins: request b, whose steps begin at b_off.
+// How the work is cut into runs, one per workgroup.
+//
+// Lines: the units of all requests in the order (request, head, row tile,
+// step), cut into runs of equal length.  Any batch.
+//
+// Levels: where all requests have the same number of row tiles, level i is
+// row tile i of every head in the order (request, head, step).  All levels
+// are cut at the same places into blocks, and the runs of one block, one per
+// level, are on one XCD: they read the same keys at the same time, so the
+// keys come from its L2 for all levels but the first.  (With lines a run
+// goes through the row tiles of a head one after the other and every one of
+// them reads the keys from memory again: trees of 257 rows on 32 requests
+// 800 us, with levels LEVELS_US us.)  A level of half-filled row tiles has
+// half as many runs of two blocks each.
 struct AttendRun {
-  int run, r_run;
-  int64_t q_run, u, end, b_off;
-  int b;
-  // run w begins at step start(w); run that holds step x
+  int run;  // index of this run; a row tile's runs follow each other
+  int64_t u, end;
+  int b;          // request that holds u; its units begin at b_off
+  int64_t b_off;
+  int level;      // row tile of the run, -1: lines
+  int full, bx, half;  // levels of full runs, blocks and half runs per XCD
+  int64_t q;      // run (block) j begins at unit j q + min(j, r)
+  int r;
+  __device__ __forceinline__ int64_t start(int j) const {
+    return j * q + min(j, r);
+  }
+  // run (block) that holds unit x
+  __device__ __forceinline__ int at(int64_t x) const {
+    const int64_t big = (int64_t)r * (q + 1);
+    return (int)(x < big ? x / (q + 1) : r + (x - big) / q);
+  }
+  // run of this run's level that holds unit x
   __device__ __forceinline__ int owner(int64_t x) const {
-    const int64_t big = (int64_t)r_run * (q_run + 1);
-    return (int)(x < big ? x / (q_run + 1) : r_run + (x - big) / q_run);
+    const int j = at(x);
+    if (level < 0) return j;
+    if (level < full) return level * 8 * bx + j;
+    return full * 8 * bx + j / bx * half + j % bx / 2;
+  }
+  __device__ __forceinline__ int64_t units(const AttendArgs& a,
+                                           const AttendReq& rq) const {
+    return level < 0 ? rq.units
+                     : (rq.M > 0 ? (int64_t)a.g.Hkv * rq.KT : (int64_t)0);
   }
 };
 
+// The steps [k0, k1) of head h and row tile rt that begin in the units
+// [u, end) of a request whose units begin at b_off; s0: the row tile's first
+// unit, w: units of its steps.  A step belongs to the run that holds its
+// first unit.
+struct AttendPiece {
+  int h, rt, k0, k1, w;
+  int64_t s0, next;  // next: the first unit after the piece
+};
+template <int W>
+__device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
+                                                    const AttendRun& run) {
+  AttendPiece p;
+  const int64_t in = run.u - run.b_off;
+  if (run.level >= 0) {
+    p.h = (int)(in / rq.KT);
+    p.rt = run.level;
+    p.w = 1;
+    p.k0 = (int)(in - (int64_t)p.h * rq.KT);
+    p.s0 = run.u - p.k0;
+    p.k1 = (int)min((int64_t)rq.KT, p.k0 + run.end - run.u);
+    p.next = run.u + p.k1 - p.k0;
+    return p;
+  }
+  p.h = (int)(in / rq.head);
+  const int64_t r = in - p.h * rq.head;
+  p.rt = (int)min(r / ((int64_t)W * rq.KT), (int64_t)rq.full);
+  p.w = p.rt < rq.full ? W : 1;
+  const int64_t off = r - (int64_t)W * p.rt * rq.KT;
+  p.s0 = run.u - off;
+  p.k0 = (int)((off + p.w - 1) / p.w);
+  p.k1 = (int)min((int64_t)rq.KT, (off + run.end - run.u + p.w - 1) / p.w);
+  p.next = min(run.end, p.s0 + (int64_t)p.w * rq.KT);
+  return p;
+}
+
 // Fills in the run of this workgroup; false when it has none (its entry of
 // the join is then empty).
-template <int MT, int KS>
+template <int MT, int KS, int W>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
                                                 const AttendWs& ws,
                                                 AttendRun& r) {
-  __shared__ int64_t wsum[4];
+  __shared__ int64_t wsum[4][2];
+  __shared__ int rows[2];  // smallest and largest M of the requests
   __shared__ int64_t seek_off;
   __shared__ int seek_b;
   const PageGeom& g = a.g;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (g.batch + 255) / 256;
-  int64_t mine = 0;
-  for (int b = tid * per; b < min((tid + 1) * per, g.batch); ++b)
-    mine += attend_req<MT, KS>(a, b).units;
-  int64_t incl = mine;
+  if (tid == 0) {
+    rows[0] = 0x7fffffff;
+    rows[1] = 0;
+  }
+  __syncthreads();
+  int64_t mine = 0, mine1 = 0;  // units of lines, of a level
+  for (int b = tid * per; b < min((tid + 1) * per, g.batch); ++b) {
+    const AttendReq q = attend_req<MT, KS, W>(a, b);
+    mine += q.units;
+    if (q.M > 0) {
+      mine1 += (int64_t)g.Hkv * q.KT;
+      atomicMin(&rows[0], q.M);
+      atomicMax(&rows[1], q.M);
+    }
+  }
+  int64_t incl = mine, incl1 = mine1;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     const int64_t x = __shfl_up(incl, d, kWave);
-    if (lane >= d) incl += x;
-  }
-  if (lane == 63) wsum[wave] = incl;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) incl += wsum[w];
-    total += wsum[w];
-  }
-  const int n_run = (int)min((int64_t)gridDim.x, total);
-  // neighbouring runs on one XCD (workgroups go round the 8 XCDs), so that
-  // the row tiles of a head read its keys and values from one L2
-  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
-  const int xbase = xcd * (n_run >> 3) + min(xcd, n_run & 7);
-  const int xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
-  if (at >= xcount) {
-    // runs n_run, ... do not exist
-    if (tid == 0) {
-      int idle = 0;  // idle workgroups of the XCDs before this one
-      for (int x = 0; x < xcd; ++x)
-        idle += (((int)gridDim.x - x + 7) >> 3) -
-                ((n_run >> 3) + (x < (n_run & 7) ? 1 : 0));
-      ws.meta[n_run + idle + at - xcount] = make_int4(0, 0, 0, -1);
+    const int64_t y = __shfl_up(incl1, d, kWave);
+    if (lane >= d) {
+      incl += x;
+      incl1 += y;
     }
+  }
+  if (lane == 63) {
+    wsum[wave][0] = incl;
+    wsum[wave][1] = incl1;
+  }
+  __syncthreads();
+  int64_t total = 0, total1 = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) {
+      incl += wsum[w][0];
+      incl1 += wsum[w][1];
+    }
+    total += wsum[w][0];
+    total1 += wsum[w][1];
+  }
+  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+  const int n_wg = gridDim.x, per_xcd = n_wg >> 3;
+
+  // levels, if they keep at least 4 of 5 workgroups busy
+  r.level = -1;
+  const int RT = (rows[1] + MT - 1) / MT;
+  const int lt = W > 1 && rows[1] - (RT - 1) * MT <= MT / 2 ? 1 : 0;
+  r.full = RT - lt;
+  r.bx = 2 * per_xcd / (2 * r.full + lt + (RT == 0));
+  if (r.full * r.bx + lt * ((r.bx + 1) / 2) > per_xcd) --r.bx;
+  r.half = (r.bx + 1) / 2;
+  const int busy = r.full * r.bx + lt * r.half;
+  const bool levels = RT > 1 && rows[0] == rows[1] && 5 * busy >= 4 * per_xcd &&
+                      total1 >= 8 * r.bx;
+  bool idle;
+  int empty;  // this workgroup's entry of the join if it is idle
+  if (levels) {
+    idle = at >= busy;
+    empty = 8 * busy + xcd * (per_xcd - busy) + at - busy;
+    r.q = total1 / (8 * r.bx);
+    r.r = (int)(total1 - r.q * (8 * r.bx));
+    int j0, j1;
+    if (at < r.full * r.bx) {
+      r.level = at / r.bx;
+      j0 = xcd * r.bx + at % r.bx;
+      j1 = j0 + 1;
+      r.run = r.level * 8 * r.bx + j0;
+    } else {
+      const int x = at - r.full * r.bx;
+      r.level = r.full;
+      j0 = xcd * r.bx + 2 * x;
+      j1 = xcd * r.bx + min(2 * x + 2, r.bx);
+      r.run = r.full * 8 * r.bx + xcd * r.half + x;
+    }
+    r.u = r.start(j0);
+    r.end = r.start(j1);
+    incl = incl1;
+    mine = mine1;
+  } else {
+    const int n_run = (int)min((int64_t)n_wg, total < W ? total : total / W);
+    // neighbouring runs on one XCD (workgroups go round the 8 XCDs)
+    const int xbase = xcd * (n_run >> 3) + min(xcd, n_run & 7);
+    const int xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
+    idle = at >= xcount;
+    int before = 0;  // idle workgroups of the XCDs before this one
+    for (int x = 0; x < xcd; ++x)
+      before += per_xcd - ((n_run >> 3) + (x < (n_run & 7) ? 1 : 0));
+    empty = n_run + before + at - xcount;
+    if (!idle) {
+      r.run = xbase + at;
+      r.q = total / n_run;
+      r.r = (int)(total - r.q * n_run);
+      r.u = r.start(r.run);
+      r.end = r.start(r.run + 1);
+    }
+  }
+  if (idle) {
+    if (tid == 0) ws.meta[empty] = make_int4(0, 0, 0, -1);
     return false;
   }
-  r.run = xbase + at;
-  r.q_run = total / n_run;
-  r.r_run = (int)(total - r.q_run * n_run);
-  r.u = r.run * r.q_run + min(r.run, r.r_run);
-  r.end = (r.run + 1) * r.q_run + min(r.run + 1, r.r_run);
   if (incl - mine <= r.u && r.u < incl) {
     int64_t off = incl - mine;
     for (int b = tid * per;; ++b) {
-      const int64_t n = attend_req<MT, KS>(a, b).units;
+      const int64_t n = r.units(a, attend_req<MT, KS, W>(a, b));
       if (r.u < off + n) {
         seek_b = b;
         seek_off = off;
@@ -215,18 +358,28 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   return true;
 }
 
-// Query rows m0 + 16 nt + lane % 16 as B operands, with the scale's sign;
+// Moves on to the request that holds unit u.
+template <int MT, int KS, int W>
+__device__ __forceinline__ void next_request(const AttendArgs& a,
+                                             AttendRun& run, AttendReq& rq) {
+  while (run.u >= run.b_off + run.units(a, rq)) {
+    run.b_off += run.units(a, rq);
+    rq = attend_req<MT, KS, W>(a, ++run.b, true);
+  }
+}
+
+// Query rows m0 + stride nt + lane % 16 as B operands, with the scale's sign;
 // irow: their rows (0: the root).
 template <class C>
 __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int h,
-                                             int m0, int M,
+                                             int m0, int stride, int M,
                                              int (&irow)[C::NT],
                                              s16x8 (&qf)[C::NT][C::KSTEP]) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const int chd = a.g.D >> 3;
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
-    const int m = m0 + nt * 16 + col;
+    const int m = m0 + nt * stride + col;
     const int i = m / a.G;
     irow[nt] = i;
     const bool ok = m < M;
@@ -341,62 +494,30 @@ __device__ __forceinline__ void probabilities(float c,
   }
 }
 
-// Leaves the scores of 32 keys that a row sees (bits of `see`, one word per
-// 16-row block) and -inf in place of the others.
+// Adds the elements of the value at position t that are not finite to the
+// rows of block nt that see it (the tile holds 0 in their place); sk: the
+// rows' scores, -inf where it is not seen, in the lanes of quad `from`.
 template <class C>
-__device__ __forceinline__ void mask_scores(const uint32_t (&see)[C::NT],
-                                            f32x4 (&s)[C::NT][2]) {
-  const int quad = (threadIdx.x & 63) >> 4;
-#pragma unroll
-  for (int nt = 0; nt < C::NT; ++nt) {
-    const uint32_t w = see[nt] >> (4 * quad);
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!((w >> (16 * x + e)) & 1)) s[nt][x][e] = neg_inf();
-  }
-}
-
-// Adds the values of the given keys of the 32 from t0 on that are not finite
-// to the rows that see them (the tile holds 0 in their place).
-template <class C>
-__device__ __forceinline__ void add_odd_values(
-    const AttendArgs& a, const int32_t* table, int h, int t0, uint32_t keys,
-    const f32x4 (&s)[C::NT][2], AttendState<C>& st) {
+__device__ __forceinline__ void add_odd_value(const AttendArgs& a,
+                                              const int32_t* table, int h,
+                                              int t, int nt, float sk,
+                                              int from, AttendState<C>& st) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const PageGeom& g = a.g;
   const int D = opaque(g.D);
-  while (keys) {
-    const int key = __builtin_ctz(keys);
-    keys &= keys - 1;
-    const int t = t0 + key;
-    const int p = table[t >> g.shift];
-    const uint16_t* v =
-        static_cast<const uint16_t*>(a.vc) +
-        ((((int64_t)p * g.Hkv + h) << g.shift) + (t & ((1 << g.shift) - 1))) *
-            g.D;
+  const int p = table[t >> g.shift];
+  const uint16_t* v =
+      static_cast<const uint16_t*>(a.vc) +
+      ((((int64_t)p * g.Hkv + h) << g.shift) + (t & ((1 << g.shift) - 1))) * D;
+  sk = __shfl(sk, from * 16 + col, kWave);
+  const float pk = __builtin_amdgcn_exp2f(__builtin_fmaf(sk, a.c, -st.ms[nt]));
 #pragma unroll
-    for (int nt = 0; nt < C::NT; ++nt) {
-      float sk = 0.f;
+  for (int d = 0; d < C::DT; ++d) {
+    if (16 * d >= D) continue;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key >> 4 == x && (key & 3) == e) sk = s[nt][x][e];
-      sk = __shfl(sk, ((key >> 2) & 3) * 16 + col, kWave);
-      const float pk =
-          __builtin_amdgcn_exp2f(__builtin_fmaf(sk, a.c, -st.ms[nt]));
-#pragma unroll
-      for (int d = 0; d < C::DT; ++d) {
-        if (16 * d >= D) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = elem<C::BF16>(v[16 * d + 4 * quad + e]);
-          if (sk != neg_inf() && !(fabsf(x) < pos_inf()))
-            st.o[nt][d][e] += pk * x;
-        }
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float x = elem<C::BF16>(v[16 * d + 4 * quad + e]);
+      if (sk != neg_inf() && !(fabsf(x) < pos_inf())) st.o[nt][d][e] += pk * x;
     }
   }
 }

@@ -48,10 +48,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   const int col = lane & 15, quad = lane >> 4;
 
   AttendRun run;
-  if (!attend_schedule<C::MT, C::KS>(a, ws, run)) return;
-  int b = run.b;
-  int64_t u = run.u, b_off = run.b_off;
-  AttendReq rq = attend_req<C::MT, C::KS>(a, b);
+  if (!attend_schedule<C::MT, C::KS, 1>(a, ws, run)) return;
+  AttendReq rq = attend_req<C::MT, C::KS, 1>(a, run.b, true);
   int4 join = make_int4(0, 0, 0, -1);
 
   const uint4* kc = static_cast<const uint4*>(a.kc);
@@ -61,22 +59,17 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   uint4* kt = lds + wave * C::TILE;
   uint4* vt = kt + KB * C::KROW;
 
-  while (u < run.end) {
-    while (u >= b_off + rq.units) {
-      b_off += rq.units;
-      rq = attend_req<C::MT, C::KS>(a, ++b);
-    }
-    const int64_t in = u - b_off;  // step within the request
-    const int seg = (int)(in / rq.KT);
-    const int k0 = (int)(in - (int64_t)seg * rq.KT);
-    const int h = seg / rq.RT, rt = seg - h * rq.RT;
-    const int k1 = (int)min((int64_t)rq.KT, k0 + (run.end - u));
+  while (run.u < run.end) {
+    next_request<C::MT, C::KS, 1>(a, run, rq);
+    const int b = run.b;
+    const AttendPiece pc = attend_piece<1>(rq, run);
+    const int h = pc.h, rt = pc.rt, k0 = pc.k0, k1 = pc.k1;
     const int ctx = rq.ctx, L = rq.L;
     const int32_t* table = g.table + (int64_t)b * g.max_pages;
 
     int irow[NT];
     s16x8 qf[NT][KSTEP];
-    load_queries<C>(a, b, h, rt * C::MT, rq.M, irow, qf);
+    load_queries<C>(a, b, h, rt * C::MT, 16, rq.M, irow, qf);
     AttendState<C> st;
     st.clear();
 
@@ -169,11 +162,16 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
       // a tile with nodes, with missing pages or past the end
       if (tail || dead_keys != 0) {
         const uint64_t all = low_bits(L - t0) & ~dead_keys;
-        uint32_t see[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          see[nt] = (uint32_t)(seen_keys(a, b, irow[nt], rq.n, ctx, t0) & all);
-        mask_scores<C>(see, s);
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint64_t see =
+              (seen_keys(a, b, irow[nt], rq.n, ctx, t0) & all) >> (4 * quad);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((see >> (16 * x + e)) & 1)) s[nt][x][e] = neg_inf();
+        }
       }
       s16x8 pf[NT];
       raise_reference<C, 2>(a.c, s, st);
@@ -195,7 +193,20 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
         for (int nt = 0; nt < NT; ++nt)
           st.o[nt][d] = mfma16<C::BF16>(vf, pf[nt], st.o[nt][d]);
       }
-      add_odd_values<C>(a, table, h, t0, (uint32_t)odd_keys, s, st);
+      while (odd_keys) {
+        const int key = __builtin_ctzll(odd_keys);
+        odd_keys &= odd_keys - 1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float sk = 0.f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key >> 4 == x && (key & 3) == e) sk = s[nt][x][e];
+          add_odd_value<C>(a, table, h, t0 + key, nt, sk, (key >> 2) & 3, st);
+        }
+      }
     }
 
     // ---- sums to LDS, joined over the waves
@@ -257,10 +268,10 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     }
     if (!whole && k0 == 0) {
       // the join adds the runs up to the one that holds the last step
-      join = make_int4(b, h, rt, run.owner(u + rq.KT - 1));
+      join = make_int4(b, h, rt, run.owner(pc.s0 + rq.KT - 1));
     }
     __syncthreads();
-    u += k1 - k0;
+    run.u = pc.next;
   }
   if (tid == 0) ws.meta[run.run] = join;
 }
