@@ -114,17 +114,13 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0 : (n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1);
 }
 
-// Work of one request in units: a step of a row tile counts W units, one of
-// a row tile that fills at most half of it 1 unit (W = 2 where the kernel
-// has a form for such tiles, else 1).
+// Work of one request in units: a step of a row tile.
 struct AttendReq {
-  int ctx, n, L;    // context, nodes, positions
-  int M, KT;        // packed rows, steps of a row tile
-  int full, light;  // row tiles that count W units, 1 unit
-  int64_t head;     // units of a head
-  int64_t units;
+  int ctx, n, L;   // context, nodes, positions
+  int M, RT, KT;   // packed rows, row tiles, steps of a row tile
+  int64_t units;   // of all heads and row tiles
 };
-template <int MT, int KS, int W>
+template <int MT, int KS>
 __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
                                                 bool uniform = false) {
   const PageGeom& g = a.g;
@@ -139,12 +135,9 @@ __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
     r.L = __builtin_amdgcn_readfirstlane(r.L);
   }
   r.M = (r.n + 1) * a.G;
+  r.RT = (r.M + MT - 1) / MT;
   r.KT = (r.L + KS - 1) / KS;
-  r.full = (r.M + MT - 1) / MT;
-  r.light = W > 1 && r.M - (r.full - 1) * MT <= MT / 2 ? 1 : 0;
-  r.full -= r.light;
-  r.head = (int64_t)(W * r.full + r.light) * r.KT;
-  r.units = g.Hkv * r.head;
+  r.units = (int64_t)g.Hkv * r.RT * r.KT;
   return r;
 }
 
@@ -157,34 +150,26 @@ __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
 // row tile i of every head in the order (request, head, step).  All levels
 // are cut at the same places into blocks, and the runs of one block, one per
 // level, are on one XCD: they read the same keys at the same time, so the
-// keys come from its L2 for all levels but the first.  (With lines a run
-// goes through the row tiles of a head one after the other and every one of
-// them reads the keys from memory again: trees of 257 rows on 32 requests
-// 800 us, with levels LEVELS_US us.)  A level of half-filled row tiles has
-// half as many runs of two blocks each.
+// keys come from its L2 for all levels but the first.  With lines a run
+// goes through the row tiles of a head one after the other, and each of
+// them reads the keys from memory again.
 struct AttendRun {
   int run;  // index of this run; a row tile's runs follow each other
   int64_t u, end;
   int b;          // request that holds u; its units begin at b_off
   int64_t b_off;
   int level;      // row tile of the run, -1: lines
-  int full, bx, half;  // levels of full runs, blocks and half runs per XCD
+  int blocks;     // of a level
   int64_t q;      // run (block) j begins at unit j q + min(j, r)
   int r;
   __device__ __forceinline__ int64_t start(int j) const {
     return j * q + min(j, r);
   }
-  // run (block) that holds unit x
-  __device__ __forceinline__ int at(int64_t x) const {
-    const int64_t big = (int64_t)r * (q + 1);
-    return (int)(x < big ? x / (q + 1) : r + (x - big) / q);
-  }
-  // run of this run's level that holds unit x
+  // run that holds unit x of the lines, or of this run's level
   __device__ __forceinline__ int owner(int64_t x) const {
-    const int j = at(x);
-    if (level < 0) return j;
-    if (level < full) return level * 8 * bx + j;
-    return full * 8 * bx + j / bx * half + j % bx / 2;
+    const int64_t big = (int64_t)r * (q + 1);
+    const int j = (int)(x < big ? x / (q + 1) : r + (x - big) / q);
+    return level < 0 ? j : level * blocks + j;
   }
   __device__ __forceinline__ int64_t units(const AttendArgs& a,
                                            const AttendReq& rq) const {
@@ -193,67 +178,51 @@ struct AttendRun {
   }
 };
 
-// The steps [k0, k1) of head h and row tile rt that begin in the units
-// [u, end) of a request whose units begin at b_off; s0: the row tile's first
-// unit, w: units of its steps.  A step belongs to the run that holds its
-// first unit.
+// The steps [k0, k1) of head h and row tile rt that a run has from unit u on;
+// s0: the row tile's first unit.
 struct AttendPiece {
-  int h, rt, k0, k1, w;
-  int64_t s0, next;  // next: the first unit after the piece
+  int h, rt, k0, k1;
+  int64_t s0;
 };
-template <int W>
 __device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
                                                     const AttendRun& run) {
   AttendPiece p;
   const int64_t in = run.u - run.b_off;
-  if (run.level >= 0) {
-    p.h = (int)(in / rq.KT);
-    p.rt = run.level;
-    p.w = 1;
-    p.k0 = (int)(in - (int64_t)p.h * rq.KT);
-    p.s0 = run.u - p.k0;
-    p.k1 = (int)min((int64_t)rq.KT, p.k0 + run.end - run.u);
-    p.next = run.u + p.k1 - p.k0;
-    return p;
-  }
-  p.h = (int)(in / rq.head);
-  const int64_t r = in - p.h * rq.head;
-  p.rt = (int)min(r / ((int64_t)W * rq.KT), (int64_t)rq.full);
-  p.w = p.rt < rq.full ? W : 1;
-  const int64_t off = r - (int64_t)W * p.rt * rq.KT;
-  p.s0 = run.u - off;
-  p.k0 = (int)((off + p.w - 1) / p.w);
-  p.k1 = (int)min((int64_t)rq.KT, (off + run.end - run.u + p.w - 1) / p.w);
-  p.next = min(run.end, p.s0 + (int64_t)p.w * rq.KT);
+  const int seg = (int)(in / rq.KT);
+  p.k0 = (int)(in - (int64_t)seg * rq.KT);
+  p.k1 = (int)min((int64_t)rq.KT, p.k0 + run.end - run.u);
+  p.s0 = run.u - p.k0;
+  p.h = run.level < 0 ? seg / rq.RT : seg;
+  p.rt = run.level < 0 ? seg - p.h * rq.RT : run.level;
   return p;
 }
 
 // Fills in the run of this workgroup; false when it has none (its entry of
 // the join is then empty).
-template <int MT, int KS, int W>
+template <int MT, int KS>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
                                                 const AttendWs& ws,
                                                 AttendRun& r) {
   __shared__ int64_t wsum[4][2];
-  __shared__ int rows[2];  // smallest and largest M of the requests
+  __shared__ int tiles[2];  // least and most row tiles of a request
   __shared__ int64_t seek_off;
   __shared__ int seek_b;
   const PageGeom& g = a.g;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (g.batch + 255) / 256;
   if (tid == 0) {
-    rows[0] = 0x7fffffff;
-    rows[1] = 0;
+    tiles[0] = 0x7fffffff;
+    tiles[1] = 0;
   }
   __syncthreads();
   int64_t mine = 0, mine1 = 0;  // units of lines, of a level
   for (int b = tid * per; b < min((tid + 1) * per, g.batch); ++b) {
-    const AttendReq q = attend_req<MT, KS, W>(a, b);
+    const AttendReq q = attend_req<MT, KS>(a, b);
     mine += q.units;
     if (q.M > 0) {
       mine1 += (int64_t)g.Hkv * q.KT;
-      atomicMin(&rows[0], q.M);
-      atomicMax(&rows[1], q.M);
+      atomicMin(&tiles[0], q.RT);
+      atomicMax(&tiles[1], q.RT);
     }
   }
   int64_t incl = mine, incl1 = mine1;
@@ -282,68 +251,50 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   }
   const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
   const int n_wg = gridDim.x, per_xcd = n_wg >> 3;
-
   // levels, if they keep at least 4 of 5 workgroups busy
-  r.level = -1;
-  const int RT = (rows[1] + MT - 1) / MT;
-  const int lt = W > 1 && rows[1] - (RT - 1) * MT <= MT / 2 ? 1 : 0;
-  r.full = RT - lt;
-  r.bx = 2 * per_xcd / (2 * r.full + lt + (RT == 0));
-  if (r.full * r.bx + lt * ((r.bx + 1) / 2) > per_xcd) --r.bx;
-  r.half = (r.bx + 1) / 2;
-  const int busy = r.full * r.bx + lt * r.half;
-  const bool levels = RT > 1 && rows[0] == rows[1] && 5 * busy >= 4 * per_xcd &&
-                      total1 >= 8 * r.bx;
-  bool idle;
-  int empty;  // this workgroup's entry of the join if it is idle
-  if (levels) {
-    idle = at >= busy;
-    empty = 8 * busy + xcd * (per_xcd - busy) + at - busy;
-    r.q = total1 / (8 * r.bx);
-    r.r = (int)(total1 - r.q * (8 * r.bx));
-    int j0, j1;
-    if (at < r.full * r.bx) {
-      r.level = at / r.bx;
-      j0 = xcd * r.bx + at % r.bx;
-      j1 = j0 + 1;
-      r.run = r.level * 8 * r.bx + j0;
-    } else {
-      const int x = at - r.full * r.bx;
-      r.level = r.full;
-      j0 = xcd * r.bx + 2 * x;
-      j1 = xcd * r.bx + min(2 * x + 2, r.bx);
-      r.run = r.full * 8 * r.bx + xcd * r.half + x;
-    }
-    r.u = r.start(j0);
-    r.end = r.start(j1);
+  const int RT = tiles[1];
+  const int bx = RT > 0 ? per_xcd / RT : 0;  // blocks of an XCD
+  int n_run, xbase, xcount;  // runs, first run and runs of this XCD
+  if (RT > 1 && tiles[0] == RT && 5 * RT * bx >= 4 * per_xcd &&
+      total1 >= 8 * bx) {
+    n_run = 8 * RT * bx;
+    xcount = RT * bx;
+    xbase = 0;
+    r.level = at / bx;
+    r.blocks = 8 * bx;
+    r.run = r.level * r.blocks + xcd * bx + at % bx;
+    r.q = total1 / r.blocks;
+    r.r = (int)(total1 - r.q * r.blocks);
+    r.u = r.start(xcd * bx + at % bx);
+    r.end = r.start(xcd * bx + at % bx + 1);
     incl = incl1;
     mine = mine1;
   } else {
-    const int n_run = (int)min((int64_t)n_wg, total < W ? total : total / W);
     // neighbouring runs on one XCD (workgroups go round the 8 XCDs)
-    const int xbase = xcd * (n_run >> 3) + min(xcd, n_run & 7);
-    const int xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
-    idle = at >= xcount;
-    int before = 0;  // idle workgroups of the XCDs before this one
-    for (int x = 0; x < xcd; ++x)
-      before += per_xcd - ((n_run >> 3) + (x < (n_run & 7) ? 1 : 0));
-    empty = n_run + before + at - xcount;
-    if (!idle) {
-      r.run = xbase + at;
-      r.q = total / n_run;
-      r.r = (int)(total - r.q * n_run);
-      r.u = r.start(r.run);
-      r.end = r.start(r.run + 1);
-    }
+    n_run = (int)min((int64_t)n_wg, total);
+    xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
+    xbase = xcd * (n_run >> 3) + min(xcd, n_run & 7);
+    r.level = -1;
+    r.run = xbase + at;
+    r.q = n_run > 0 ? total / n_run : 0;
+    r.r = (int)(total - r.q * n_run);
+    r.u = r.start(r.run);
+    r.end = r.start(r.run + 1);
   }
-  if (idle) {
-    if (tid == 0) ws.meta[empty] = make_int4(0, 0, 0, -1);
+  if (at >= xcount) {  // no run
+    int before = 0;    // such workgroups of the XCDs before this one
+    for (int x = 0; x < xcd; ++x)
+      before += per_xcd - (r.level >= 0 ? xcount
+                                        : (n_run >> 3) +
+                                              (x < (n_run & 7) ? 1 : 0));
+    if (tid == 0)
+      ws.meta[n_run + before + at - xcount] = make_int4(0, 0, 0, -1);
     return false;
   }
   if (incl - mine <= r.u && r.u < incl) {
     int64_t off = incl - mine;
     for (int b = tid * per;; ++b) {
-      const int64_t n = r.units(a, attend_req<MT, KS, W>(a, b));
+      const int64_t n = r.units(a, attend_req<MT, KS>(a, b));
       if (r.u < off + n) {
         seek_b = b;
         seek_off = off;
@@ -359,12 +310,12 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
 }
 
 // Moves on to the request that holds unit u.
-template <int MT, int KS, int W>
+template <int MT, int KS>
 __device__ __forceinline__ void next_request(const AttendArgs& a,
                                              AttendRun& run, AttendReq& rq) {
   while (run.u >= run.b_off + run.units(a, rq)) {
     run.b_off += run.units(a, rq);
-    rq = attend_req<MT, KS, W>(a, ++run.b, true);
+    rq = attend_req<MT, KS>(a, ++run.b, true);
   }
 }
 

@@ -48,8 +48,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   const int col = lane & 15, quad = lane >> 4;
 
   AttendRun run;
-  if (!attend_schedule<C::MT, C::KS, 1>(a, ws, run)) return;
-  AttendReq rq = attend_req<C::MT, C::KS, 1>(a, run.b, true);
+  if (!attend_schedule<C::MT, C::KS>(a, ws, run)) return;
+  AttendReq rq = attend_req<C::MT, C::KS>(a, run.b, true);
   int4 join = make_int4(0, 0, 0, -1);
 
   const uint4* kc = static_cast<const uint4*>(a.kc);
@@ -60,9 +60,9 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   uint4* vt = kt + KB * C::KROW;
 
   while (run.u < run.end) {
-    next_request<C::MT, C::KS, 1>(a, run, rq);
+    next_request<C::MT, C::KS>(a, run, rq);
     const int b = run.b;
-    const AttendPiece pc = attend_piece<1>(rq, run);
+    const AttendPiece pc = attend_piece(rq, run);
     const int h = pc.h, rt = pc.rt, k0 = pc.k0, k1 = pc.k1;
     const int ctx = rq.ctx, L = rq.L;
     const int32_t* table = g.table + (int64_t)b * g.max_pages;
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
       join = make_int4(b, h, rt, run.owner(pc.s0 + rq.KT - 1));
     }
     __syncthreads();
-    run.u = pc.next;
+    run.u += pc.k1 - pc.k0;
   }
   if (tid == 0) ws.meta[run.run] = join;
 }

@@ -50,7 +50,7 @@ struct TilesCfg {
 // current one (both lie in one array): nothing is written to a register,
 // and the loop waits for the loads itself, before the barrier that precedes
 // the reads.
-__device__ __forceinline__ void load_to_lds(const uint4* base, int bytes,
+__device__ __forceinline__ void load_to_lds(const char* base, int bytes,
                                             int off, int to) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const uint64_t at = reinterpret_cast<uint64_t>(base);
@@ -98,6 +98,25 @@ __device__ __forceinline__ void tiles_piece(
   const int kp0 = (lane % SL) ^ C::swizzle_k(row0);
   const int vp0 = (lane % SL) ^ C::swizzle_v(row0);
   const int row_bytes = chd * 16, group_bytes = 8 * row_bytes;
+  // Load i's bytes from the beginning of its 8-key group on; a slot past the
+  // head size gets an offset past the group, which the bound of the buffer
+  // descriptor keeps from being read.
+  int koff[NI], voff[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int off = (lane / SL + (i * C::RPI & 7)) * row_bytes;
+    const int kp = kp0 ^ C::swizzle_k(i * C::RPI);
+    const int vp = vp0 ^ C::swizzle_v(i * C::RPI);
+    koff[i] = kp < chd ? off + kp * 16 : group_bytes;
+    voff[i] = vp < chd ? off + vp * 16 : group_bytes;
+  }
+  // bytes of a page, and of head h within it
+  const uint32_t page_bytes = (uint32_t)(g.Hkv * row_bytes) << g.shift;
+  const uint32_t head_bytes = (uint32_t)(h * row_bytes) << g.shift;
+  const char* k_head = static_cast<const char*>(a.kc) + head_bytes;
+  const char* v_head = static_cast<const char*>(a.vc) + head_bytes;
+  const int lds0 = __builtin_amdgcn_readfirstlane(
+      (int)(uintptr_t)(lds_s16x4)reinterpret_cast<s16x4*>(tiles));
   // operand reads: bytes of K for the first 32 elements, of V for the first
   // 16; later ones differ in bits of the swizzled slot only
   const int kx = (col * SL + (quad ^ C::swizzle_k(col))) * 16;
@@ -153,30 +172,18 @@ __device__ __forceinline__ void tiles_piece(
       pv_next = group_pages(kv + C::TPV);
     }
     const int first = (k - kv) * C::GPS;
-    const int lds0 = __builtin_amdgcn_readfirstlane(
-        (int)(uintptr_t)(lds_s16x4)reinterpret_cast<s16x4*>(tiles));
-    const int lr = opaque((lane / SL) * row_bytes);
-    const int kp = opaque(kp0), vp = opaque(vp0);
-    // bytes of a piece from its 8-key group on; a slot past the head size
-    // gets an offset past the group, which the bound of the buffer
-    // descriptor keeps from being read
-    auto bytes = [&](int piece, int i) {
-      const int off = lr + (i * C::RPI & 7) * row_bytes + piece * 16;
-      return piece < chd ? off : group_bytes;
-    };
+    int to = lds0 + (par * BUF + wave * NI * 64) * 16;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int grp = (wave * (KB / 4) + i * C::RPI) >> 3;
-      int p = __builtin_amdgcn_readlane(pv, first + grp);
-      p = (unsigned)p < (unsigned)g.n_pages ? p : 0;
-      const int64_t at = ((((int64_t)p * g.Hkv + h) << g.shift) +
-                          ((k * KB + 8 * grp) & page_mask)) * chd;
-      load_to_lds(static_cast<const uint4*>(a.kc) + at, group_bytes,
-                  bytes(kp ^ C::swizzle_k(i * C::RPI), i),
-                  lds0 + (par * BUF + (wave * NI + i) * 64) * 16);
-      load_to_lds(static_cast<const uint4*>(a.vc) + at, group_bytes,
-                  bytes(vp ^ C::swizzle_v(i * C::RPI), i),
-                  lds0 + (par * BUF + KB * SL + (wave * NI + i) * 64) * 16);
+      uint32_t p = __builtin_amdgcn_readlane(pv, first + grp);
+      p = p < (uint32_t)g.n_pages ? p : 0;
+      const uint64_t at =
+          (uint64_t)p * page_bytes +
+          (uint32_t)(((k * KB + 8 * grp) & page_mask) * row_bytes);
+      load_to_lds(k_head + at, group_bytes, koff[i], to);
+      load_to_lds(v_head + at, group_bytes, voff[i], to + KB * SL * 16);
+      to += 64 * 16;
     }
     return ((no_page >> first) & low_bits(C::GPS)) != 0;
   };
@@ -189,12 +196,15 @@ __device__ __forceinline__ void tiles_piece(
     for (int z = 0; z < KSTEP; ++z)
       kf[z] = *reinterpret_cast<const s16x8*>(kb + (kx0 ^ (64 * z)));
   };
-  auto scores = [&](const s16x8(&kf)[KSTEP], int nt)
+  auto scores = [&](const s16x8(&kf)[KSTEP], f32x4(&s)[NT])
       __attribute__((always_inline)) {
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int z = 0; z < KSTEP; ++z) s = mfma16<C::BF16>(kf[z], qf[nt][z], s);
-    return s;
+    for (int nt = 0; nt < NT; ++nt) s[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int z = 0; z < KSTEP; ++z)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        s[nt] = mfma16<C::BF16>(kf[z], qf[nt][z], s[nt]);
   };
   // operands of keys 32 y .. and elements 16 GD d0 .. of the tile in vt, and
   // their products
@@ -226,6 +236,8 @@ __device__ __forceinline__ void tiles_piece(
   // tiles are context that every row sees.
   auto tile = [&](auto edge_c, int k, int par)
       __attribute__((always_inline)) {
+    par = __builtin_amdgcn_readfirstlane(par);
+    k = __builtin_amdgcn_readfirstlane(k);
     uint4* kt = tiles + par * BUF;
     uint4* vt = kt + KB * SL;
     constexpr bool EDGE = decltype(edge_c)::value;
@@ -282,8 +294,10 @@ __device__ __forceinline__ void tiles_piece(
       else
         read_v(vt, 0, 0, vx0, vf[0]);
       __builtin_amdgcn_sched_barrier(0);
+      f32x4 sx[NT];
+      scores(kf[x & 1], sx);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][x] = scores(kf[x & 1], nt);
+      for (int nt = 0; nt < NT; ++nt) s[nt][x] = sx[nt];
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (EDGE) {
@@ -313,12 +327,16 @@ __device__ __forceinline__ void tiles_piece(
       while (odd_keys) {
         const int key = __builtin_ctzll(odd_keys);
         odd_keys &= odd_keys - 1;
+        f32x4 sx[NT];
         read_k(kt, key >> 4, kx0, kf[0]);
+        scores(kf[0], sx);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const f32x4 sx = scores(kf[0], nt);
           const int e = key & 3;
-          const float se = e == 0 ? sx[0] : e == 1 ? sx[1] : e == 2 ? sx[2] : sx[3];
+          const float se = e == 0   ? sx[nt][0]
+                           : e == 1 ? sx[nt][1]
+                           : e == 2 ? sx[nt][2]
+                                    : sx[nt][3];
           const bool on = (see[nt] >> ((key & ~15) + e)) & 1;
           add_odd_value<C>(a, table, h, t0 + key, nt,
                            on ? se : neg_inf(), (key >> 2) & 3, st);
@@ -383,13 +401,12 @@ template <class C>
 __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     AttendArgs a, AttendWs ws) {
   constexpr int KB = C::KB, SL = C::SL, MT = C::MT;
-  constexpr int W = C::NT;  // a tile of at most 64 rows counts half
   __shared__ __align__(16) uint4 tiles[4 * KB * SL];
   __shared__ uint64_t odd_s[2][4];
 
   AttendRun run;
-  if (!attend_schedule<MT, KB, W>(a, ws, run)) return;
-  AttendReq rq = attend_req<MT, KB, W>(a, run.b, true);
+  if (!attend_schedule<MT, KB>(a, ws, run)) return;
+  AttendReq rq = attend_req<MT, KB>(a, run.b, true);
   int4 join = make_int4(0, 0, 0, -1);
   if ((a.g.D >> 3) < SL) {
     // slots past the head size are read and never loaded
@@ -397,17 +414,17 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     for (int i = threadIdx.x; i < 4 * KB * SL; i += 256) tiles[i] = zero;
   }
   while (run.u < run.end) {
-    next_request<MT, KB, W>(a, run, rq);
+    next_request<MT, KB>(a, run, rq);
     const int b = run.b;
-    const AttendPiece pc = attend_piece<W>(rq, run);
-    // half-filled row tiles take the form with one block per wave
-    const bool light = W > 1 && pc.rt >= rq.full;
+    const AttendPiece pc = attend_piece(rq, run);
+    // row tiles that are at most half full take one block per wave
+    const bool light = C::NT > 1 && rq.M - pc.rt * MT <= MT / 2;
     // (the same in every lane, which the compiler cannot see)
     const int h = __builtin_amdgcn_readfirstlane(pc.h);
     const int m0 = __builtin_amdgcn_readfirstlane(pc.rt * MT);
     const int k0 = __builtin_amdgcn_readfirstlane(pc.k0);
     const int k1 = __builtin_amdgcn_readfirstlane(pc.k1);
-    if (k0 < k1) {
+    {
       const int slot = 2 * run.run + (k0 == 0 ? 1 : 0);
       if (light)
         tiles_piece<TilesCfg<C::DP, 1, C::BF16>, MT>(a, ws, rq, b, h, m0, k0,
@@ -417,9 +434,9 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
       // the join adds the runs up to the one that holds the last step
       if (k0 == 0 && k1 < rq.KT)
         join = make_int4(
-            b, h, pc.rt, run.owner(pc.s0 + (int64_t)pc.w * (rq.KT - 1)));
+            b, h, pc.rt, run.owner(pc.s0 + rq.KT - 1));
     }
-    run.u = pc.next;
+    run.u += pc.k1 - pc.k0;
   }
   if (threadIdx.x == 0) ws.meta[run.run] = join;
 }
