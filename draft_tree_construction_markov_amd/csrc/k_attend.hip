@@ -41,11 +41,13 @@ WsLayout layout(const AttendPlan& p) {
 
 }  // namespace
 
-// One workgroup per (run, quarter of the row tile) adds up the sums of a row
-// tile that starts in this run and ends in a later one, in order of runs
-// within each of PG groups of runs and then over the groups:
-//   m = max_w m_w, out = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w.
-constexpr int kJoinThreads = 1024;
+// A workgroup adds up ROWS rows of a row tile that starts in run blockIdx.x
+// and ends in a later one: LR threads per row (4 elements each), PG groups of
+// runs side by side, kInFlight runs of a group loaded at a time:
+//   m = max_w m_w, out = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w,
+// in order of runs within a group, then of groups.  Few rows are split over
+// many runs (PG = 4), many rows over few.
+constexpr int kJoinThreads = 256, kInFlight = 8;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t round_pair(float x, float y) {
@@ -59,11 +61,34 @@ __device__ __forceinline__ uint32_t round_pair(float x, float y) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
-template <bool BF16>
+struct JoinSum {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void scale(float m2) {
+    const float f = m2 == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(m - m2);
+    m = m2;
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+  }
+  __device__ __forceinline__ void add(float2 ml, const float4& v) {
+    const float f = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
+    l += f * ml.y;
+    o.x += f * v.x;
+    o.y += f * v.y;
+    o.z += f * v.z;
+    o.w += f * v.w;
+  }
+};
+
+template <bool BF16, int LR, int PG>
 __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
     AttendArgs a, AttendPlan p, AttendWs ws) {
-  __shared__ float4 acc_s[kJoinThreads];
-  __shared__ float2 ml_s[kJoinThreads];
+  constexpr int ROWS = kJoinThreads / LR / PG;
+  __shared__ float4 o_s[PG > 1 ? kJoinThreads : 1];
+  __shared__ float2 ml_s[PG > 1 ? kJoinThreads : 1];
   const PageGeom& g = a.g;
   const int run = blockIdx.x;
   const int4 seg = ws.meta[run];
@@ -71,100 +96,81 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
   const int b = seg.x, h = seg.y, rt = seg.z;
   const int runs = seg.w - run + 1;
   const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
-  const int M = (n + 1) * a.G;
   const int tid = threadIdx.x;
-  // LR threads per row (4 elements each), rows at a time, groups of runs
-  const int LR = p.dp <= 64 ? 16 : p.dp <= 128 ? 32 : 64;
-  const int quarter = p.mt / 4;
-  const int rows = min(quarter, kJoinThreads / LR);
-  const int PG = kJoinThreads / (LR * rows);
-  const int c = tid % LR, r_in = tid / LR % rows, pg = tid / (LR * rows);
-  const bool on = 4 * c < g.D;
-  for (int r0 = 0; r0 < quarter; r0 += rows) {
-    const int r = blockIdx.y * quarter + r0 + r_in;
-    const int m = rt * p.mt + r;
-    const bool live = m < M && on;
-    float top = neg_inf(), sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      constexpr int U = 8;  // runs in flight
-      for (int x0 = pg; x0 < runs; x0 += U * PG) {
-        float2 ml[U];
-        float4 o[U];
+  const int c = tid % LR, pg = tid / (LR * ROWS);
+  const int r = blockIdx.y * ROWS + tid / LR % ROWS;
+  const int m = rt * p.mt + r;
+  const bool live = m < (n + 1) * a.G && 4 * c < g.D;
+  JoinSum s{neg_inf(), 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (live) {
+    for (int x0 = pg; x0 < runs; x0 += kInFlight * PG) {
+      float2 ml[kInFlight];
+      float4 o[kInFlight];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const int x = x0 + k * PG;
-          ml[k] = make_float2(neg_inf(), 0.f);
-          o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (x < runs) {
-            const int64_t row =
-                (int64_t)(2 * (run + x) + (x == 0 ? 1 : 0)) * p.mt + r;
-            ml[k] = ws.ml[row];
-            o[k] = reinterpret_cast<const float4*>(ws.o + row * p.dp)[c];
-          }
-        }
-        float t2 = top;
-#pragma unroll
-        for (int k = 0; k < U; ++k) t2 = fmaxf(t2, ml[k].x);
-        const float f0 =
-            t2 == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(top - t2);
-        sum *= f0;
-        acc.x *= f0;
-        acc.y *= f0;
-        acc.z *= f0;
-        acc.w *= f0;
-        top = t2;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          if (x0 + k * PG >= runs) continue;
-          const float f =
-              t2 == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(ml[k].x - t2);
-          sum += f * ml[k].y;
-          acc.x += f * o[k].x;
-          acc.y += f * o[k].y;
-          acc.z += f * o[k].z;
-          acc.w += f * o[k].w;
-        }
+      for (int k = 0; k < kInFlight; ++k) {
+        // (past the last run: that one again, without weight)
+        const int x = min(x0 + k * PG, runs - 1);
+        const int64_t row =
+            (int64_t)(2 * (run + x) + (x == 0 ? 1 : 0)) * p.mt + r;
+        ml[k] = ws.ml[row];
+        o[k] = reinterpret_cast<const float4*>(ws.o + row * p.dp)[c];
       }
-    }
-    if (PG > 1) {
-      __syncthreads();
-      acc_s[tid] = acc;
-      ml_s[tid] = make_float2(top, sum);
-      __syncthreads();
-      if (pg == 0) {
-        const int step = LR * rows;
-        float t2 = neg_inf();
-        for (int y = 0; y < PG; ++y) t2 = fmaxf(t2, ml_s[tid + y * step].x);
-        sum = 0.f;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y = 0; y < PG; ++y) {
-          const float2 q = ml_s[tid + y * step];
-          const float4 v = acc_s[tid + y * step];
-          const float f =
-              t2 == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(q.x - t2);
-          sum += f * q.y;
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
-        }
-        top = t2;
-      }
-    }
-    if (live && pg == 0) {
-      const int i = m / a.G;
-      const int64_t row =
-          ((int64_t)b * (g.N + 1) + i) * a.Hq + h * a.G + (m - i * a.G);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * g.D)[c] =
-          make_uint2(round_pair<BF16>(acc.x * inv, acc.y * inv),
-                     round_pair<BF16>(acc.z * inv, acc.w * inv));
-      if (a.lse && c == 0)
-        a.lse[row] = sum == 0.f ? neg_inf()
-                                : (top + __builtin_log2f(sum)) * (float)kLn2;
+      float m2 = s.m;
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) m2 = fmaxf(m2, ml[k].x);
+      s.scale(m2);
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k)
+        if (x0 + k * PG < runs) s.add(ml[k], o[k]);
     }
   }
+  if constexpr (PG > 1) {
+    o_s[tid] = s.o;
+    ml_s[tid] = make_float2(s.m, s.l);
+    __syncthreads();
+    if (pg > 0) return;
+    float m2 = s.m;
+#pragma unroll
+    for (int y = 1; y < PG; ++y) m2 = fmaxf(m2, ml_s[tid + y * LR * ROWS].x);
+    s.scale(m2);
+#pragma unroll
+    for (int y = 1; y < PG; ++y)
+      s.add(ml_s[tid + y * LR * ROWS], o_s[tid + y * LR * ROWS]);
+  }
+  if (!live) return;
+  const int i = m / a.G;
+  const int64_t row =
+      ((int64_t)b * (g.N + 1) + i) * a.Hq + h * a.G + (m - i * a.G);
+  // nothing seen: zero (a NaN stays one)
+  const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * g.D)[c] =
+      make_uint2(round_pair<BF16>(s.o.x * inv, s.o.y * inv),
+                 round_pair<BF16>(s.o.z * inv, s.o.w * inv));
+  if (a.lse && c == 0)
+    a.lse[row] = s.l == 0.f ? neg_inf()
+                            : (s.m + __builtin_log2f(s.l)) * (float)kLn2;
+}
+
+template <bool BF16, int LR>
+hipError_t launch_join(const AttendArgs& a, const AttendPlan& p,
+                       const AttendWs& ws, hipStream_t s) {
+  if (p.mt <= 32)
+    hipLaunchKernelGGL((attend_join_kernel<BF16, LR, 4>),
+                       dim3(p.n_wg, p.mt / (kJoinThreads / LR / 4)),
+                       dim3(kJoinThreads), 0, s, a, p, ws);
+  else
+    hipLaunchKernelGGL((attend_join_kernel<BF16, LR, 1>),
+                       dim3(p.n_wg, p.mt / (kJoinThreads / LR)),
+                       dim3(kJoinThreads), 0, s, a, p, ws);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_join_type(const AttendArgs& a, const AttendPlan& p,
+                            const AttendWs& ws, hipStream_t s) {
+  if (p.dp <= 64) return launch_join<BF16, 16>(a, p, ws, s);
+  if (p.dp <= 128) return launch_join<BF16, 32>(a, p, ws, s);
+  return launch_join<BF16, 64>(a, p, ws, s);
 }
 
 size_t tree_attention_workspace(const pct_cache_shape& sh) {
@@ -197,14 +203,8 @@ hipError_t launch_tree_attention(const AttendArgs& a, void* workspace,
   }
   if (e != hipSuccess) return e;
   ProfScope ps(PROF_JOIN, (int64_t)g.batch * (g.N + 1), s);
-  const dim3 grid(p.n_wg, 4);
-  if (a.bf16)
-    hipLaunchKernelGGL(attend_join_kernel<true>, grid, dim3(kJoinThreads), 0,
-                       s, a, p, ws);
-  else
-    hipLaunchKernelGGL(attend_join_kernel<false>, grid, dim3(kJoinThreads), 0,
-                       s, a, p, ws);
-  return hipGetLastError();
+  return a.bf16 ? launch_join_type<true>(a, p, ws, s)
+                : launch_join_type<false>(a, p, ws, s);
 }
 
 }  // namespace pct

@@ -141,6 +141,12 @@ __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
   return r;
 }
 
+// x / d for x >= 0, d > 0, which mostly fit 32 bits.
+__device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t d) {
+  if (((x | d) >> 31) == 0) return (uint32_t)x / (uint32_t)d;
+  return x / d;
+}
+
 // How the work is cut into runs, one per workgroup.
 //
 // Lines: the units of all requests in the order (request, head, row tile,
@@ -168,7 +174,8 @@ struct AttendRun {
   // run that holds unit x of the lines, or of this run's level
   __device__ __forceinline__ int owner(int64_t x) const {
     const int64_t big = (int64_t)r * (q + 1);
-    const int j = (int)(x < big ? x / (q + 1) : r + (x - big) / q);
+    const int j = (int)(x < big ? div_up_to_64(x, q + 1)
+                                : r + div_up_to_64(x - big, q));
     return level < 0 ? j : level * blocks + j;
   }
   __device__ __forceinline__ int64_t units(const AttendArgs& a,
@@ -188,7 +195,7 @@ __device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
                                                     const AttendRun& run) {
   AttendPiece p;
   const int64_t in = run.u - run.b_off;
-  const int seg = (int)(in / rq.KT);
+  const int seg = (int)div_up_to_64(in, rq.KT);
   p.k0 = (int)(in - (int64_t)seg * rq.KT);
   p.k1 = (int)min((int64_t)rq.KT, p.k0 + run.end - run.u);
   p.s0 = run.u - p.k0;
@@ -263,7 +270,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     r.level = at / bx;
     r.blocks = 8 * bx;
     r.run = r.level * r.blocks + xcd * bx + at % bx;
-    r.q = total1 / r.blocks;
+    r.q = div_up_to_64(total1, r.blocks);
     r.r = (int)(total1 - r.q * r.blocks);
     r.u = r.start(xcd * bx + at % bx);
     r.end = r.start(xcd * bx + at % bx + 1);
@@ -276,7 +283,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     xbase = xcd * (n_run >> 3) + min(xcd, n_run & 7);
     r.level = -1;
     r.run = xbase + at;
-    r.q = n_run > 0 ? total / n_run : 0;
+    r.q = n_run > 0 ? div_up_to_64(total, n_run) : 0;
     r.r = (int)(total - r.q * n_run);
     r.u = r.start(r.run);
     r.end = r.start(r.run + 1);
@@ -319,18 +326,18 @@ __device__ __forceinline__ void next_request(const AttendArgs& a,
   }
 }
 
-// Query rows m0 + stride nt + lane % 16 as B operands, with the scale's sign;
+// Query rows m0 + 16 nt + lane % 16 as B operands, as they are;
 // irow: their rows (0: the root).
 template <class C>
 __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int h,
-                                             int m0, int stride, int M,
+                                             int m0, int M,
                                              int (&irow)[C::NT],
                                              s16x8 (&qf)[C::NT][C::KSTEP]) {
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const int chd = a.g.D >> 3;
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt) {
-    const int m = m0 + nt * stride + col;
+    const int m = m0 + nt * 16 + col;
     const int i = m / a.G;
     irow[nt] = i;
     const bool ok = m < M;
@@ -342,14 +349,26 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int h,
     for (int s = 0; s < C::KSTEP; ++s) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (ok && 4 * s + quad < chd) x = q[4 * s + quad];
-      // a scale of zero leaves zeros
+      qf[nt][s] = __builtin_bit_cast(s16x8, x);
+    }
+  }
+}
+
+// The scale's sign into the queries; a scale of zero leaves zeros.
+template <class C>
+__device__ __forceinline__ void sign_queries(const AttendArgs& a,
+                                             s16x8 (&qf)[C::NT][C::KSTEP]) {
+#pragma unroll
+  for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+    for (int s = 0; s < C::KSTEP; ++s) {
+      uint4 x = __builtin_bit_cast(uint4, qf[nt][s]);
       x.x = (x.x & a.qand) ^ a.qxor;
       x.y = (x.y & a.qand) ^ a.qxor;
       x.z = (x.z & a.qand) ^ a.qxor;
       x.w = (x.w & a.qand) ^ a.qxor;
       qf[nt][s] = __builtin_bit_cast(s16x8, x);
     }
-  }
 }
 
 // The keys t0 .. t0 + 63 that row i of request b sees, as bits (pages and

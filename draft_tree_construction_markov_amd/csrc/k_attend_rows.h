@@ -69,7 +69,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 
     int irow[NT];
     s16x8 qf[NT][KSTEP];
-    load_queries<C>(a, b, h, rt * C::MT, 16, rq.M, irow, qf);
+    load_queries<C>(a, b, h, rt * C::MT, rq.M, irow, qf);
+    sign_queries<C>(a, qf);
     AttendState<C> st;
     st.clear();
 

@@ -71,10 +71,9 @@ __device__ __forceinline__ void load_to_lds(const char* base, int bytes,
 #endif
 }
 
-// The steps [k0, k1) of one row tile, whose rows begin at m0: block nt of
-// wave w holds rows m0 + 64 nt + 16 w ...  Writes finished rows, or sums to
-// slot `slot` (of MT rows) for the join.
-template <class C, int MT>
+// The steps [k0, k1) of one row tile, whose rows begin at m0.  Writes finished
+// rows, or sums to slot `slot` (of MT rows) for the join.
+template <class C>
 __device__ __forceinline__ void tiles_piece(
     const AttendArgs& a, const AttendWs& ws, const AttendReq& rq, int b,
     int h, int m0, int k0, int k1, int slot, uint4* tiles,
@@ -123,14 +122,6 @@ __device__ __forceinline__ void tiles_piece(
   const int vkey = 4 * quad + (col >> 2);
   const int vx = (vkey * SL + C::swizzle_v(vkey)) * 16 + (col & 3) * 8;
 
-  int irow[NT];
-  s16x8 qf[NT][KSTEP];
-  m0 += 16 * wave;
-  load_queries<C>(a, b, h, m0, 64, rq.M, irow, qf);
-  const bool idle = m0 >= rq.M;  // a wave without rows loads keys only
-  AttendState<C> st;
-  st.clear();
-
   // Pages of the 8-key groups of TPV tiles, one per lane, and of the TPV
   // tiles after them.
   auto group_pages = [&](int k) {
@@ -139,7 +130,15 @@ __device__ __forceinline__ void tiles_piece(
   };
   int kv = k0;
   int pv = group_pages(k0), pv_next = group_pages(k0 + C::TPV);
+
+  m0 += 16 * NT * wave;
+  const bool idle = m0 >= rq.M;  // a wave without rows loads keys only
+  int irow[NT];
+  s16x8 qf[NT][KSTEP];
+  load_queries<C>(a, b, h, m0, rq.M, irow, qf);
   uint64_t no_page = __ballot((unsigned)pv >= (unsigned)g.n_pages);
+  AttendState<C> st;
+  st.clear();
 
   // LDS slots of K of buffer par, followed by those of V
   constexpr int BUF = 2 * KB * SL;
@@ -263,15 +262,17 @@ __device__ __forceinline__ void tiles_piece(
       // not exist become 0.  A node's value that is not finite must not meet
       // the probability 0 of a row that does not see it: it is taken out
       // here and added to the rows that see it below.
-#pragma unroll 1
-      for (int x = wave * (KB / 4) * SL + lane; x < (wave + 1) * (KB / 4) * SL;
-           x += 64) {
-        const int r = x / SL;
+      uint4 v[NI];
+      const int x0 = wave * (KB / 4) * SL + lane;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) v[i] = vt[x0 + 64 * i];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = (x0 + 64 * i) / SL;
         const bool live = (all >> r) & 1;
-        uint4 v = vt[x];
-        if (!live) vt[x] = make_uint4(0, 0, 0, 0);
-        const bool odd = live && t0 + r > ctx && drop_odd<C::BF16>(v);
-        if (odd) vt[x] = v;
+        if (!live) vt[x0 + 64 * i] = make_uint4(0, 0, 0, 0);
+        const bool odd = live && t0 + r > ctx && drop_odd<C::BF16>(v[i]);
+        if (odd) vt[x0 + 64 * i] = v[i];
         odd_keys |= key_bits(odd, r);
       }
       if (lane == 0) odd_s[par][wave] = odd_keys;
@@ -347,6 +348,8 @@ __device__ __forceinline__ void tiles_piece(
 
   __syncthreads();  // the previous piece's last tile has been read
   holes = issue(k0, 0);
+  // (the queries' own loads are on their way as well)
+  sign_queries<C>(a, qf);
   constexpr std::false_type plain{};
   constexpr std::true_type edge{};
   for (int k = k0, par = 0; k < k1;) {
@@ -367,7 +370,7 @@ __device__ __forceinline__ void tiles_piece(
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float sum = row_sum(st.l[nt]);
-    const int m = m0 + 64 * nt + col;
+    const int m = m0 + 16 * nt + col;
     if (m >= rq.M) continue;
     if (whole) {
       const int i = irow[nt];
@@ -387,7 +390,8 @@ __device__ __forceinline__ void tiles_piece(
                                 : (st.mx[nt] + __builtin_log2f(sum)) *
                                       (float)kLn2;
     } else {
-      const int64_t row = (int64_t)slot * MT + 64 * nt + 16 * wave + col;
+      const int64_t row =
+          (int64_t)slot * C::MT + (wave * NT + nt) * 16 + col;
       float* to = ws.o + row * C::DP + 4 * quad;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
@@ -417,25 +421,16 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     next_request<MT, KB>(a, run, rq);
     const int b = run.b;
     const AttendPiece pc = attend_piece(rq, run);
-    // row tiles that are at most half full take one block per wave
-    const bool light = C::NT > 1 && rq.M - pc.rt * MT <= MT / 2;
     // (the same in every lane, which the compiler cannot see)
     const int h = __builtin_amdgcn_readfirstlane(pc.h);
     const int m0 = __builtin_amdgcn_readfirstlane(pc.rt * MT);
     const int k0 = __builtin_amdgcn_readfirstlane(pc.k0);
     const int k1 = __builtin_amdgcn_readfirstlane(pc.k1);
-    {
-      const int slot = 2 * run.run + (k0 == 0 ? 1 : 0);
-      if (light)
-        tiles_piece<TilesCfg<C::DP, 1, C::BF16>, MT>(a, ws, rq, b, h, m0, k0,
-                                                     k1, slot, tiles, odd_s);
-      else
-        tiles_piece<C, MT>(a, ws, rq, b, h, m0, k0, k1, slot, tiles, odd_s);
-      // the join adds the runs up to the one that holds the last step
-      if (k0 == 0 && k1 < rq.KT)
-        join = make_int4(
-            b, h, pc.rt, run.owner(pc.s0 + rq.KT - 1));
-    }
+    tiles_piece<C>(a, ws, rq, b, h, m0, k0, k1, 2 * run.run + (k0 == 0),
+                   tiles, odd_s);
+    // the join adds the runs up to the one that holds the last step
+    if (k0 == 0 && k1 < rq.KT)
+      join = make_int4(b, h, pc.rt, run.owner(pc.s0 + rq.KT - 1));
     run.u += pc.k1 - pc.k0;
   }
   if (threadIdx.x == 0) ws.meta[run.run] = join;
