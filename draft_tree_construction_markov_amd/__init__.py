@@ -512,52 +512,49 @@ def _cache_dtype(dtype) -> int:
     return _CACHE_TYPES[dtype]
 
 
-def _want(name, t, dtype, shape, device):
-    """Check one tensor of a cache call and return its address."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of "
-                         f"shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t.data_ptr()
+def _want(name, t, dtype, shape, dev):
+    """Check one tensor of a cache call (dev: device index) and return its
+    address."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
+            t.is_contiguous()):
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
+                     f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _rows(name, t, dtype, shape, device):
+def _rows(name, t, dtype, shape, dev):
     """Check rows [batch][R][heads][D] whose heads are contiguous and whose
     rows are evenly spaced (a joint projection's view); returns the address
     and the row stride."""
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} tensor of shape "
                          f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
     b, R, H, D = shape
     sb, sr, sh, sd = t.stride()
     if R == 1:
         sr = sb if b > 1 else H * D
-    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (b > 1 and
-                                                      sb != R * sr):
+    if ((sd != 1 and D > 1) or (sh != D and H > 1) or
+            (b > 1 and sb != R * sr)):
         raise ValueError(f"{name} needs contiguous heads and evenly spaced "
                          f"rows, got strides {t.stride()}")
     return t.data_ptr(), sr
 
 
-class _on:
-    """Makes a device current for a call when it is not."""
-
-    def __init__(self, device):
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _enqueue(fn, dev: int, *args):
+    """Call a cache entry point on the current stream of device `dev`, which
+    is made current for the call when it is not."""
+    cuda = torch._C
+    if cuda._cuda_getDevice() == dev:
+        rc = fn(*args, cuda._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, cuda._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        _check(rc)
 
 
 def _device(device) -> torch.device:
@@ -585,59 +582,64 @@ class CachePlan:
                  max_pages: int, device="cuda"):
         self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, 1, 1,
                                 16, PCT_BF16)
-        self.device = _device(device)
-        dev = self.device
+        self.device = dev = _device(device)
         self.ws = _workspace(lib().pct_cache_plan_workspace(batch), dev)
         i32 = dict(dtype=torch.int32, device=dev)
         self.out = CacheRows(
             slot=torch.empty(batch, N + 1, dtype=torch.int64, device=dev),
             pos=torch.empty(batch, N + 1, **i32),
             missing=torch.empty(batch, **i32))
+        o = self.out
+        self._fn, self._ref = lib().pct_cache_plan, C.byref(self.shape)
+        self._shapes = ((batch,), (batch, N), (batch, max_pages), (n_pages,),
+                        (2,))
+        self._tail = tuple(C.c_void_p(x.data_ptr()) for x in (
+            o.slot, o.pos, o.missing, self.ws)) + (self.ws.numel(),)
 
     def run(self, ctx_len, n_nodes, block_table, n_held, ring, ring_state,
             depth=None) -> CacheRows:
         """n_nodes None = N everywhere; depth [batch][N] gives nodes their
         place in the sequence and is required unless N = 0."""
-        sh, o, dev, i32 = self.shape, self.out, self.device, torch.int32
-        one = (sh.batch,)
-        if depth is None and sh.N > 0:
+        dev, i32 = self.device.index, torch.int32
+        one, nodes, pages, free, state = self._shapes
+        if nodes[1] == 0:
+            dp = None
+        elif depth is None:
             raise ValueError("depth is required when N > 0")
-        args = (_want("ctx_len", ctx_len, i32, one, dev),
-                None if n_nodes is None else
-                _want("n_nodes", n_nodes, i32, one, dev),
-                None if sh.N == 0 else
-                _want("depth", depth, i32, (sh.batch, sh.N), dev),
-                _want("block_table", block_table, i32,
-                      (sh.batch, sh.max_pages), dev),
-                _want("n_held", n_held, i32, one, dev),
-                _want("ring", ring, i32, (sh.n_pages,), dev),
-                _want("ring_state", ring_state, i32, (2,), dev))
-        with _on(dev):
-            _check(lib().pct_cache_plan(
-                C.byref(sh), *args, o.slot.data_ptr(), o.pos.data_ptr(),
-                o.missing.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-                _stream(dev)))
-        return o
+        else:
+            dp = _want("depth", depth, i32, nodes, dev)
+        _enqueue(self._fn, dev, self._ref,
+                 _want("ctx_len", ctx_len, i32, one, dev),
+                 None if n_nodes is None else
+                 _want("n_nodes", n_nodes, i32, one, dev), dp,
+                 _want("block_table", block_table, i32, pages, dev),
+                 _want("n_held", n_held, i32, one, dev),
+                 _want("ring", ring, i32, free, dev),
+                 _want("ring_state", ring_state, i32, state, dev),
+                 *self._tail)
+        return self.out
 
 
 def cache_write(k, v, slot, k_cache, v_cache):
     """Write the rows k, v [batch][R][Hkv][D] (views with evenly spaced rows
     allowed) into slots slot [batch][R] of k_cache, v_cache
     [n_pages][Hkv][page_size][D]; a slot outside the cache is left out."""
-    dev = _dev(k_cache)
-    n_pages, Hkv, page, D = k_cache.shape
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise ValueError("libpctree needs device tensors")
+    cache = k_cache.shape
+    n_pages, Hkv, page, D = cache
     batch, R = slot.shape
     dt = k_cache.dtype
+    rows = (batch, R, Hkv, D)
     sh = CacheShape(batch, R - 1, n_pages, page, 1, Hkv, Hkv, D,
                     _cache_dtype(dt))
-    kp, ks = _rows("k", k, dt, (batch, R, Hkv, D), dev)
-    vp, vs = _rows("v", v, dt, (batch, R, Hkv, D), dev)
-    sp = _want("slot", slot, torch.int64, slot.shape, dev)
-    kc = _want("k_cache", k_cache, dt, k_cache.shape, dev)
-    vc = _want("v_cache", v_cache, dt, k_cache.shape, dev)
-    with _on(dev):
-        _check(lib().pct_cache_write(C.byref(sh), kp, ks, vp, vs, sp, kc, vc,
-                                     _stream(dev)))
+    kp, ks = _rows("k", k, dt, rows, dev)
+    vp, vs = _rows("v", v, dt, rows, dev)
+    _enqueue(lib().pct_cache_write, dev, C.byref(sh), kp, ks, vp, vs,
+             _want("slot", slot, torch.int64, (batch, R), dev),
+             _want("k_cache", k_cache, dt, cache, dev),
+             _want("v_cache", v_cache, dt, cache, dev))
 
 
 class TreeAttention:
@@ -650,9 +652,9 @@ class TreeAttention:
         self.dtype = dtype
         self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, Hq,
                                 Hkv, D, _cache_dtype(dtype))
-        self.device = _device(device)
-        dev = self.device
-        nbytes = lib().pct_tree_attention_workspace(C.byref(self.shape))
+        self.device = dev = _device(device)
+        self._fn, self._ref = lib().pct_tree_attention, C.byref(self.shape)
+        nbytes = lib().pct_tree_attention_workspace(self._ref)
         if nbytes == 0:
             raise PCTError(1, lib().pct_last_error().decode())
         self.ws = _workspace(nbytes, dev)
@@ -660,6 +662,13 @@ class TreeAttention:
         self.out = torch.zeros(batch, N + 1, Hq, D, dtype=dtype, device=dev)
         self.lse = (torch.zeros(batch, N + 1, Hq, dtype=torch.float32,
                                 device=dev) if lse else None)
+        self._shapes = ((batch, N + 1, Hq, D), (n_pages, Hkv, page_size, D),
+                        (batch, max_pages), (batch,),
+                        (batch, N, (N + 63) // 64))
+        self._op = C.c_void_p(self.out.data_ptr())
+        self._tail = (None if self.lse is None else
+                      C.c_void_p(self.lse.data_ptr()),
+                      C.c_void_p(self.ws.data_ptr()), self.ws.numel())
 
     def run(self, q, k_cache, v_cache, block_table, ctx_len, n_nodes=None,
             mask=None, scale=None, out=None):
@@ -667,30 +676,24 @@ class TreeAttention:
         mask [batch][N][ceil(N/64)] int64 or None (straight drafts); scale
         defaults to 1/sqrt(D).  Returns (out, lse), lse None unless the
         handle keeps it; out: another tensor for the outputs."""
-        sh, dev, dt, i32 = self.shape, self.device, self.dtype, torch.int32
-        rows = (sh.batch, sh.N + 1, sh.Hq, sh.D)
-        cache = (sh.n_pages, sh.Hkv, sh.page_size, sh.D)
+        dev, dt, i32 = self.device.index, self.dtype, torch.int32
+        rows, cache, pages, one, words = self._shapes
         if out is None:
-            out = self.out
-            op = out.data_ptr()
+            out, op = self.out, self._op
         else:
             op = _want("out", out, dt, rows, dev)
         qp, qs = _rows("q", q, dt, rows, dev)
-        args = (qp, qs, _want("k_cache", k_cache, dt, cache, dev),
-                _want("v_cache", v_cache, dt, cache, dev),
-                _want("block_table", block_table, i32,
-                      (sh.batch, sh.max_pages), dev),
-                _want("ctx_len", ctx_len, i32, (sh.batch,), dev),
-                None if n_nodes is None else
-                _want("n_nodes", n_nodes, i32, (sh.batch,), dev),
-                None if mask is None or sh.N == 0 else
-                _want("mask", mask, torch.int64,
-                      (sh.batch, sh.N, (sh.N + 63) // 64), dev))
-        with _on(dev):
-            _check(lib().pct_tree_attention(
-                C.byref(sh), sh.D ** -0.5 if scale is None else scale, *args,
-                op, None if self.lse is None else self.lse.data_ptr(),
-                self.ws.data_ptr(), self.ws.numel(), _stream(dev)))
+        _enqueue(self._fn, dev, self._ref,
+                 rows[3] ** -0.5 if scale is None else scale, qp, qs,
+                 _want("k_cache", k_cache, dt, cache, dev),
+                 _want("v_cache", v_cache, dt, cache, dev),
+                 _want("block_table", block_table, i32, pages, dev),
+                 _want("ctx_len", ctx_len, i32, one, dev),
+                 None if n_nodes is None else
+                 _want("n_nodes", n_nodes, i32, one, dev),
+                 None if mask is None or words[1] == 0 else
+                 _want("mask", mask, torch.int64, words, dev),
+                 op, *self._tail)
         return out, self.lse
 
 
@@ -714,31 +717,31 @@ def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
     k_cache, v_cache [layers][n_pages][Hkv][page_size][D] (or one layer).
     Returns the new context lengths, in `out` when given (which may be
     ctx_len itself)."""
-    dev = _dev(k_cache)
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    n_pages, Hkv, page, D = k_cache.shape[-4:]
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise ValueError("libpctree needs device tensors")
+    cache = k_cache.shape
+    n_pages, Hkv, page, D = cache[-4:]
+    layers = cache[0] if len(cache) == 5 else 1
     batch, B = accept_node.shape
-    dt, i32 = k_cache.dtype, torch.int32
+    width = block_table.shape[-1]
+    dt, i32, one = k_cache.dtype, torch.int32, (batch,)
     if out is None:
         out = torch.empty_like(ctx_len)
     # the rows are not read: any number of nodes up to the largest may be
     # accepted
-    sh = CacheShape(batch, 8192, n_pages, page, block_table.shape[1], Hkv,
-                    Hkv, D, _cache_dtype(dt))
-    args = (_want("tau", tau, i32, (batch,), dev),
-            _want("accept_node", accept_node, i32, (batch, B), dev),
-            None if n_nodes is None else
-            _want("n_nodes", n_nodes, i32, (batch,), dev),
-            _want("block_table", block_table, i32,
-                  (batch, block_table.shape[1]), dev),
-            _want("ctx_len", ctx_len, i32, (batch,), dev),
-            _want("k_cache", k_cache, dt, k_cache.shape, dev),
-            _want("v_cache", v_cache, dt, k_cache.shape, dev),
-            _want("out", out, i32, (batch,), dev))
-    with _on(dev):
-        _check(lib().pct_cache_commit(
-            C.byref(sh), layers, n_pages * Hkv * page * D, B, *args,
-            _stream(dev)))
+    sh = CacheShape(batch, 8192, n_pages, page, width, Hkv, Hkv, D,
+                    _cache_dtype(dt))
+    _enqueue(lib().pct_cache_commit, dev, C.byref(sh), layers,
+             n_pages * Hkv * page * D, B, _want("tau", tau, i32, one, dev),
+             _want("accept_node", accept_node, i32, (batch, B), dev),
+             None if n_nodes is None else
+             _want("n_nodes", n_nodes, i32, one, dev),
+             _want("block_table", block_table, i32, (batch, width), dev),
+             _want("ctx_len", ctx_len, i32, one, dev),
+             _want("k_cache", k_cache, dt, cache, dev),
+             _want("v_cache", v_cache, dt, cache, dev),
+             _want("out", out, i32, one, dev))
     return out
 
 

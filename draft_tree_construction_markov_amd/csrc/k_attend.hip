@@ -25,7 +25,14 @@ AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   p.shared = M > 32;
   p.nt = M <= 16 || (p.shared && M <= 64) ? 1 : 2;
   p.mt = 16 * p.nt * (p.shared ? 4 : 1);
+  p.ks = p.shared ? tiles_kb(p.dp) : 4 * kRowsKb;
+  p.least = p.shared ? kTilesLeast : kRowsLeast;
+  // as many runs as stay on the chip, or as the longest requests could fill
+  const int64_t steps = (cap + p.ks - 1) / p.ks;
+  const int64_t units = batch * (Hkv * ((M + p.mt - 1) / p.mt) * steps);
+  const int64_t runs = (units + p.least - 1) / p.least;
   p.n_wg = kCus * (p.dp <= 128 ? 2 : 1);
+  if (runs < p.n_wg) p.n_wg = (int)(runs + 7) / 8 * 8;
   return p;
 }
 

@@ -121,24 +121,41 @@ struct AttendReq {
   int64_t units;   // of all heads and row tiles
 };
 template <int MT, int KS>
+__device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
+                                                    int ctx, int n) {
+  AttendReq r;
+  r.n = n;
+  r.ctx = ctx;
+  r.L = min(ctx + n + 1, a.g.max_pages << a.g.shift);
+  r.M = (n + 1) * a.G;
+  r.RT = (r.M + MT - 1) / MT;
+  r.KT = (r.L + KS - 1) / KS;
+  r.units = (int64_t)a.g.Hkv * r.RT * r.KT;
+  return r;
+}
+// Lengths of request b; uniform: b is the same in every lane, and the lengths
+// are held in scalar registers.
+template <int MT, int KS>
 __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
                                                 bool uniform = false) {
   const PageGeom& g = a.g;
-  AttendReq r;
-  r.n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
-  r.ctx = clamp_ctx(g.ctx_len[b]);
-  r.L = min(r.ctx + r.n + 1, g.max_pages << g.shift);
-  // the same in every lane when b is: held in scalar registers
+  int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+  int ctx = clamp_ctx(g.ctx_len[b]);
   if (uniform) {
-    r.n = __builtin_amdgcn_readfirstlane(r.n);
-    r.ctx = __builtin_amdgcn_readfirstlane(r.ctx);
-    r.L = __builtin_amdgcn_readfirstlane(r.L);
+    n = __builtin_amdgcn_readfirstlane(n);
+    ctx = __builtin_amdgcn_readfirstlane(ctx);
   }
-  r.M = (r.n + 1) * a.G;
-  r.RT = (r.M + MT - 1) / MT;
-  r.KT = (r.L + KS - 1) / KS;
-  r.units = (int64_t)g.Hkv * r.RT * r.KT;
-  return r;
+  return attend_lengths<MT, KS>(a, ctx, n);
+}
+
+// a 64-bit value of lane l, of the last lane
+__device__ __forceinline__ int64_t lane_value(int64_t x, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, l);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(x >> 32), l);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int64_t last_lane(int64_t x) {
+  return lane_value(x, kWave - 1);
 }
 
 // x / d for x >= 0, d > 0, which mostly fit 32 bits.
@@ -204,32 +221,40 @@ __device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
   return p;
 }
 
-// Fills in the run of this workgroup; false when it has none (its entry of
-// the join is then empty).
+// Moves on to the request that holds unit u.
 template <int MT, int KS>
+__device__ __forceinline__ void next_request(const AttendArgs& a,
+                                             AttendRun& run, AttendReq& rq) {
+  while (run.u >= run.b_off + run.units(a, rq)) {
+    run.b_off += run.units(a, rq);
+    rq = attend_req<MT, KS>(a, ++run.b, true);
+  }
+}
+
+// Fills in the run of this workgroup; false when it has none (its entry of
+// the join is then empty).  Runs have at least LEAST units where there are as
+// many: each costs the sums it leaves for the join.  Every wave does this by
+// itself: lane l goes through requests l per .. (l + 1) per - 1, and the
+// sums over lanes need no LDS.
+template <int MT, int KS, int LEAST>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
                                                 const AttendWs& ws,
-                                                AttendRun& r) {
-  __shared__ int64_t wsum[4][2];
-  __shared__ int tiles[2];  // least and most row tiles of a request
-  __shared__ int64_t seek_off;
-  __shared__ int seek_b;
+                                                AttendRun& r, AttendReq& rq) {
   const PageGeom& g = a.g;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (g.batch + 255) / 256;
-  if (tid == 0) {
-    tiles[0] = 0x7fffffff;
-    tiles[1] = 0;
-  }
-  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  const int per = (g.batch + 63) / 64;
+  const int b0 = lane * per, b1 = min(b0 + per, g.batch);
   int64_t mine = 0, mine1 = 0;  // units of lines, of a level
-  for (int b = tid * per; b < min((tid + 1) * per, g.batch); ++b) {
-    const AttendReq q = attend_req<MT, KS>(a, b);
+  int least = 0x7fffffff, most = 0;  // row tiles of a request
+  AttendReq q{};
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) {
+    q = attend_req<MT, KS>(a, b);
     mine += q.units;
     if (q.M > 0) {
       mine1 += (int64_t)g.Hkv * q.KT;
-      atomicMin(&tiles[0], q.RT);
-      atomicMax(&tiles[1], q.RT);
+      least = min(least, q.RT);
+      most = max(most, q.RT);
     }
   }
   int64_t incl = mine, incl1 = mine1;
@@ -242,47 +267,36 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
       incl1 += y;
     }
   }
-  if (lane == 63) {
-    wsum[wave][0] = incl;
-    wsum[wave][1] = incl1;
-  }
-  __syncthreads();
-  int64_t total = 0, total1 = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) {
-      incl += wsum[w][0];
-      incl1 += wsum[w][1];
-    }
-    total += wsum[w][0];
-    total1 += wsum[w][1];
-  }
+  const int64_t total = last_lane(incl), total1 = last_lane(incl1);
+  const int RT = wave_max(most);
+  const bool same = __ballot(least != 0x7fffffff && least != RT) == 0;
   const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
   const int n_wg = gridDim.x, per_xcd = n_wg >> 3;
   // levels, if they keep at least 4 of 5 workgroups busy
-  const int RT = tiles[1];
-  const int bx = RT > 0 ? per_xcd / RT : 0;  // blocks of an XCD
-  int n_run, xbase, xcount;  // runs, first run and runs of this XCD
-  if (RT > 1 && tiles[0] == RT && 5 * RT * bx >= 4 * per_xcd &&
-      total1 >= 8 * bx) {
+  int bx = RT > 0 ? per_xcd / RT : 0;  // blocks of an XCD
+  const bool levels = RT > 1 && same && 5 * RT * bx >= 4 * per_xcd &&
+                      total1 >= 8 * LEAST;
+  bx = (int)min((int64_t)bx, total1 / (8 * LEAST));
+  int n_run, xcount;  // runs, and runs of this XCD
+  if (levels) {
     n_run = 8 * RT * bx;
     xcount = RT * bx;
-    xbase = 0;
+    const int j = xcd * bx + at % bx;
     r.level = at / bx;
     r.blocks = 8 * bx;
-    r.run = r.level * r.blocks + xcd * bx + at % bx;
+    r.run = r.level * r.blocks + j;
     r.q = div_up_to_64(total1, r.blocks);
     r.r = (int)(total1 - r.q * r.blocks);
-    r.u = r.start(xcd * bx + at % bx);
-    r.end = r.start(xcd * bx + at % bx + 1);
+    r.u = r.start(j);
+    r.end = r.start(j + 1);
     incl = incl1;
     mine = mine1;
   } else {
     // neighbouring runs on one XCD (workgroups go round the 8 XCDs)
-    n_run = (int)min((int64_t)n_wg, total);
+    n_run = (int)min((int64_t)n_wg, total < LEAST ? total : total / LEAST);
     xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
-    xbase = xcd * (n_run >> 3) + min(xcd, n_run & 7);
     r.level = -1;
-    r.run = xbase + at;
+    r.run = xcd * (n_run >> 3) + min(xcd, n_run & 7) + at;
     r.q = n_run > 0 ? div_up_to_64(total, n_run) : 0;
     r.r = (int)(total - r.q * n_run);
     r.u = r.start(r.run);
@@ -294,36 +308,24 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
       before += per_xcd - (r.level >= 0 ? xcount
                                         : (n_run >> 3) +
                                               (x < (n_run & 7) ? 1 : 0));
-    if (tid == 0)
+    if (threadIdx.x == 0)
       ws.meta[n_run + before + at - xcount] = make_int4(0, 0, 0, -1);
     return false;
   }
-  if (incl - mine <= r.u && r.u < incl) {
-    int64_t off = incl - mine;
-    for (int b = tid * per;; ++b) {
-      const int64_t n = r.units(a, attend_req<MT, KS>(a, b));
-      if (r.u < off + n) {
-        seek_b = b;
-        seek_off = off;
-        break;
-      }
-      off += n;
-    }
+  // the lane whose requests hold unit u, then the request
+  const int l = __builtin_ctzll(__ballot(r.u < incl));
+  r.b = l * per;
+  r.b_off = lane_value(incl - mine, l);
+  if (per == 1) {
+    // (already loaded)
+    rq = attend_lengths<MT, KS>(
+        a, __builtin_amdgcn_readlane(q.ctx, l),
+        __builtin_amdgcn_readlane(q.n, l));
+  } else {
+    rq = attend_req<MT, KS>(a, r.b, true);
+    next_request<MT, KS>(a, r, rq);
   }
-  __syncthreads();
-  r.b = __builtin_amdgcn_readfirstlane(seek_b);
-  r.b_off = seek_off;
   return true;
-}
-
-// Moves on to the request that holds unit u.
-template <int MT, int KS>
-__device__ __forceinline__ void next_request(const AttendArgs& a,
-                                             AttendRun& run, AttendReq& rq) {
-  while (run.u >= run.b_off + run.units(a, rq)) {
-    run.b_off += run.units(a, rq);
-    rq = attend_req<MT, KS>(a, ++run.b, true);
-  }
 }
 
 // Query rows m0 + 16 nt + lane % 16 as B operands, as they are;

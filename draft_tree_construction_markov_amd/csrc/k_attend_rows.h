@@ -15,7 +15,7 @@ struct RowsCfg {
   static constexpr int DP = DP_;  // head size, padded
   static constexpr int NT = NT_;  // 16-row blocks
   static constexpr bool BF16 = BF16_;
-  static constexpr int KB = 32;  // keys of a wave's tile
+  static constexpr int KB = kRowsKb;  // keys of a wave's tile
   static constexpr int DT = DP / 16, KSTEP = DP / 32;
   static constexpr int CH = DP / 8;  // 16-byte pieces of a row
   static constexpr int KS = 4 * KB;
@@ -32,7 +32,15 @@ struct RowsCfg {
   static constexpr int LDS_DUMP = 4 * MT * DROW * 4;
   static constexpr int LDS = LDS_TILES > LDS_DUMP ? LDS_TILES : LDS_DUMP;
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
+  static constexpr int LEAST = kRowsLeast;  // steps of a run
 };
+
+// 16 bytes that nothing reads again soon
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
 
 template <class C>
 __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
@@ -48,8 +56,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   const int col = lane & 15, quad = lane >> 4;
 
   AttendRun run;
-  if (!attend_schedule<C::MT, C::KS>(a, ws, run)) return;
-  AttendReq rq = attend_req<C::MT, C::KS>(a, run.b, true);
+  AttendReq rq;
+  if (!attend_schedule<C::MT, C::KS, C::LEAST>(a, ws, run, rq)) return;
   int4 join = make_int4(0, 0, 0, -1);
 
   const uint4* kc = static_cast<const uint4*>(a.kc);
@@ -101,8 +109,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
         const int c = piece_of(j);
         kr[j] = vr[j] = make_uint4(0, 0, 0, 0);
         if (c < chd) {
-          kr[j] = kc[row * chd + c];
-          vr[j] = vc[row * chd + c];
+          kr[j] = load_once(kc + row * chd + c);
+          vr[j] = load_once(vc + row * chd + c);
         }
       }
     };

@@ -25,7 +25,7 @@ struct TilesCfg {
   static constexpr int NT = NT_;  // 16-row blocks per wave
   static constexpr bool BF16 = BF16_;
   static constexpr int SL = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;
-  static constexpr int KB = DP <= 128 ? 64 : 32;  // keys of a tile
+  static constexpr int KB = tiles_kb(DP);  // keys of a tile
   static constexpr int DT = DP / 16, KSTEP = DP / 32;
   static constexpr int GD = DT % 4 == 0 ? 4 : 2;  // V operands of a group
   static constexpr int KS = KB;
@@ -35,6 +35,7 @@ struct TilesCfg {
   static constexpr int GPS = KB / 8;        // 8-key groups of a tile
   static constexpr int TPV = 64 / GPS;      // tiles whose pages fit a wave
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
+  static constexpr int LEAST = kTilesLeast;  // tiles of a run
   static __device__ __forceinline__ int swizzle_k(int r) {
     return SL == 8 ? (r >> 1) & 7 : r & 15;
   }
@@ -409,8 +410,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
   __shared__ uint64_t odd_s[2][4];
 
   AttendRun run;
-  if (!attend_schedule<MT, KB>(a, ws, run)) return;
-  AttendReq rq = attend_req<MT, KB>(a, run.b, true);
+  AttendReq rq;
+  if (!attend_schedule<MT, KB, C::LEAST>(a, ws, run, rq)) return;
   int4 join = make_int4(0, 0, 0, -1);
   if ((a.g.D >> 3) < SL) {
     // slots past the head size are read and never loaded

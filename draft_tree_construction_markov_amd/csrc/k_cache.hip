@@ -16,13 +16,18 @@ namespace pct {
 // behind it never meet (free and held pages together are at most n_pages),
 // so takes and gives of different requests need no order between them.
 //
-// plan_scan: one workgroup computes both prefix sums and the new state;
+// plan_scan: one workgroup computes both prefix sums and the new state.
 // plan_apply: block tables, ring entries, slots and places, a workgroup for
-// each piece of a request's rows.
+// each piece of a request's rows.  Both are bound by the latency of a few
+// dependent loads.  Plans of few rows and requests run in plan_small, one
+// workgroup that does both (65 rows of one request: SMALL_US us instead of
+// TWO_US us for the two launches).
 
 constexpr int kScanThreads = 1024;
 constexpr int kApplyThreads = 256;
-constexpr int kApplyRows = 1024;  // rows per workgroup of plan_apply
+constexpr int kApplyRows = 256;   // rows per workgroup of plan_apply
+constexpr int kSmallRows = 4096;  // rows of a plan in one workgroup, at most
+constexpr int kSmallBatch = 64;   // and requests
 
 __device__ __forceinline__ int64_t pages_for(int64_t tokens, int shift) {
   return (tokens + ((1 << shift) - 1)) >> shift;
@@ -51,7 +56,7 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b,
   }
 }
 
-__global__ __launch_bounds__(kScanThreads) void plan_scan_kernel(PlanArgs a) {
+__device__ __forceinline__ void plan_scan(const PlanArgs& a) {
   __shared__ int64_t sum[kScanThreads / kWave][2];
   __shared__ int64_t total[3];  // wanted, given back, taken
   const int tid = threadIdx.x;
@@ -104,36 +109,28 @@ __global__ __launch_bounds__(kScanThreads) void plan_scan_kernel(PlanArgs a) {
   }
 }
 
-__global__ __launch_bounds__(kApplyThreads) void plan_apply_kernel(
-    PlanArgs a) {
+// Rows [r0, r1) of request b; its pages as well where r0 is 0.
+template <int THREADS>
+__device__ __forceinline__ void plan_apply(const PlanArgs& a, int b, int r0,
+                                           int r1) {
   const PageGeom& g = a.g;
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const int4 rq = a.req[b];
   const int2 ring0 = a.ring0[0];
+  const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+  const int ctx = clamp_ctx(g.ctx_len[b]);
   const int held = rq.z, after = rq.w;
   const int P = g.n_pages;
   int32_t* table = a.table + (int64_t)b * g.max_pages;
-  if (blockIdx.y == 0) {
-    for (int j = held + tid; j < after; j += kApplyThreads)
-      table[j] = a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
-    for (int j = after + tid; j < held; j += kApplyThreads) {
-      a.ring[((int64_t)ring0.x + ring0.y + rq.y + j - after) % P] = table[j];
-      table[j] = -1;
-    }
-  }
-  const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
-  const int ctx = clamp_ctx(g.ctx_len[b]);
-  const int R = g.N + 1;
-  const int r1 = min((int)(blockIdx.y + 1) * kApplyRows, R);
   const int page_mask = (1 << g.shift) - 1;
-  for (int i = blockIdx.y * kApplyRows + tid; i < r1; i += kApplyThreads) {
+  for (int i = r0 + tid; i < r1; i += THREADS) {
     int64_t s = -1;
     int place = -1;
     if (i <= n) {
       const int p = ctx + i, j = p >> g.shift;
       if (j < after) {
-        // pages taken by this call are read where they come from: another
-        // workgroup may not have written them to the table yet
+        // pages taken by this call are read where they come from: the table
+        // may not hold them yet
         const int page =
             j < held ? table[j]
                      : a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
@@ -142,12 +139,43 @@ __global__ __launch_bounds__(kApplyThreads) void plan_apply_kernel(
       }
       if (a.pos) place = ctx + (i > 0 ? a.depth[(int64_t)b * g.N + i - 1] : 0);
     }
-    a.slot[(int64_t)b * R + i] = s;
-    if (a.pos) a.pos[(int64_t)b * R + i] = place;
+    a.slot[(int64_t)b * (g.N + 1) + i] = s;
+    if (a.pos) a.pos[(int64_t)b * (g.N + 1) + i] = place;
+  }
+  if (r0 == 0) {
+    for (int j = held + tid; j < after; j += THREADS)
+      table[j] = a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
+    for (int j = after + tid; j < held; j += THREADS) {
+      a.ring[((int64_t)ring0.x + ring0.y + rq.y + j - after) % P] = table[j];
+      table[j] = -1;
+    }
   }
 }
 
+__global__ __launch_bounds__(kScanThreads) void plan_scan_kernel(PlanArgs a) {
+  plan_scan(a);
+}
+
+__global__ __launch_bounds__(kApplyThreads) void plan_apply_kernel(
+    PlanArgs a) {
+  plan_apply<kApplyThreads>(a, blockIdx.x, blockIdx.y * kApplyRows,
+                            min((int)(blockIdx.y + 1) * kApplyRows, a.g.N + 1));
+}
+
+__global__ __launch_bounds__(kScanThreads) void plan_small_kernel(PlanArgs a) {
+  plan_scan(a);
+  __syncthreads();
+  for (int b = 0; b < a.g.batch; ++b)
+    plan_apply<kScanThreads>(a, b, 0, a.g.N + 1);
+}
+
 hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s) {
+  if (a.g.batch <= kSmallBatch &&
+      (int64_t)a.g.batch * (a.g.N + 1) <= kSmallRows) {
+    hipLaunchKernelGGL(plan_small_kernel, dim3(1), dim3(kScanThreads), 0, s,
+                       a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -194,8 +222,11 @@ hipError_t launch_cache_write(const WriteArgs& a, hipStream_t s) {
 // its request in ascending j, kMove sources loaded before their stores,
 // reads every source before anything overwrites it (a later source a_j is
 // at least j, past every place written so far), and columns do not touch
-// each other.  Moves onto themselves are left out.
-constexpr int kMove = 8;
+// each other.  Moves onto themselves are left out.  A path of the usual
+// depth is one round of loads: the time is the latency of the chain lengths
+// and nodes -> pages -> rows -> stores, then the bytes (COMMIT_US).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+constexpr int kMove = 16;
 constexpr int kMoveList = 128;  // moves resolved to slots at a time
 
 __global__ __launch_bounds__(256) void cache_commit_kernel(CommitArgs a,
@@ -204,11 +235,14 @@ __global__ __launch_bounds__(256) void cache_commit_kernel(CommitArgs a,
   __shared__ int s_end;
   const PageGeom& g = a.g;
   const int b = blockIdx.y, tid = threadIdx.x;
+  const int32_t* acc = a.accept + (int64_t)b * a.B;
+  const int nd0 = tid < min(kMoveList, a.B) ? acc[tid] : -1;
+  const int len = g.ctx_len[b];
   const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
-  const int ctx = clamp_ctx(g.ctx_len[b]);
+  const int ctx = clamp_ctx(len);
   const int tau = min(max(a.tau[b], 0), a.B + 1);
   if (write_len && blockIdx.x == 0 && tid == 0)
-    a.ctx_out[b] = n < 0 ? g.ctx_len[b] : ctx + tau;
+    a.ctx_out[b] = n < 0 ? len : ctx + tau;
   const int moves = n < 0 ? 0 : min(min(tau - 1, a.B), n);
   const int hc = g.D / 8;
   const int cols = a.layers * g.Hkv * hc * 2;
@@ -221,7 +255,6 @@ __global__ __launch_bounds__(256) void cache_commit_kernel(CommitArgs a,
   cache += (int64_t)(lh / g.Hkv) * a.layer_stride +
            ((int64_t)h << g.shift) * hc + c;
   const int32_t* table = g.table + (int64_t)b * g.max_pages;
-  const int32_t* acc = a.accept + (int64_t)b * a.B;
   const int64_t page_chunks = ((int64_t)g.Hkv << g.shift) * hc;
   auto place = [&](int64_t p) -> int64_t {  // chunk of a position, -1: none
     const int64_t j = p >> g.shift;
@@ -234,7 +267,7 @@ __global__ __launch_bounds__(256) void cache_commit_kernel(CommitArgs a,
     __syncthreads();
     const int j = j0 + tid;
     if (tid < kMoveList && j < moves) {
-      const int nd = acc[j];
+      const int nd = j0 == 0 ? nd0 : acc[j];
       if (nd < 0 || nd >= n) {
         atomicMin(&s_end, tid);
       } else {
@@ -248,13 +281,17 @@ __global__ __launch_bounds__(256) void cache_commit_kernel(CommitArgs a,
     const int end = s_end;
     if (live) {
       for (int i0 = 0; i0 < end; i0 += kMove) {
-        uint4 x[kMove];
+        u32x4 x[kMove];
+#pragma unroll
+        for (int u = 0; u < kMove; ++u) {
+          // (without a move: the first row of the cache, not stored)
+          const int64_t f = i0 + u < end ? from[i0 + u] : -1;
+          x[u] = *reinterpret_cast<const u32x4*>(cache + (f < 0 ? 0 : f));
+        }
 #pragma unroll
         for (int u = 0; u < kMove; ++u)
-          if (i0 + u < end && from[i0 + u] >= 0) x[u] = cache[from[i0 + u]];
-#pragma unroll
-        for (int u = 0; u < kMove; ++u)
-          if (i0 + u < end && from[i0 + u] >= 0) cache[to[i0 + u]] = x[u];
+          if (i0 + u < end && from[i0 + u] >= 0)
+            *reinterpret_cast<u32x4*>(cache + to[i0 + u]) = x[u];
       }
     }
     if (end < min(moves - j0, kMoveList)) break;

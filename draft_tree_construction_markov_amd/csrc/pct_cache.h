@@ -70,10 +70,17 @@ struct AttendArgs {
 };
 // Tile of a call: heads padded to dp elements, nt 16-row blocks per wave, the
 // waves share their keys (and hold different rows) or not, mt rows per
-// workgroup, n_wg runs.
+// workgroup, steps of ks keys, runs of `least` steps at least, n_wg runs at
+// most (a multiple of 8).
 struct AttendPlan {
-  int dp, nt, shared, mt, n_wg;
+  int dp, nt, shared, mt, ks, least, n_wg;
 };
+// Keys of a tile: of a wave's own one, of one that the waves share (32 where
+// 64 would leave no room for two buffers twice on a CU).
+constexpr int kRowsKb = 32;
+constexpr int tiles_kb(int dp) { return dp <= 128 ? 64 : 32; }
+// Steps of a run at least.  LEAST_NOTE
+constexpr int kRowsLeast = 1, kTilesLeast = 6;
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
 // end; meta {request, head, row tile, last run} of the latter, w < 0: none.

@@ -152,13 +152,13 @@ def test_commit_refuses():
 
 def test_binding_checks_tensors():
     t = torch.zeros(4, 6, dtype=torch.int32)
-    cpu = torch.device("cpu")
+    cpu = -1  # the device index of host tensors
     assert pct._want("t", t, torch.int32, (4, 6), cpu) == t.data_ptr()
     for bad in (t.long(), t[:, :5], t.T, t[:3]):
         with pytest.raises(ValueError):
             pct._want("t", bad, torch.int32, (4, 6), cpu)
     with pytest.raises(ValueError):
-        pct._want("t", t, torch.int32, (4, 6), torch.device("cuda", 0))
+        pct._want("t", t, torch.int32, (4, 6), 0)
     x = torch.zeros(2, 3, 10, 16, dtype=torch.bfloat16)
     s = (2, 3, 4, 16)
     assert pct._rows("x", x[:, :, 2:6], x.dtype, s, cpu)[1] == 160
@@ -173,7 +173,17 @@ def test_binding_checks_tensors():
         with pytest.raises(ValueError):
             pct._rows("x", bad, x.dtype, s, cpu)
     with pytest.raises(ValueError):
+        pct._rows("x", x[:, :, :4], x.dtype, s, 0)
+    with pytest.raises(ValueError):
         pct._cache_dtype(torch.float32)
+    # host tensors are refused before any call
+    c = torch.zeros(3, 2, 8, 16, dtype=torch.bfloat16)
+    i = torch.zeros(2, 1, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        pct.cache_write(c, c, i, c, c)
+    j = torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        pct.cache_commit(j[:, 0], j, j[:, 0], None, j, c, c)
 
 
 def test_definition_of_the_plan():
