@@ -109,6 +109,13 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
+// x of lane l
+__device__ __forceinline__ uint64_t shfl_bits(uint64_t x, int l) {
+  const uint32_t lo = __shfl((int)(uint32_t)x, l, kWave);
+  const uint32_t hi = __shfl((int)(x >> 32), l, kWave);
+  return (uint64_t)hi << 32 | lo;
+}
+
 // the lowest n bits (n clamped to [0, 64])
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0 : (n >= 64 ? ~(uint64_t)0 : ((uint64_t)1 << n) - 1);

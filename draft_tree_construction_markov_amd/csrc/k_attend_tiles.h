@@ -141,6 +141,32 @@ __device__ __forceinline__ void tiles_piece(
   AttendState<C> st;
   st.clear();
 
+  // Mask words of a tile's nodes, loaded with the tile: lane l has the word
+  // of the first node for row l % 32 (l % 16 with one block) of the wave's
+  // rows if l < 32, else the word after it.
+  const int mrow = m0 + (lane & (16 * NT - 1));
+  const int node = mrow < rq.M ? mrow / a.G : 0;  // 0: the root
+  uint64_t word = 0;
+  auto load_word = [&](int k) __attribute__((always_inline)) {
+    if (a.mask == nullptr || (k + 1) * KB <= ctx + 1) return;
+    const int w = (max(k * KB - ctx - 1, 0) >> 6) + (lane >> 5);
+    word = 0;
+    if (node > 0 && w < a.words)
+      word = a.mask[((int64_t)b * g.N + node - 1) * a.words + w];
+  };
+  // The keys t0 .. t0 + 63 that the lane's row of block nt sees, as bits
+  // (pages and the end of the positions aside).
+  auto seen = [&](int nt, int t0) __attribute__((always_inline)) {
+    const int j0 = t0 - ctx - 1;   // node of the first key
+    uint64_t see = low_bits(-j0);  // the context and the root
+    if (a.mask == nullptr) return see | low_bits(irow[nt] - j0);
+    const uint64_t lo = shfl_bits(word, 16 * nt + col);
+    const uint64_t hi = shfl_bits(word, 32 + 16 * nt + col);
+    if (j0 < 0) return j0 > -64 ? see | lo << -j0 : see;
+    const int sh = j0 & 63;
+    return lo >> sh | (sh != 0 ? hi << (64 - sh) : 0);
+  };
+
   // LDS slots of K of buffer par, followed by those of V
   constexpr int BUF = 2 * KB * SL;
   // issues the loads of this wave's rows of tile k into buffer par; returns
@@ -252,13 +278,12 @@ __device__ __forceinline__ void tiles_piece(
           on = (unsigned)table[(t0 + lane) >> g.shift] < (unsigned)g.n_pages;
         all = __ballot(on);
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        see[nt] = (seen_keys(a, b, irow[nt], rq.n, ctx, t0) & all) >>
-                  (4 * quad);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if constexpr (EDGE) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        see[nt] = (seen(nt, t0) & all) >> (4 * quad);
       // Each wave looks through the values it loaded: those of keys that do
       // not exist become 0.  A node's value that is not finite must not meet
       // the probability 0 of a row that does not see it: it is taken out
@@ -281,7 +306,10 @@ __device__ __forceinline__ void tiles_piece(
     // every wave's loads of this tile have arrived, and every wave is done
     // with the other buffer
     __syncthreads();
-    if (k + 1 < k1) holes = issue(k + 1, par ^ 1);
+    if (k + 1 < k1) {
+      load_word(k + 1);
+      holes = issue(k + 1, par ^ 1);
+    }
     if (idle) return;
     // Operands are read one group of products ahead; the barriers keep the
     // compiler from moving a group's reads back to its products.
@@ -348,6 +376,7 @@ __device__ __forceinline__ void tiles_piece(
   };
 
   __syncthreads();  // the previous piece's last tile has been read
+  load_word(k0);
   holes = issue(k0, 0);
   // (the queries' own loads are on their way as well)
   sign_queries<C>(a, qf);
