@@ -7,8 +7,6 @@ namespace pct {
 
 namespace {
 
-constexpr int kCus = 256;  // compute units of an MI355X
-
 int padded(int D) {
   return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256;
 }
@@ -20,19 +18,23 @@ struct WsLayout {
 AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   AttendPlan p{};
   p.dp = padded(D);
-  // the smallest row tile that holds a request's rows of one head
+  // The smallest row tile that holds a request's rows of one head; waves
+  // with keys of their own up to 16 rows (with 32, 64 requests of 8 rows
+  // over up to 8 k positions took 205 us, with shared tiles 166).
   const int64_t M = (int64_t)(N + 1) * (Hq / Hkv);
-  p.shared = M > 32;
-  p.nt = M <= 16 || (p.shared && M <= 64) ? 1 : 2;
+  p.shared = M > 16;
+  p.nt = M <= 64 ? 1 : 2;
   p.mt = 16 * p.nt * (p.shared ? 4 : 1);
   p.ks = p.shared ? tiles_kb(p.dp) : 4 * kRowsKb;
-  p.least = p.shared ? kTilesLeast : kRowsLeast;
   // as many runs as stay on the chip, or as the longest requests could fill
   const int64_t steps = (cap + p.ks - 1) / p.ks;
-  const int64_t units = batch * (Hkv * ((M + p.mt - 1) / p.mt) * steps);
-  const int64_t runs = (units + p.least - 1) / p.least;
+  const int64_t tiles = batch * (Hkv * ((M + p.mt - 1) / p.mt));
+  const int64_t units = tiles * steps;
+  const int few = p.shared ? kTilesFew : kRowsFew;
+  const int64_t runs = units / (steps < few ? steps : few) + 1;
   p.n_wg = kCus * (p.dp <= 128 ? 2 : 1);
   if (runs < p.n_wg) p.n_wg = (int)(runs + 7) / 8 * 8;
+  p.groups = p.mt <= 16 || p.n_wg >= 32 * tiles ? 4 : 1;
   return p;
 }
 
@@ -52,8 +54,10 @@ WsLayout layout(const AttendPlan& p) {
 // and ends in a later one: LR threads per row (4 elements each), PG groups of
 // runs side by side, kInFlight runs of a group loaded at a time:
 //   m = max_w m_w, out = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w,
-// in order of runs within a group, then of groups.  Few rows are split over
-// many runs (PG = 4), many rows over few.
+// in order of runs within a group, then of groups.  PG = 4 where rows are few
+// or split over many runs (32 rows over 60 k positions: 56 us with the
+// attention, 66 with one group), else one (512 rows over up to 5 k: 87 us,
+// 96 with four).
 constexpr int kJoinThreads = 256, kInFlight = 8;
 
 template <bool BF16>
@@ -161,7 +165,7 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
 template <bool BF16, int LR>
 hipError_t launch_join(const AttendArgs& a, const AttendPlan& p,
                        const AttendWs& ws, hipStream_t s) {
-  if (p.mt <= 32)
+  if (p.groups > 1)
     hipLaunchKernelGGL((attend_join_kernel<BF16, LR, 4>),
                        dim3(p.n_wg, p.mt / (kJoinThreads / LR / 4)),
                        dim3(kJoinThreads), 0, s, a, p, ws);

@@ -18,7 +18,7 @@
 // reads (ds_read_b64_tr_b16: 4 keys of one element per lane).
 //
 // The query rows of one key-value head are packed (row i, head g of the
-// group) -> i G + g.  Up to 32 of them are the columns of every wave, whose
+// group) -> i G + g.  Up to 16 of them are the columns of every wave, whose
 // waves take different keys (k_attend_rows.h, bound by memory); more are cut
 // into tiles whose waves share the keys (k_attend_tiles.h, bound by the
 // matrix units and the exponentials).
@@ -171,6 +171,19 @@ __device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t d) {
   return x / d;
 }
 
+// How many runs `units` units of row tiles of mostly `steps` steps are cut
+// into.  Up to LEAST steps stay together: the sums that the runs of a row
+// tile leave, and their join, would cost more.  Longer row tiles are cut
+// finely while every run has a CU of its own, and less so beyond that: two
+// runs on a CU slow each other down.
+template <int FEW, int LEAST>
+__device__ __forceinline__ int64_t runs_for(int64_t units, int steps) {
+  const int many = min(LEAST, steps), few = steps > LEAST ? FEW : many;
+  const int64_t x = div_up_to_64(units + few - 1, few);
+  const int64_t y = div_up_to_64(units, many);
+  return min(x, max(y, (int64_t)kCus));
+}
+
 // How the work is cut into runs, one per workgroup.
 //
 // Lines: the units of all requests in the order (request, head, row tile,
@@ -239,11 +252,10 @@ __device__ __forceinline__ void next_request(const AttendArgs& a,
 }
 
 // Fills in the run of this workgroup; false when it has none (its entry of
-// the join is then empty).  Runs have at least LEAST units where there are as
-// many: each costs the sums it leaves for the join.  Every wave does this by
-// itself: lane l goes through requests l per .. (l + 1) per - 1, and the
-// sums over lanes need no LDS.
-template <int MT, int KS, int LEAST>
+// the join is then empty).  Every wave does this by itself: lane l goes
+// through requests l per .. (l + 1) per - 1, and the sums over lanes need no
+// LDS.
+template <int MT, int KS, int FEW, int LEAST>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
                                                 const AttendWs& ws,
                                                 AttendRun& r, AttendReq& rq) {
@@ -253,6 +265,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   const int b0 = lane * per, b1 = min(b0 + per, g.batch);
   int64_t mine = 0, mine1 = 0;  // units of lines, of a level
   int least = 0x7fffffff, most = 0;  // row tiles of a request
+  float tiles = 0.f;                 // row tiles of all requests
   AttendReq q{};
 #pragma unroll 4
   for (int b = b0; b < b1; ++b) {
@@ -262,6 +275,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
       mine1 += (int64_t)g.Hkv * q.KT;
       least = min(least, q.RT);
       most = max(most, q.RT);
+      tiles += (float)(g.Hkv * q.RT);
     }
   }
   int64_t incl = mine, incl1 = mine1;
@@ -276,14 +290,19 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   }
   const int64_t total = last_lane(incl), total1 = last_lane(incl1);
   const int RT = wave_max(most);
+  // steps of a row tile, on average
+  const int steps = max(1, (int)((float)total / fmaxf(wave_sum(tiles), 1.f)));
   const bool same = __ballot(least != 0x7fffffff && least != RT) == 0;
   const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
   const int n_wg = gridDim.x, per_xcd = n_wg >> 3;
   // levels, if they keep at least 4 of 5 workgroups busy
   int bx = RT > 0 ? per_xcd / RT : 0;  // blocks of an XCD
-  const bool levels = RT > 1 && same && 5 * RT * bx >= 4 * per_xcd &&
-                      total1 >= 8 * LEAST;
-  bx = (int)min((int64_t)bx, total1 / (8 * LEAST));
+  const int fit =
+      RT > 0 ? (int)min((int64_t)n_wg, runs_for<FEW, LEAST>(
+                                           RT * total1, steps)) / (8 * RT)
+             : 0;
+  const bool levels = RT > 1 && same && 5 * RT * bx >= 4 * per_xcd && fit > 0;
+  bx = min(bx, fit);
   int n_run, xcount;  // runs, and runs of this XCD
   if (levels) {
     n_run = 8 * RT * bx;
@@ -300,7 +319,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     mine = mine1;
   } else {
     // neighbouring runs on one XCD (workgroups go round the 8 XCDs)
-    n_run = (int)min((int64_t)n_wg, total < LEAST ? total : total / LEAST);
+    n_run = (int)min((int64_t)n_wg, runs_for<FEW, LEAST>(total, steps));
     xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
     r.level = -1;
     r.run = xcd * (n_run >> 3) + min(xcd, n_run & 7) + at;

@@ -15,12 +15,9 @@ hipError_t launch_attend_type(const AttendArgs& a, const AttendPlan& p,
   else if (p.shared)
     hipLaunchKernelGGL((attend_tiles_kernel<TilesCfg<DP, 2, BF16>>), grid,
                        block, 0, s, a, ws);
-  else if (p.nt == 1)
-    hipLaunchKernelGGL((attend_rows_kernel<RowsCfg<DP, 1, BF16>>), grid,
-                       block, 0, s, a, ws);
   else
-    hipLaunchKernelGGL((attend_rows_kernel<RowsCfg<DP, 2, BF16>>), grid,
-                       block, 0, s, a, ws);
+    hipLaunchKernelGGL((attend_rows_kernel<RowsCfg<DP, BF16>>), grid, block,
+                       0, s, a, ws);
   return hipGetLastError();
 }
 

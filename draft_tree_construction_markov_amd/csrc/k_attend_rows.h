@@ -1,5 +1,5 @@
-// k_attend_rows.h -- attention of at most 32 packed rows per key-value head
-// (plain decoding, short drafts): each of a workgroup's 4 waves holds all rows
+// k_attend_rows.h -- attention of at most 16 packed rows per key-value head
+// (plain decoding, short chains): each of a workgroup's 4 waves holds all rows
 // and takes its own key tiles, so nothing in the loop waits for another wave;
 // the four sums are joined through LDS at the end of a run.  Bound by the
 // cache's read: a tile's 16-byte pieces are loaded into registers one tile
@@ -10,10 +10,10 @@
 
 namespace pct {
 
-template <int DP_, int NT_, bool BF16_>
+template <int DP_, bool BF16_>
 struct RowsCfg {
   static constexpr int DP = DP_;  // head size, padded
-  static constexpr int NT = NT_;  // 16-row blocks
+  static constexpr int NT = 1;     // 16-row blocks
   static constexpr bool BF16 = BF16_;
   static constexpr int KB = kRowsKb;  // keys of a wave's tile
   static constexpr int DT = DP / 16, KSTEP = DP / 32;
@@ -32,7 +32,7 @@ struct RowsCfg {
   static constexpr int LDS_DUMP = 4 * MT * DROW * 4;
   static constexpr int LDS = LDS_TILES > LDS_DUMP ? LDS_TILES : LDS_DUMP;
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
-  static constexpr int LEAST = kRowsLeast;  // steps of a run
+  static constexpr int FEW = kRowsFew, LEAST = kRowsLeast;  // of a run
 };
 
 // 16 bytes that nothing reads again soon
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 
   AttendRun run;
   AttendReq rq;
-  if (!attend_schedule<C::MT, C::KS, C::LEAST>(a, ws, run, rq)) return;
+  if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST>(a, ws, run, rq)) return;
   int4 join = make_int4(0, 0, 0, -1);
 
   const uint4* kc = static_cast<const uint4*>(a.kc);

@@ -1,4 +1,4 @@
-// k_attend_tiles.h -- attention of more than 32 packed rows per key-value
+// k_attend_tiles.h -- attention of more than 16 packed rows per key-value
 // head (draft trees, pieces of prompts): the 4 waves of a workgroup hold 16 NT
 // rows each and share every key tile.  Tiles go from the cache straight to
 // LDS (16-byte direct loads) into two buffers, so the next tile's loads are
@@ -35,7 +35,7 @@ struct TilesCfg {
   static constexpr int GPS = KB / 8;        // 8-key groups of a tile
   static constexpr int TPV = 64 / GPS;      // tiles whose pages fit a wave
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
-  static constexpr int LEAST = kTilesLeast;  // tiles of a run
+  static constexpr int FEW = kTilesFew, LEAST = kTilesLeast;  // of a run
   static __device__ __forceinline__ int swizzle_k(int r) {
     return SL == 8 ? (r >> 1) & 7 : r & 15;
   }
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
 
   AttendRun run;
   AttendReq rq;
-  if (!attend_schedule<MT, KB, C::LEAST>(a, ws, run, rq)) return;
+  if (!attend_schedule<MT, KB, C::FEW, C::LEAST>(a, ws, run, rq)) return;
   int4 join = make_int4(0, 0, 0, -1);
   if ((a.g.D >> 3) < SL) {
     // slots past the head size are read and never loaded

@@ -70,17 +70,21 @@ struct AttendArgs {
 };
 // Tile of a call: heads padded to dp elements, nt 16-row blocks per wave, the
 // waves share their keys (and hold different rows) or not, mt rows per
-// workgroup, steps of ks keys, runs of `least` steps at least, n_wg runs at
-// most (a multiple of 8).
+// workgroup, steps of ks keys, n_wg runs at most (a multiple of 8), joined in
+// so many groups side by side.
 struct AttendPlan {
-  int dp, nt, shared, mt, ks, least, n_wg;
+  int dp, nt, shared, mt, ks, n_wg, groups;
 };
 // Keys of a tile: of a wave's own one, of one that the waves share (32 where
 // 64 would leave no room for two buffers twice on a CU).
 constexpr int kRowsKb = 32;
 constexpr int tiles_kb(int dp) { return dp <= 128 ? 64 : 32; }
-// Steps of a run at least.  LEAST_NOTE
-constexpr int kRowsLeast = 1, kTilesLeast = 6;
+// Steps of a run at least while runs are few, and beyond (runs_for).  Shared
+// tiles, 65 rows over 4066 positions, from 3, 4, 5, 6 steps on: 43, 44, 41,
+// 39 us; over 566 positions, from 6 or from 2 steps on: 28 or 23 us.  Runs of
+// the rows kernel leave a few rows of sums only.
+constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2, kTilesLeast = 6;
+constexpr int kCus = 256;  // compute units of an MI355X
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
 // end; meta {request, head, row tile, last run} of the latter, w < 0: none.
