@@ -33,12 +33,22 @@ __device__ __forceinline__ int64_t pages_for(int64_t tokens, int shift) {
   return (tokens + ((1 << shift) - 1)) >> shift;
 }
 
-// inclusive prefix sums of two values over the workgroup
+// x / d and x % d for x >= 0, d > 0; both mostly fit 32 bits, where the
+// division is several times shorter.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
+  if (((x | d) >> 32) == 0) return (uint32_t)x / (uint32_t)d;
+  return x / d;
+}
+__device__ __forceinline__ int64_t remainder_of(int64_t x, int64_t d) {
+  return x - quotient(x, d) * d;
+}
+
+// inclusive prefix sums of two values over the first n threads
 __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b,
-                                            int64_t (*sum)[2], int tid) {
+                                            int64_t (*sum)[2], int tid,
+                                            int n) {
   const int lane = tid & 63, wave = tid >> 6;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
+  for (int d = 1; d < kWave && d < n; d <<= 1) {
     const int64_t x = __shfl_up(a, d, kWave), y = __shfl_up(b, d, kWave);
     if (lane >= d) {
       a += x;
@@ -50,7 +60,7 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b,
     sum[wave][1] = b;
   }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
+  for (int w = 0; w < wave && wave * kWave < n; ++w) {
     a += sum[w][0];
     b += sum[w][1];
   }
@@ -62,7 +72,8 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
   const int tid = threadIdx.x;
   const PageGeom& g = a.g;
   const int head0 = a.ring_state[0], count0 = a.ring_state[1];
-  const int head = ((head0 % g.n_pages) + g.n_pages) % g.n_pages;
+  int head = head0 % g.n_pages;
+  head += head < 0 ? g.n_pages : 0;
   const int count = min(max(count0, 0), g.n_pages);
   if (tid == 0) total[0] = total[1] = total[2] = 0;
   for (int b0 = 0; b0 < g.batch; b0 += kScanThreads) {
@@ -79,7 +90,7 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
     const int to = (int)min(need, (int64_t)g.max_pages);
     const int64_t want = max(to - held, 0), back = max(held - to, 0);
     int64_t wi = want, bi = back;
-    block_scan2(wi, bi, sum, tid);
+    block_scan2(wi, bi, sum, tid, min(kScanThreads, g.batch - b0));
     wi += total[0];
     bi += total[1];
     const bool fits = wi <= count;
@@ -87,13 +98,14 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
     if (in) {
       const int after = fits ? to : min(held, to);
       // (offsets into the ring; the first is used only where it fits)
-      a.req[b] = make_int4((int)(wi - want), (int)((bi - back) % g.n_pages),
-                           held, after);
+      a.req[b] = make_int4((int)(wi - want),
+                           (int)remainder_of(bi - back, g.n_pages), held,
+                           after);
       a.held[b] = after;
       a.missing[b] = (int)(need - after);
       // the last request that is served has the largest sum
-      if (fits) atomicMax((unsigned long long*)&total[2],
-                          (unsigned long long)wi);
+      if (fits && (tid & 63) == 63 - __builtin_clzll(__ballot(fits)))
+        atomicMax((unsigned long long*)&total[2], (unsigned long long)wi);
       if (b == g.batch - 1 || tid == kScanThreads - 1) {
         total[0] = wi;
         total[1] = bi;
@@ -103,7 +115,7 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
   __syncthreads();
   if (tid == 0) {
     a.ring0[0] = make_int2(head, count);
-    a.ring_state[0] = (int)((head + total[2]) % g.n_pages);
+    a.ring_state[0] = (int)remainder_of(head + total[2], g.n_pages);
     a.ring_state[1] = (int)min(count - total[2] + total[1],
                                (int64_t)g.n_pages);
   }
@@ -133,7 +145,7 @@ __device__ __forceinline__ void plan_apply(const PlanArgs& a, int b, int r0,
         // may not hold them yet
         const int page =
             j < held ? table[j]
-                     : a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
+                     : a.ring[remainder_of((int64_t)ring0.x + rq.x + j - held, P)];
         if (page >= 0 && page < P)
           s = ((int64_t)page << g.shift) + (p & page_mask);
       }
@@ -144,9 +156,11 @@ __device__ __forceinline__ void plan_apply(const PlanArgs& a, int b, int r0,
   }
   if (r0 == 0) {
     for (int j = held + tid; j < after; j += THREADS)
-      table[j] = a.ring[((int64_t)ring0.x + rq.x + j - held) % P];
+      table[j] =
+          a.ring[remainder_of((int64_t)ring0.x + rq.x + j - held, P)];
     for (int j = after + tid; j < held; j += THREADS) {
-      a.ring[((int64_t)ring0.x + ring0.y + rq.y + j - after) % P] = table[j];
+      a.ring[remainder_of((int64_t)ring0.x + ring0.y + rq.y + j - after, P)] =
+          table[j];
       table[j] = -1;
     }
   }
@@ -193,7 +207,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
   const int64_t total = a.rows * rc;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / rc;
+    const int64_t row = quotient(i, rc);
     const int c = (int)(i - row * rc);
     const int64_t slot = a.slot[row];
     if (slot < 0 || slot >= a.n_slots) continue;
