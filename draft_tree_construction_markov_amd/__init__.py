@@ -11,6 +11,7 @@ Build it with ``python -m draft_tree_construction_markov_amd.build``.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -524,6 +525,12 @@ def _want(name, t, dtype, shape, dev):
                      f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
+@functools.lru_cache(maxsize=64)
+def _shape_ref(*fields):
+    """A reference to the shape structure of these fields (read only)."""
+    return C.byref(CacheShape(*fields))
+
+
 def _rows(name, t, dtype, shape, dev):
     """Check rows [batch][R][heads][D] whose heads are contiguous and whose
     rows are evenly spaced (a joint projection's view); returns the address
@@ -632,11 +639,11 @@ def cache_write(k, v, slot, k_cache, v_cache):
     batch, R = slot.shape
     dt = k_cache.dtype
     rows = (batch, R, Hkv, D)
-    sh = CacheShape(batch, R - 1, n_pages, page, 1, Hkv, Hkv, D,
+    sh = _shape_ref(batch, R - 1, n_pages, page, 1, Hkv, Hkv, D,
                     _cache_dtype(dt))
     kp, ks = _rows("k", k, dt, rows, dev)
     vp, vs = _rows("v", v, dt, rows, dev)
-    _enqueue(lib().pct_cache_write, dev, C.byref(sh), kp, ks, vp, vs,
+    _enqueue(lib().pct_cache_write, dev, sh, kp, ks, vp, vs,
              _want("slot", slot, torch.int64, (batch, R), dev),
              _want("k_cache", k_cache, dt, cache, dev),
              _want("v_cache", v_cache, dt, cache, dev))
@@ -730,9 +737,9 @@ def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
         out = torch.empty_like(ctx_len)
     # the rows are not read: any number of nodes up to the largest may be
     # accepted
-    sh = CacheShape(batch, 8192, n_pages, page, width, Hkv, Hkv, D,
+    sh = _shape_ref(batch, 8192, n_pages, page, width, Hkv, Hkv, D,
                     _cache_dtype(dt))
-    _enqueue(lib().pct_cache_commit, dev, C.byref(sh), layers,
+    _enqueue(lib().pct_cache_commit, dev, sh, layers,
              n_pages * Hkv * page * D, B, _want("tau", tau, i32, one, dev),
              _want("accept_node", accept_node, i32, (batch, B), dev),
              None if n_nodes is None else
