@@ -28,13 +28,19 @@ AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   p.ks = p.shared ? tiles_kb(p.dp) : 4 * kRowsKb;
   // as many runs as stay on the chip, or as the longest requests could fill
   const int64_t steps = (cap + p.ks - 1) / p.ks;
-  const int64_t tiles = batch * (Hkv * ((M + p.mt - 1) / p.mt));
-  const int64_t units = tiles * steps;
+  const int64_t row_tiles = (M + p.mt - 1) / p.mt;
+  const int64_t tiles = batch * (Hkv * row_tiles);
+  // (bounded, so that no shape overflows it)
+  const int64_t units = (tiles < 1 << 30 ? tiles : 1 << 30) * steps;
   const int few = p.shared ? kTilesFew : kRowsFew;
   const int64_t runs = units / (steps < few ? steps : few) + 1;
   p.n_wg = kCus * (p.dp <= 128 ? 2 : 1);
   if (runs < p.n_wg) p.n_wg = (int)(runs + 7) / 8 * 8;
-  p.groups = p.mt <= 16 || p.n_wg >= 32 * tiles ? 4 : 1;
+  if (tiles <= p.n_wg) {
+    p.row_tiles = (int)row_tiles;
+    p.tiles = (int)tiles;
+  }
+  p.groups = p.mt <= 16 || p.n_wg >= 16 * tiles ? 4 : 1;
   return p;
 }
 
@@ -50,8 +56,8 @@ WsLayout layout(const AttendPlan& p) {
 
 }  // namespace
 
-// A workgroup adds up ROWS rows of a row tile that starts in run blockIdx.x
-// and ends in a later one: LR threads per row (4 elements each), PG groups of
+// A workgroup adds up ROWS rows of a row tile that starts in one run and ends
+// in a later one: LR threads per row (4 elements each), PG groups of
 // runs side by side, kInFlight runs of a group loaded at a time:
 //   m = max_w m_w, out = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w,
 // in order of runs within a group, then of groups.  PG = 4 where rows are few
@@ -101,12 +107,20 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
   __shared__ float4 o_s[PG > 1 ? kJoinThreads : 1];
   __shared__ float2 ml_s[PG > 1 ? kJoinThreads : 1];
   const PageGeom& g = a.g;
-  const int run = blockIdx.x;
-  const int4 seg = ws.meta[run];
-  if (seg.w < 0) return;
-  const int b = seg.x, h = seg.y, rt = seg.z;
-  const int runs = seg.w - run + 1;
+  const int4 seg = ws.meta[blockIdx.x];
+  int b = seg.x, h = seg.y >> 20, rt = seg.y & 0xfffff;
+  if (p.row_tiles > 0) {
+    // entries of row tiles that the request does not have are not written
+    h = blockIdx.x / p.row_tiles;
+    rt = blockIdx.x - h * p.row_tiles;
+    b = h / g.Hkv;
+    h -= b * g.Hkv;
+  } else if (seg.w < 0) {
+    return;
+  }
   const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+  if (rt * p.mt >= (n + 1) * a.G || seg.w < 0) return;
+  const int run = seg.z, runs = seg.w - run + 1;
   const int tid = threadIdx.x;
   const int c = tid % LR, pg = tid / (LR * ROWS);
   const int r = blockIdx.y * ROWS + tid / LR % ROWS;
@@ -165,13 +179,14 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
 template <bool BF16, int LR>
 hipError_t launch_join(const AttendArgs& a, const AttendPlan& p,
                        const AttendWs& ws, hipStream_t s) {
+  const int x = p.row_tiles > 0 ? p.tiles : p.n_wg;
   if (p.groups > 1)
     hipLaunchKernelGGL((attend_join_kernel<BF16, LR, 4>),
-                       dim3(p.n_wg, p.mt / (kJoinThreads / LR / 4)),
+                       dim3(x, p.mt / (kJoinThreads / LR / 4)),
                        dim3(kJoinThreads), 0, s, a, p, ws);
   else
     hipLaunchKernelGGL((attend_join_kernel<BF16, LR, 1>),
-                       dim3(p.n_wg, p.mt / (kJoinThreads / LR)),
+                       dim3(x, p.mt / (kJoinThreads / LR)),
                        dim3(kJoinThreads), 0, s, a, p, ws);
   return hipGetLastError();
 }
@@ -200,7 +215,7 @@ hipError_t launch_tree_attention(const AttendArgs& a, void* workspace,
   char* base = static_cast<char*>(workspace);
   AttendWs ws{reinterpret_cast<float*>(base + w.o),
               reinterpret_cast<float2*>(base + w.ml),
-              reinterpret_cast<int4*>(base + w.meta)};
+              reinterpret_cast<int4*>(base + w.meta), p.row_tiles};
   hipError_t e;
   {
     ProfScope ps(PROF_ATTEND, (int64_t)g.batch * (g.N + 1), s);

@@ -36,6 +36,7 @@
 namespace pct {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -155,14 +156,11 @@ __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
   return attend_lengths<MT, KS>(a, ctx, n);
 }
 
-// a 64-bit value of lane l, of the last lane
+// a 64-bit value of lane l
 __device__ __forceinline__ int64_t lane_value(int64_t x, int l) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, l);
   const uint32_t hi = __builtin_amdgcn_readlane((int)(x >> 32), l);
   return (int64_t)((uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ int64_t last_lane(int64_t x) {
-  return lane_value(x, kWave - 1);
 }
 
 // x / d for x >= 0, d > 0, which mostly fit 32 bits.
@@ -279,8 +277,10 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     }
   }
   int64_t incl = mine, incl1 = mine1;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
+  // (lane `lanes` - 1 is the last one with requests)
+  const int lanes = min(g.batch, kWave);
+#pragma unroll 1
+  for (int d = 1; d < lanes; d <<= 1) {
     const int64_t x = __shfl_up(incl, d, kWave);
     const int64_t y = __shfl_up(incl1, d, kWave);
     if (lane >= d) {
@@ -288,7 +288,8 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
       incl1 += y;
     }
   }
-  const int64_t total = last_lane(incl), total1 = last_lane(incl1);
+  const int64_t total = lane_value(incl, lanes - 1);
+  const int64_t total1 = lane_value(incl1, lanes - 1);
   const int RT = wave_max(most);
   // steps of a row tile, on average
   const int steps = max(1, (int)((float)total / fmaxf(wave_sum(tiles), 1.f)));
@@ -329,6 +330,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     r.end = r.start(r.run + 1);
   }
   if (at >= xcount) {  // no run
+    if (ws.row_tiles > 0) return false;
     int before = 0;    // such workgroups of the XCDs before this one
     for (int x = 0; x < xcd; ++x)
       before += per_xcd - (r.level >= 0 ? xcount
@@ -352,6 +354,28 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     next_request<MT, KS>(a, r, rq);
   }
   return true;
+}
+
+__device__ __forceinline__ void store_meta(const AttendWs& ws, int at,
+                                           i32x4 x) {
+  reinterpret_cast<i32x4*>(ws.meta)[at] = x;
+}
+
+// Notes for the join that the run has the piece pc.
+__device__ __forceinline__ void note_piece(const AttendArgs& a,
+                                           const AttendWs& ws,
+                                           const AttendRun& run,
+                                           const AttendReq& rq,
+                                           const AttendPiece& pc,
+                                           i32x4& join) {
+  if (pc.k0 != 0) return;
+  // the join adds the runs up to the one that holds the last step
+  const int last = pc.k1 < rq.KT ? run.owner(pc.s0 + rq.KT - 1) : -1;
+  const i32x4 j = {run.b, pc.h << 20 | pc.rt, run.run, last};
+  if (ws.row_tiles == 0)
+    join = j;
+  else if (threadIdx.x == 0)
+    store_meta(ws, (run.b * a.g.Hkv + pc.h) * ws.row_tiles + pc.rt, j);
 }
 
 // Query rows m0 + 16 nt + lane % 16 as B operands, as they are;

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   AttendRun run;
   AttendReq rq;
   if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST>(a, ws, run, rq)) return;
-  int4 join = make_int4(0, 0, 0, -1);
+  i32x4 join = {0, 0, 0, -1};
 
   const uint4* kc = static_cast<const uint4*>(a.kc);
   const uint4* vc = static_cast<const uint4*>(a.vc);
@@ -117,6 +117,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     load_pages(k0);
     load_rows(k0);
     if (k0 + 1 < k1) load_pages(k0 + 1);
+    note_piece(a, ws, run, rq, pc, join);  // (while these are on their way)
 
     for (int k = k0; k < k1; ++k) {
       const int t0 = tile_t0(k);
@@ -275,14 +276,10 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
         if (c == 0) part_ml[r] = make_float2(top, sum);
       }
     }
-    if (!whole && k0 == 0) {
-      // the join adds the runs up to the one that holds the last step
-      join = make_int4(b, h, rt, run.owner(pc.s0 + rq.KT - 1));
-    }
     __syncthreads();
     run.u += pc.k1 - pc.k0;
   }
-  if (tid == 0) ws.meta[run.run] = join;
+  if (tid == 0 && ws.row_tiles == 0) store_meta(ws, run.run, join);
 }
 
 }  // namespace pct

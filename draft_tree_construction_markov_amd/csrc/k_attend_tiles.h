@@ -17,8 +17,6 @@
 
 namespace pct {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
 template <int DP_, int NT_, bool BF16_>
 struct TilesCfg {
   static constexpr int DP = DP_;  // head size, padded
@@ -441,7 +439,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
   AttendRun run;
   AttendReq rq;
   if (!attend_schedule<MT, KB, C::FEW, C::LEAST>(a, ws, run, rq)) return;
-  int4 join = make_int4(0, 0, 0, -1);
+  i32x4 join = {0, 0, 0, -1};
   if ((a.g.D >> 3) < SL) {
     // slots past the head size are read and never loaded
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -458,12 +456,10 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
     const int k1 = __builtin_amdgcn_readfirstlane(pc.k1);
     tiles_piece<C>(a, ws, rq, b, h, m0, k0, k1, 2 * run.run + (k0 == 0),
                    tiles, odd_s);
-    // the join adds the runs up to the one that holds the last step
-    if (k0 == 0 && k1 < rq.KT)
-      join = make_int4(b, h, pc.rt, run.owner(pc.s0 + rq.KT - 1));
+    note_piece(a, ws, run, rq, pc, join);
     run.u += pc.k1 - pc.k0;
   }
-  if (threadIdx.x == 0) ws.meta[run.run] = join;
+  if (threadIdx.x == 0 && ws.row_tiles == 0) store_meta(ws, run.run, join);
 }
 
 }  // namespace pct

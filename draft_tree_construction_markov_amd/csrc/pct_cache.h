@@ -70,10 +70,12 @@ struct AttendArgs {
 };
 // Tile of a call: heads padded to dp elements, nt 16-row blocks per wave, the
 // waves share their keys (and hold different rows) or not, mt rows per
-// workgroup, steps of ks keys, n_wg runs at most (a multiple of 8), joined in
-// so many groups side by side.
+// workgroup, steps of ks keys, n_wg runs at most (a multiple of 8); the join
+// goes through the `tiles` row tiles (row_tiles of a request at most), or
+// through the runs where these are fewer (row_tiles 0), and adds so many
+// groups of runs side by side.
 struct AttendPlan {
-  int dp, nt, shared, mt, ks, n_wg, groups;
+  int dp, nt, shared, mt, ks, n_wg, row_tiles, tiles, groups;
 };
 // Keys of a tile: of a wave's own one, of one that the waves share (32 where
 // 64 would leave no room for two buffers twice on a CU).
@@ -87,11 +89,14 @@ constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2, kTilesLeast = 6;
 constexpr int kCus = 256;  // compute units of an MI355X
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
-// end; meta {request, head, row tile, last run} of the latter, w < 0: none.
+// end.  meta {request, head << 20 | row tile, first run, last run} of a row
+// tile that is cut, w < 0: it is not; its index is the row tile's if
+// row_tiles > 0, else the first run's.
 struct AttendWs {
   float* o;    // [2 n_wg][mt][dp]
   float2* ml;  // [2 n_wg][mt] {m, sum}
   int4* meta;  // [n_wg]
+  int row_tiles;
 };
 hipError_t launch_attend_d64(const AttendArgs&, const AttendPlan&,
                              const AttendWs&, hipStream_t);
