@@ -170,13 +170,15 @@ __device__ __forceinline__ int64_t div_up_to_64(int64_t x, int64_t d) {
 }
 
 // How many runs `units` units of row tiles of mostly `steps` steps are cut
-// into.  Up to LEAST steps stay together: the sums that the runs of a row
-// tile leave, and their join, would cost more.  Longer row tiles are cut
-// finely while every run has a CU of its own, and less so beyond that: two
-// runs on a CU slow each other down.
+// into.  Up to kWhole steps of shared tiles stay together: the sums that the
+// runs of a row tile leave, and their join, would cost more (2 requests of
+// 256 rows over 306 positions: 26 us, cut at 4 of their 5 steps 33).  Longer
+// row tiles are cut finely while every run has a CU of its own, and less so
+// beyond that: two runs on a CU slow each other down.
 template <int FEW, int LEAST>
 __device__ __forceinline__ int64_t runs_for(int64_t units, int steps) {
-  const int many = min(LEAST, steps), few = steps > LEAST ? FEW : many;
+  const bool whole = steps <= kWhole && LEAST > 1;
+  const int few = whole ? steps : FEW, many = whole ? steps : LEAST;
   const int64_t x = div_up_to_64(units + few - 1, few);
   const int64_t y = div_up_to_64(units, many);
   return min(x, max(y, (int64_t)kCus));

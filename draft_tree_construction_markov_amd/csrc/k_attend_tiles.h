@@ -33,7 +33,7 @@ struct TilesCfg {
   static constexpr int GPS = KB / 8;        // 8-key groups of a tile
   static constexpr int TPV = 64 / GPS;      // tiles whose pages fit a wave
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
-  static constexpr int FEW = kTilesFew, LEAST = kTilesLeast;  // of a run
+  static constexpr int FEW = kTilesFew, LEAST = tiles_least(NT);  // of a run
   static __device__ __forceinline__ int swizzle_k(int r) {
     return SL == 8 ? (r >> 1) & 7 : r & 15;
   }

@@ -82,10 +82,13 @@ struct AttendPlan {
 constexpr int kRowsKb = 32;
 constexpr int tiles_kb(int dp) { return dp <= 128 ? 64 : 32; }
 // Steps of a run at least while runs are few, and beyond (runs_for).  Shared
-// tiles, 65 rows over 4066 positions, from 3, 4, 5, 6 steps on: 43, 44, 41,
-// 39 us; over 566 positions, from 6 or from 2 steps on: 28 or 23 us.  Runs of
-// the rows kernel leave a few rows of sums only.
-constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2, kTilesLeast = 6;
+// tiles of 128 rows, 65 rows of 4 heads over 4066 positions, from 3, 4, 6
+// steps on: 35, 29, 34 us; of 64 rows, 4 requests of 16 rows over up to
+// 5 k positions, from 4, 6 on: 28, 25 us; 16 rows over 1 k, from 6 or from 2
+// steps on: 20 or 14 us.  Runs of the rows kernel leave a few rows only.
+constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2;
+constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
+constexpr int tiles_least(int nt) { return nt == 1 ? 6 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
