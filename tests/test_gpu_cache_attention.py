@@ -309,3 +309,74 @@ def test_cache_offsets_past_32_bits():
     out, lse = h.run(q, *big, moved, ctx, n, mask=mask)
     torch.cuda.synchronize()
     compare(c, out, lse)
+
+
+@pytest.mark.parametrize("D", [80, 192, 256])
+@pytest.mark.parametrize("N,ctx", [(70, [0, 200]), (150, [63, 5]),
+                                   (129, [31, 700])])
+def test_large_trees_of_other_heads(D, N, ctx):
+    check(Case(D + N, 2, N, 4, 2, D, 16, ctx, n=[N, N - 7]))
+
+
+@pytest.mark.parametrize("N,G", [(4, 4), (16, 1), (7, 4), (10, 3), (8, 4),
+                                 (15, 4), (16, 4)])
+@pytest.mark.parametrize("chain", [False, True])
+def test_rows_around_the_bounds_of_the_tiles(N, G, chain):
+    check(Case(N * G, 3, N, 2 * G, 2, 128, 16, [2001, 31, 700],
+               n=[N, N // 2, N], chain=chain))
+
+
+@pytest.mark.parametrize("batch,N,Hq,Hkv,hi", [
+    (3, 90, 8, 2, 900),      # fewer row tiles than runs
+    (40, 40, 32, 8, 60),     # more
+    (3, 3, 4, 2, 3000)])     # few rows
+def test_workspace_may_hold_anything(batch, N, Hq, Hkv, hi):
+    # lengths change from call to call, and with them the row tiles that a
+    # request has and those that are cut
+    rng = np.random.default_rng(batch + N)
+    h = None
+    for turn in range(3):
+        c = Case(71 + turn, batch, N, Hq, Hkv, 64, 16,
+                 rng.integers(0, hi, batch),
+                 n=rng.integers(-1, N + 1, batch))
+        q, k, v, table, ctx, n, mask = device_args(c)
+        new = handle(c)
+        if h is not None and h.ws.numel() >= new.ws.numel():
+            new.ws.copy_(h.ws[:new.ws.numel()])  # what the last call left
+        else:
+            new.ws.random_(0, 256)
+        h = new
+        announce("workspace", (batch, N, turn))
+        out, lse = h.run(q, k, v, table, ctx, n, mask=mask)
+        torch.cuda.synchronize()
+        compare(c, out, lse)
+        out.zero_(), lse.zero_()
+        h.ws.random_(0, 256)
+        h.run(q, k, v, table, ctx, n, mask=mask)
+        torch.cuda.synchronize()
+        compare(c, out, lse)
+
+
+def test_values_that_are_not_finite_in_large_trees():
+    # nodes in several key tiles, shared tiles of 128 rows
+    c = Case(81, 1, 180, 8, 2, 128, 16, [45])
+    bad = [0, 30, 77, 150]
+    for i in bad:
+        t = 46 + i
+        c.v[c.table[0, t // 16], :, t % 16, 64:70] = math.inf
+    want = c.want()
+    reached = c.anc[0][:, bad].any(-1)
+    assert reached.any() and not reached.all()
+    h = handle(c)
+    q, k, v, table, ctx, n, mask = device_args(c)
+    announce("not finite, large tree")
+    out, lse = h.run(q, k, v, table, ctx, n, mask=mask)
+    torch.cuda.synchronize()
+    got = out[0, 1:].double().cpu().numpy()
+    o, tol = want[0][0, 1:], want[2][0, 1:]
+    at = np.zeros(128, bool)
+    at[64:70] = True
+    assert (np.abs(got - o)[~reached] <= tol[~reached]).all()
+    assert np.isinf(got[reached][:, :, at]).all()
+    assert (np.abs(got - o)[reached][:, :, ~at] <=
+            tol[reached][:, :, ~at]).all()
