@@ -1,5 +1,7 @@
 // k_attend.hip -- tree attention: the choice of tile, the workspace and the
 // join of row tiles whose keys were split over workgroups.
+#include <type_traits>
+
 #include "pct_cache.h"
 #include "pct_device.h"
 
@@ -127,26 +129,33 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
   const int m = rt * p.mt + r;
   const bool live = m < (n + 1) * a.G && 4 * c < g.D;
   JoinSum s{neg_inf(), 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  auto add_runs = [&](auto count, int x0) __attribute__((always_inline)) {
+    constexpr int IN = decltype(count)::value;
+    float2 ml[IN];
+    float4 o[IN];
+#pragma unroll
+    for (int k = 0; k < IN; ++k) {
+      // (past the last run: that one again, without weight)
+      const int x = min(x0 + k * PG, runs - 1);
+      const int64_t row =
+          (int64_t)(2 * (run + x) + (x == 0 ? 1 : 0)) * p.mt + r;
+      ml[k] = ws.ml[row];
+      o[k] = reinterpret_cast<const float4*>(ws.o + row * p.dp)[c];
+    }
+    float m2 = s.m;
+#pragma unroll
+    for (int k = 0; k < IN; ++k) m2 = fmaxf(m2, ml[k].x);
+    s.scale(m2);
+#pragma unroll
+    for (int k = 0; k < IN; ++k)
+      if (x0 + k * PG < runs) s.add(ml[k], o[k]);
+  };
   if (live) {
-    for (int x0 = pg; x0 < runs; x0 += kInFlight * PG) {
-      float2 ml[kInFlight];
-      float4 o[kInFlight];
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        // (past the last run: that one again, without weight)
-        const int x = min(x0 + k * PG, runs - 1);
-        const int64_t row =
-            (int64_t)(2 * (run + x) + (x == 0 ? 1 : 0)) * p.mt + r;
-        ml[k] = ws.ml[row];
-        o[k] = reinterpret_cast<const float4*>(ws.o + row * p.dp)[c];
-      }
-      float m2 = s.m;
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) m2 = fmaxf(m2, ml[k].x);
-      s.scale(m2);
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k)
-        if (x0 + k * PG < runs) s.add(ml[k], o[k]);
+    if (runs <= 2 * PG) {
+      if (pg < runs) add_runs(std::integral_constant<int, 2>{}, pg);
+    } else {
+      for (int x0 = pg; x0 < runs; x0 += kInFlight * PG)
+        add_runs(std::integral_constant<int, kInFlight>{}, x0);
     }
   }
   if constexpr (PG > 1) {
