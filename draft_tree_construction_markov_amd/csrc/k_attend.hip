@@ -24,17 +24,16 @@ AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   // with keys of their own up to 16 rows (with 32, 64 requests of 8 rows
   // over up to 8 k positions took 205 us, with shared tiles 166).
   const int64_t M = (int64_t)(N + 1) * (Hq / Hkv);
-  p.shared = M > 16;
-  p.nt = M <= 64 ? 1 : 2;
-  p.mt = 16 * p.nt * (p.shared ? 4 : 1);
-  p.ks = p.shared ? tiles_kb(p.dp) : 4 * kRowsKb;
+  p.mt = M <= 16 ? 16 : M <= 64 ? 64 : 128;
+  const bool shared = p.mt > 16;
+  p.ks = shared ? kTilesKb : 4 * kRowsKb;
   // as many runs as stay on the chip, or as the longest requests could fill
   const int64_t steps = (cap + p.ks - 1) / p.ks;
   const int64_t row_tiles = (M + p.mt - 1) / p.mt;
   const int64_t tiles = batch * (Hkv * row_tiles);
   // (bounded, so that no shape overflows it)
   const int64_t units = (tiles < 1 << 30 ? tiles : 1 << 30) * steps;
-  const int few = p.shared ? kTilesFew : kRowsFew;
+  const int few = shared ? kTilesFew : kRowsFew;
   const int64_t runs = units / (steps < few ? steps : few) + 1;
   p.n_wg = kCus * (p.dp <= 128 ? 2 : 1);
   if (runs < p.n_wg) p.n_wg = (int)(runs + 7) / 8 * 8;

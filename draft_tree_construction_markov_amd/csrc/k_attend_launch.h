@@ -9,12 +9,14 @@ template <int DP, bool BF16>
 hipError_t launch_attend_type(const AttendArgs& a, const AttendPlan& p,
                               const AttendWs& ws, hipStream_t s) {
   const dim3 grid(p.n_wg), block(256);
-  if (p.shared && p.nt == 1)
-    hipLaunchKernelGGL((attend_tiles_kernel<TilesCfg<DP, 1, BF16>>), grid,
-                       block, 0, s, a, ws);
-  else if (p.shared)
-    hipLaunchKernelGGL((attend_tiles_kernel<TilesCfg<DP, 2, BF16>>), grid,
-                       block, 0, s, a, ws);
+  using Half = TilesCfg<DP, 64, BF16>;
+  using Full = TilesCfg<DP, 128, BF16>;
+  if (p.mt == 64)
+    hipLaunchKernelGGL((attend_tiles_kernel<Half>), grid, dim3(64 * Half::W),
+                       0, s, a, ws);
+  else if (p.mt == 128)
+    hipLaunchKernelGGL((attend_tiles_kernel<Full>), grid, dim3(64 * Full::W),
+                       0, s, a, ws);
   else
     hipLaunchKernelGGL((attend_rows_kernel<RowsCfg<DP, BF16>>), grid, block,
                        0, s, a, ws);

@@ -1,6 +1,6 @@
 // k_attend_tiles.h -- attention of more than 16 packed rows per key-value
-// head (draft trees, pieces of prompts): the 4 waves of a workgroup hold 16 NT
-// rows each and share every key tile.  Tiles go from the cache straight to
+// head (draft trees, pieces of prompts): the W waves of a workgroup hold 16
+// NT rows each and share every key tile.  Tiles go from the cache straight to
 // LDS (16-byte direct loads) into two buffers, so the next tile's loads are
 // in flight while the current one is multiplied.
 //
@@ -17,23 +17,27 @@
 
 namespace pct {
 
-template <int DP_, int NT_, bool BF16_>
+template <int DP_, int MT_, bool BF16_>
 struct TilesCfg {
   static constexpr int DP = DP_;  // head size, padded
-  static constexpr int NT = NT_;  // 16-row blocks per wave
+  static constexpr int MT = MT_;  // rows of the workgroup: 64 or 128
+  // Waves, and 16-row blocks of each: two per operand read from LDS, and two
+  // waves per SIMD, as long as the registers hold the sums.  (Wide heads: 16
+  // requests of 256 rows over 4352 positions, D = 256, 1130 us with 4 waves
+  // of two blocks, one per SIMD, 865 with 8 waves of one; D = 192, 829, 685.)
+  static constexpr int W = DP > 128 && MT > 64 ? 8 : 4, NT = MT / 16 / W;
   static constexpr bool BF16 = BF16_;
   static constexpr int SL = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;
-  static constexpr int KB = tiles_kb(DP);  // keys of a tile
+  static constexpr int KB = kTilesKb;  // keys of a tile
   static constexpr int DT = DP / 16, KSTEP = DP / 32;
   static constexpr int GD = DT % 4 == 0 ? 4 : 2;  // V operands of a group
   static constexpr int KS = KB;
-  static constexpr int MT = 64 * NT;
   static constexpr int RPI = 64 / SL;       // rows per direct load
-  static constexpr int NI = KB / 4 / RPI;   // direct loads of K per wave
+  static constexpr int NI = KB / W / RPI;   // direct loads of K per wave
   static constexpr int GPS = KB / 8;        // 8-key groups of a tile
   static constexpr int TPV = 64 / GPS;      // tiles whose pages fit a wave
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
-  static constexpr int FEW = kTilesFew, LEAST = tiles_least(NT);  // of a run
+  static constexpr int FEW = kTilesFew, LEAST = tiles_least(MT);  // of a run
   static __device__ __forceinline__ int swizzle_k(int r) {
     return SL == 8 ? (r >> 1) & 7 : r & 15;
   }
@@ -76,8 +80,8 @@ template <class C>
 __device__ __forceinline__ void tiles_piece(
     const AttendArgs& a, const AttendWs& ws, const AttendReq& rq, int b,
     int h, int m0, int k0, int k1, int slot, uint4* tiles,
-    uint64_t (*odd_s)[4]) {
-  constexpr int NT = C::NT, KB = C::KB, SL = C::SL, NI = C::NI;
+    uint64_t (*odd_s)[C::W]) {
+  constexpr int NT = C::NT, KB = C::KB, SL = C::SL, NI = C::NI, W = C::W;
   constexpr int DT = C::DT, KSTEP = C::KSTEP, GD = C::GD;
   const PageGeom& g = a.g;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -92,7 +96,7 @@ __device__ __forceinline__ void tiles_piece(
   // direct loads: this lane's row of load 0 and its pieces there.  Load i
   // reads rows i RPI further; the bits of a row and of i RPI are distinct, so
   // its swizzle differs by that of i RPI.
-  const int row0 = wave * (KB / 4) + lane / SL;
+  const int row0 = wave * (KB / W) + lane / SL;
   const int kp0 = (lane % SL) ^ C::swizzle_k(row0);
   const int vp0 = (lane % SL) ^ C::swizzle_v(row0);
   const int row_bytes = chd * 16, group_bytes = 8 * row_bytes;
@@ -175,7 +179,7 @@ __device__ __forceinline__ void tiles_piece(
     if (small) {
       // a page of its own for every row: through registers
 #pragma unroll 1
-      for (int x = wave * (KB / 4) * SL + lane; x < (wave + 1) * (KB / 4) * SL;
+      for (int x = wave * (KB / W) * SL + lane; x < (wave + 1) * (KB / W) * SL;
            x += 64) {
         const int r = x / SL, sl = x % SL;
         const int t = min(k * KB + r, L - 1);
@@ -199,7 +203,7 @@ __device__ __forceinline__ void tiles_piece(
     int to = lds0 + (par * BUF + wave * NI * 64) * 16;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int grp = (wave * (KB / 4) + i * C::RPI) >> 3;
+      const int grp = (wave * (KB / W) + i * C::RPI) >> 3;
       uint32_t p = __builtin_amdgcn_readlane(pv, first + grp);
       p = p < (uint32_t)g.n_pages ? p : 0;
       const uint64_t at =
@@ -287,7 +291,7 @@ __device__ __forceinline__ void tiles_piece(
       // the probability 0 of a row that does not see it: it is taken out
       // here and added to the rows that see it below.
       uint4 v[NI];
-      const int x0 = wave * (KB / 4) * SL + lane;
+      const int x0 = wave * (KB / W) * SL + lane;
 #pragma unroll
       for (int i = 0; i < NI; ++i) v[i] = vt[x0 + 64 * i];
 #pragma unroll
@@ -348,8 +352,9 @@ __device__ __forceinline__ void tiles_piece(
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (EDGE) {
-      odd_keys = odd_s[par][0] | odd_s[par][1] | odd_s[par][2] |
-                 odd_s[par][3];
+      odd_keys = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) odd_keys |= odd_s[par][w];
       // the scores of these keys once more: it is rare, and they would
       // occupy registers through every tile
       while (odd_keys) {
@@ -430,11 +435,11 @@ __device__ __forceinline__ void tiles_piece(
 }
 
 template <class C>
-__global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
+__global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
     AttendArgs a, AttendWs ws) {
   constexpr int KB = C::KB, SL = C::SL, MT = C::MT;
   __shared__ __align__(16) uint4 tiles[4 * KB * SL];
-  __shared__ uint64_t odd_s[2][4];
+  __shared__ uint64_t odd_s[2][C::W];
 
   AttendRun run;
   AttendReq rq;
@@ -443,7 +448,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_tiles_kernel(
   if ((a.g.D >> 3) < SL) {
     // slots past the head size are read and never loaded
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < 4 * KB * SL; i += 256) tiles[i] = zero;
+    for (int i = threadIdx.x; i < 4 * KB * SL; i += 64 * C::W)
+      tiles[i] = zero;
   }
   while (run.u < run.end) {
     next_request<MT, KB>(a, run, rq);

@@ -68,19 +68,17 @@ struct AttendArgs {
   void* out;
   float* lse;
 };
-// Tile of a call: heads padded to dp elements, nt 16-row blocks per wave, the
-// waves share their keys (and hold different rows) or not, mt rows per
-// workgroup, steps of ks keys, n_wg runs at most (a multiple of 8); the join
+// Tile of a call: heads padded to dp elements, mt rows per workgroup (16: all
+// waves hold these rows and have keys of their own; 64, 128: they hold
+// different ones and share the keys), steps of ks keys, n_wg runs at most (a multiple of 8); the join
 // goes through the `tiles` row tiles (row_tiles of a request at most), or
 // through the runs where these are fewer (row_tiles 0), and adds so many
 // groups of runs side by side.
 struct AttendPlan {
-  int dp, nt, shared, mt, ks, n_wg, row_tiles, tiles, groups;
+  int dp, mt, ks, n_wg, row_tiles, tiles, groups;
 };
-// Keys of a tile: of a wave's own one, of one that the waves share (32 where
-// 64 would leave no room for two buffers twice on a CU).
-constexpr int kRowsKb = 32;
-constexpr int tiles_kb(int dp) { return dp <= 128 ? 64 : 32; }
+// Keys of a tile: of a wave's own one, of one that the waves share.
+constexpr int kRowsKb = 32, kTilesKb = 64;
 // Steps of a run at least while runs are few, and beyond (runs_for).  Shared
 // tiles of 128 rows, 65 rows of 4 heads over 4066 positions, from 3, 4, 6
 // steps on: 35, 29, 34 us; of 64 rows, 4 requests of 16 rows over up to
@@ -88,7 +86,7 @@ constexpr int tiles_kb(int dp) { return dp <= 128 ? 64 : 32; }
 // steps on: 20 or 14 us.  Runs of the rows kernel leave a few rows only.
 constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2;
 constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
-constexpr int tiles_least(int nt) { return nt == 1 ? 6 : 4; }
+constexpr int tiles_least(int mt) { return mt == 64 ? 6 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
