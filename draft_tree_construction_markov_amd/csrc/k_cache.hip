@@ -17,16 +17,17 @@ namespace pct {
 // so takes and gives of different requests need no order between them.
 //
 // plan_scan: one workgroup computes both prefix sums and the new state.
-// plan_apply: block tables, ring entries, slots and places, a workgroup for
-// each piece of a request's rows.  Both are bound by the latency of a few
-// dependent loads.  Plans of few rows and requests run in plan_small, one
-// workgroup that does both (65 rows of one request: SMALL_US us instead of
-// TWO_US us for the two launches).
+// plan_apply: a thread for each row, and the first workgroup of a request
+// for its pages.  Both are bound by the latency of a few dependent loads:
+// 3.5 and 5 us for 128 requests of 513 rows, whose 1 MB takes 0.2.  Plans of
+// few rows and requests run in plan_small, one workgroup that does both (65
+// rows of one request 3.4 us instead of 4.2 for the two launches, 16 x 65
+// rows 5.2 and 5.8, 64 x 64 rows 9.6 and 6.4; the host's part of a launch is
+// 2.5 us more).
 
 constexpr int kScanThreads = 1024;
 constexpr int kApplyThreads = 256;
-constexpr int kApplyRows = 256;   // rows per workgroup of plan_apply
-constexpr int kSmallRows = 4096;  // rows of a plan in one workgroup, at most
+constexpr int kSmallRows = 2048;  // rows of a plan in one workgroup, at most
 constexpr int kSmallBatch = 64;   // and requests
 
 __device__ __forceinline__ int64_t pages_for(int64_t tokens, int shift) {
@@ -121,48 +122,48 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
   }
 }
 
-// Rows [r0, r1) of request b; its pages as well where r0 is 0.
-template <int THREADS>
-__device__ __forceinline__ void plan_apply(const PlanArgs& a, int b, int r0,
-                                           int r1) {
+// Slot and place of row i of request b.
+__device__ __forceinline__ void plan_row(const PlanArgs& a, int b, int i) {
   const PageGeom& g = a.g;
-  const int tid = threadIdx.x;
   const int4 rq = a.req[b];
-  const int2 ring0 = a.ring0[0];
   const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
   const int ctx = clamp_ctx(g.ctx_len[b]);
   const int held = rq.z, after = rq.w;
-  const int P = g.n_pages;
-  int32_t* table = a.table + (int64_t)b * g.max_pages;
-  const int page_mask = (1 << g.shift) - 1;
-  for (int i = r0 + tid; i < r1; i += THREADS) {
-    int64_t s = -1;
-    int place = -1;
-    if (i <= n) {
-      const int p = ctx + i, j = p >> g.shift;
-      if (j < after) {
-        // pages taken by this call are read where they come from: the table
-        // may not hold them yet
-        const int page =
-            j < held ? table[j]
-                     : a.ring[remainder_of((int64_t)ring0.x + rq.x + j - held, P)];
-        if (page >= 0 && page < P)
-          s = ((int64_t)page << g.shift) + (p & page_mask);
-      }
-      if (a.pos) place = ctx + (i > 0 ? a.depth[(int64_t)b * g.N + i - 1] : 0);
+  int64_t s = -1;
+  int place = -1;
+  if (i <= n) {
+    const int p = ctx + i, j = p >> g.shift;
+    if (j < after) {
+      // pages taken by this call are read where they come from: the table
+      // may not hold them yet
+      const int page =
+          j < held ? a.table[(int64_t)b * g.max_pages + j]
+                   : a.ring[remainder_of(
+                         (int64_t)a.ring0[0].x + rq.x + j - held, g.n_pages)];
+      if (page >= 0 && page < g.n_pages)
+        s = ((int64_t)page << g.shift) + (p & ((1 << g.shift) - 1));
     }
-    a.slot[(int64_t)b * (g.N + 1) + i] = s;
-    if (a.pos) a.pos[(int64_t)b * (g.N + 1) + i] = place;
+    if (a.pos) place = ctx + (i > 0 ? a.depth[(int64_t)b * g.N + i - 1] : 0);
   }
-  if (r0 == 0) {
-    for (int j = held + tid; j < after; j += THREADS)
-      table[j] =
-          a.ring[remainder_of((int64_t)ring0.x + rq.x + j - held, P)];
-    for (int j = after + tid; j < held; j += THREADS) {
-      a.ring[remainder_of((int64_t)ring0.x + ring0.y + rq.y + j - after, P)] =
-          table[j];
-      table[j] = -1;
-    }
+  a.slot[(int64_t)b * (g.N + 1) + i] = s;
+  if (a.pos) a.pos[(int64_t)b * (g.N + 1) + i] = place;
+}
+
+// Pages that request b takes or gives back, by `threads` threads.
+__device__ __forceinline__ void plan_pages(const PlanArgs& a, int b, int t,
+                                           int threads) {
+  const PageGeom& g = a.g;
+  const int4 rq = a.req[b];
+  const int2 ring0 = a.ring0[0];
+  const int held = rq.z, after = rq.w;
+  int32_t* table = a.table + (int64_t)b * g.max_pages;
+  for (int j = held + t; j < after; j += threads)
+    table[j] =
+        a.ring[remainder_of((int64_t)ring0.x + rq.x + j - held, g.n_pages)];
+  for (int j = after + t; j < held; j += threads) {
+    a.ring[remainder_of((int64_t)ring0.x + ring0.y + rq.y + j - after,
+                        g.n_pages)] = table[j];
+    table[j] = -1;
   }
 }
 
@@ -172,15 +173,20 @@ __global__ __launch_bounds__(kScanThreads) void plan_scan_kernel(PlanArgs a) {
 
 __global__ __launch_bounds__(kApplyThreads) void plan_apply_kernel(
     PlanArgs a) {
-  plan_apply<kApplyThreads>(a, blockIdx.x, blockIdx.y * kApplyRows,
-                            min((int)(blockIdx.y + 1) * kApplyRows, a.g.N + 1));
+  const int b = blockIdx.x, i = blockIdx.y * kApplyThreads + threadIdx.x;
+  if (i <= a.g.N) plan_row(a, b, i);
+  if (blockIdx.y == 0) plan_pages(a, b, threadIdx.x, kApplyThreads);
 }
 
+// all rows over the threads, the requests' pages over the waves
 __global__ __launch_bounds__(kScanThreads) void plan_small_kernel(PlanArgs a) {
   plan_scan(a);
   __syncthreads();
-  for (int b = 0; b < a.g.batch; ++b)
-    plan_apply<kScanThreads>(a, b, 0, a.g.N + 1);
+  const int tid = threadIdx.x, R = a.g.N + 1;
+  for (int x = tid; x < a.g.batch * R; x += kScanThreads)
+    plan_row(a, x / R, x % R);
+  for (int b = tid >> 6; b < a.g.batch; b += kScanThreads / kWave)
+    plan_pages(a, b, tid & 63, kWave);
 }
 
 hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s) {
@@ -193,7 +199,7 @@ hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int pieces = (a.g.N + kApplyRows) / kApplyRows;
+  const int pieces = a.g.N / kApplyThreads + 1;
   hipLaunchKernelGGL(plan_apply_kernel, dim3(a.g.batch, pieces),
                      dim3(kApplyThreads), 0, s, a);
   return hipGetLastError();
@@ -201,7 +207,10 @@ hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s) {
 
 // ---------------------------------------------------------------------
 // Row writes: one thread copies a 16-byte piece of a row's key and of its
-// value; consecutive threads take consecutive pieces of a row.
+// value; consecutive threads take consecutive pieces of a row, so a wave's
+// loads and stores are whole rows.  Bound by memory: 65,664 rows of 8 heads
+// of 128 (538 MB read and written) in 105 us, 5.1 TB/s, what a copy of 1 GiB
+// reaches; 64 rows 2.4 us, the latency of the slot, the row and the store.
 __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
   const int hc = a.D / 8, rc = a.Hkv * hc;  // pieces of a head, of a row
   const int64_t total = a.rows * rc;
@@ -238,7 +247,9 @@ hipError_t launch_cache_write(const WriteArgs& a, hipStream_t s) {
 // at least j, past every place written so far), and columns do not touch
 // each other.  Moves onto themselves are left out.  A path of the usual
 // depth is one round of loads: the time is the latency of the chain lengths
-// and nodes -> pages -> rows -> stores, then the bytes (COMMIT_US).
+// and nodes -> pages -> rows -> stores, then the bytes (one request of 32
+// layers 3.5 us, 32 requests of 16 layers 7.0 us, 32 MB read and written: 4.6
+// TB/s).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kMove = 16;
 constexpr int kMoveList = 128;  // moves resolved to slots at a time

@@ -68,6 +68,12 @@ def test_plan_over_rounds(batch, N, page, width, P, hi):
     assert s.state[1] == P and sorted(s.ring) == list(range(P))
 
 
+@pytest.mark.parametrize("batch,N", [(64, 31), (64, 32), (64, 0), (65, 0),
+                                     (17, 119), (2, 1023), (1, 2048)])
+def test_plan_around_the_bounds_of_one_workgroup(batch, N):
+    test_plan_over_rounds(batch, N, 16, 90 + N // 16, 4000, 900)
+
+
 def test_plan_without_nodes_and_out_of_pages():
     rng = np.random.default_rng(1)
     h = pct.CachePlan(4, 6, 10, 4, 5)
