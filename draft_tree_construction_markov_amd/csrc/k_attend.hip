@@ -64,7 +64,9 @@ WsLayout layout(const AttendPlan& p) {
 // in order of runs within a group, then of groups.  PG = 4 where rows are few
 // or split over many runs (32 rows over 60 k positions: 56 us with the
 // attention, 66 with one group), else one (512 rows over up to 5 k: 87 us,
-// 96 with four).
+// 96 with four).  A workgroup for every row tile if these are fewer than the
+// runs, else for every run; the others leave at once, but 8192 of them took
+// 3 us.  Bound by the sums' read: 32 trees of 257 rows 16 us for 66 MB.
 constexpr int kJoinThreads = 256, kInFlight = 8;
 
 template <bool BF16>
