@@ -22,7 +22,11 @@
 // second product) saves 4 to 15%, so none of them alone bounds the kernel.
 // What did not help: operands read two groups ahead and a check for
 // non-finite sums at the end of a piece in place of the search (registers
-// spill, +2 .. 4%), probabilities before the check of the reference.
+// spill, and a spill's load waits for the tile under way: +2 .. 4%);
+// probabilities before the check of the reference; exponentials between the
+// products of the same wave (D = 128 -1%, D = 64 +5%); four blocks of rows
+// per wave and one wave per SIMD (half the LDS reads, +45% at D = 64); three
+// workgroups per CU at D = 64 (-5 .. +15%).
 #pragma once
 #include <type_traits>
 
