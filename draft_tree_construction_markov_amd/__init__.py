@@ -592,10 +592,12 @@ class CachePlan:
         self.device = dev = _device(device)
         self.ws = _workspace(lib().pct_cache_plan_workspace(batch), dev)
         i32 = dict(dtype=torch.int32, device=dev)
+        # no slots before the first run
         self.out = CacheRows(
-            slot=torch.empty(batch, N + 1, dtype=torch.int64, device=dev),
-            pos=torch.empty(batch, N + 1, **i32),
-            missing=torch.empty(batch, **i32))
+            slot=torch.full((batch, N + 1), -1, dtype=torch.int64,
+                            device=dev),
+            pos=torch.full((batch, N + 1), -1, **i32),
+            missing=torch.zeros(batch, **i32))
         o = self.out
         self._fn, self._ref = lib().pct_cache_plan, C.byref(self.shape)
         self._shapes = ((batch,), (batch, N), (batch, max_pages), (n_pages,),
@@ -651,7 +653,8 @@ def cache_write(k, v, slot, k_cache, v_cache):
 
 class TreeAttention:
     """Attention of a round's rows over a paged cache, fixed shape, with its
-    workspace and outputs allocated once; run() only enqueues kernels."""
+    workspace and outputs allocated once; run() only enqueues kernels.  Its
+    outputs carry no gradient."""
 
     def __init__(self, batch: int, N: int, Hq: int, Hkv: int, D: int,
                  n_pages: int, page_size: int, max_pages: int,

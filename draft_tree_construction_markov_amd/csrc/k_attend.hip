@@ -20,19 +20,25 @@ struct WsLayout {
 AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   AttendPlan p{};
   p.dp = padded(D);
-  // The smallest row tile that holds a request's rows of one head; waves
-  // with keys of their own up to 16 rows (with 32, 64 requests of 8 rows
-  // over up to 8 k positions took 205 us, with shared tiles 166).
+  // The smallest row tile that holds a request's rows of one head, or 64 rows
+  // for little work; waves with keys of their own up to 16 rows (with 32, 64
+  // requests of 8 rows over up to 8 k positions took 205 us, with shared
+  // tiles 166).
   const int64_t M = (int64_t)(N + 1) * (Hq / Hkv);
   p.mt = M <= 16 ? 16 : M <= 64 ? 64 : 128;
+  // (bounded, so that no shape overflows the products below)
+  const auto bounded = [](int64_t x) { return x < 1 << 30 ? x : 1 << 30; };
+  const int64_t key_tiles = (cap + kTilesKb - 1) / kTilesKb;
+  if (p.mt == 128 && p.dp <= 128 &&
+      bounded(batch * (Hkv * ((M + 127) / 128))) * key_tiles <= kHalfUnits)
+    p.mt = 64;
   const bool shared = p.mt > 16;
   p.ks = shared ? kTilesKb : 4 * kRowsKb;
   // as many runs as stay on the chip, or as the longest requests could fill
   const int64_t steps = (cap + p.ks - 1) / p.ks;
   const int64_t row_tiles = (M + p.mt - 1) / p.mt;
   const int64_t tiles = batch * (Hkv * row_tiles);
-  // (bounded, so that no shape overflows it)
-  const int64_t units = (tiles < 1 << 30 ? tiles : 1 << 30) * steps;
+  const int64_t units = bounded(tiles) * steps;
   const int few = shared ? kTilesFew : kRowsFew;
   const int64_t runs = units / (steps < few ? steps : few) + 1;
   p.n_wg = kCus * (p.dp <= 128 ? 2 : 1);

@@ -202,17 +202,16 @@ struct AttendRun {
   int b;          // request that holds u; its units begin at b_off
   int64_t b_off;
   int level;      // row tile of the run, -1: lines
-  int blocks;     // of a level
-  int64_t q;      // run (block) j begins at unit j q + min(j, r)
-  int r;
+  // Run (block) j of `blocks` begins at unit floor(j total / blocks): as many
+  // runs for every row tile of equal lengths end where it ends.
+  int blocks;
+  int64_t total;
   __device__ __forceinline__ int64_t start(int j) const {
-    return j * q + min(j, r);
+    return div_up_to_64(j * total, blocks);
   }
   // run that holds unit x of the lines, or of this run's level
   __device__ __forceinline__ int owner(int64_t x) const {
-    const int64_t big = (int64_t)r * (q + 1);
-    const int j = (int)(x < big ? div_up_to_64(x, q + 1)
-                                : r + div_up_to_64(x - big, q));
+    const int j = (int)div_up_to_64((x + 1) * blocks - 1, total);
     return level < 0 ? j : level * blocks + j;
   }
   __device__ __forceinline__ int64_t units(const AttendArgs& a,
@@ -314,8 +313,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     r.level = at / bx;
     r.blocks = 8 * bx;
     r.run = r.level * r.blocks + j;
-    r.q = div_up_to_64(total1, r.blocks);
-    r.r = (int)(total1 - r.q * r.blocks);
+    r.total = total1;
     r.u = r.start(j);
     r.end = r.start(j + 1);
     incl = incl1;
@@ -326,8 +324,8 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
     xcount = (n_run >> 3) + (xcd < (n_run & 7) ? 1 : 0);
     r.level = -1;
     r.run = xcd * (n_run >> 3) + min(xcd, n_run & 7) + at;
-    r.q = n_run > 0 ? div_up_to_64(total, n_run) : 0;
-    r.r = (int)(total - r.q * n_run);
+    r.blocks = max(n_run, 1);
+    r.total = total;
     r.u = r.start(r.run);
     r.end = r.start(r.run + 1);
   }

@@ -85,6 +85,14 @@ constexpr int kRowsKb = 32, kTilesKb = 64;
 // 5 k positions, from 4, 6 on: 28, 25 us; 16 rows over 1 k, from 6 or from 2
 // steps on: 20 or 14 us.  Runs of the rows kernel leave a few rows only.
 constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2;
+// Up to so many tiles of 128 rows by 64 keys, if requests are as long as the
+// block table allows, rows are cut into tiles of 64: more runs with a shorter
+// chain of steps each, for twice the reads of keys (from the L2) and of
+// operands.  4 requests of 256 rows over 656 positions (2816 tiles) 54 us
+// with 128, 37 with 64; 65 rows over 2 k (792) 29, 23; 256 rows over 9 k
+// (9280) 79, 82, over 32 k (32 k tiles) 168, 214.  Not for heads past 128,
+// whose 64 rows leave one wave per SIMD (256 rows over 2 k, D = 256: 53, 67).
+constexpr int kHalfUnits = 6144;
 constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
 constexpr int tiles_least(int mt) { return mt == 64 ? 6 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X

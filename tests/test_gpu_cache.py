@@ -291,3 +291,12 @@ def test_rounds_on_a_paged_cache_follow_the_plain_sequence():
                     assert torch.equal(got, emb[layer, kind][text[b]])
     assert min(len(x) for x in text) > 5 and not math.isnan(
         float(outs[0].float().sum()))
+
+
+def test_a_write_before_the_first_plan_leaves_the_cache():
+    cache = pct.PagedCache(2, 3, 8, 16, 4, 4, 2, 32)
+    k = torch.ones(2, 4, 2, 32, dtype=torch.bfloat16, device="cuda")
+    announce("write before plan")
+    cache.write(0, k, k)
+    torch.cuda.synchronize()
+    assert not cache.k.any() and not cache.v.any()
