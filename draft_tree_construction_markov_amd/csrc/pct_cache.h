@@ -79,11 +79,12 @@ struct AttendPlan {
 };
 // Keys of a tile: of a wave's own one, of one that the waves share.
 constexpr int kRowsKb = 32, kTilesKb = 64;
-// Steps of a run at least while runs are few, and beyond (runs_for).  Shared
-// tiles of 128 rows, 65 rows of 4 heads over 4066 positions, from 3, 4, 6
-// steps on: 35, 29, 34 us; of 64 rows, 4 requests of 16 rows over up to
-// 5 k positions, from 4, 6 on: 28, 25 us; 16 rows over 1 k, from 6 or from 2
-// steps on: 20 or 14 us.  Runs of the rows kernel leave a few rows only.
+// Steps of a run at least while runs are few, and beyond (runs_for).  Tiles of
+// 64 rows, 16 rows of 4 heads over 1 k positions, from 6 or from 2 steps on:
+// 20 or 14 us; from 5, 6 and 8 on with many runs: 65 rows over 4 k 29.6,
+// 28.9, 27.0, 4 requests of 65 rows over up to 2 k 31.7, 31.4, 32.2 us.  Of
+// 128 rows, 65 rows over 4 k, from 3, 4, 6 on: 35, 29, 34 us.  Runs of the
+// rows kernel leave a few rows only.
 constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2;
 // Up to so many tiles of 128 rows by 64 keys, if requests are as long as the
 // block table allows, rows are cut into tiles of 64: more runs with a shorter
@@ -94,7 +95,7 @@ constexpr int kRowsFew = 1, kRowsLeast = 1, kTilesFew = 2;
 // whose 64 rows leave one wave per SIMD (256 rows over 2 k, D = 256: 53, 67).
 constexpr int kHalfUnits = 6144;
 constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
-constexpr int tiles_least(int mt) { return mt == 64 ? 6 : 4; }
+constexpr int tiles_least(int mt) { return mt == 64 ? 8 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X
 // Per run two row tiles of sums that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
