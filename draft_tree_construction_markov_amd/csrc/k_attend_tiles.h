@@ -14,7 +14,7 @@
 // Measured, D = 128, 4 query heads per key-value head, with the join: 8
 // requests of 256 rows over 33 k positions 1190 us, 924 TFLOP/s (a library's
 // 8192^3 product reaches 1160); 32 trees of 257 rows over 512 .. 8192
-// positions 620 us, 600 TFLOP/s of work that counts: the ninth row tile of a
+// positions 626 us, 597 TFLOP/s of work that counts: the ninth row tile of a
 // head has 4 rows, and a tile with nodes takes almost twice the 2.3 us of one
 // without (masks, the search for values that are not finite).  A step of a
 // wave is a chain of products, exponentials and products that two waves per
