@@ -380,3 +380,81 @@ def test_values_that_are_not_finite_in_large_trees():
     assert np.isinf(got[reached][:, :, at]).all()
     assert (np.abs(got - o)[reached][:, :, ~at] <=
             tol[reached][:, :, ~at]).all()
+
+
+def wide(c):
+    """The same case with a block table for long requests, so that the shape
+    asks for row tiles of 128 rows whatever the lengths are."""
+    width = 64 * 6300 // c.k.shape[2]
+    t = np.full((c.batch, width), -1, np.int32)
+    t[:, :c.table.shape[1]] = c.table
+    c.table = t
+    return c
+
+
+@pytest.mark.parametrize("D", [16, 64, 80, 96, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_wide_tables_head_sizes(D, dtype):
+    check(wide(Case(D + 3, 3, 37, 8, 2, D, 16, [0, 77, 301], dtype=dtype)))
+
+
+@pytest.mark.parametrize("N", [16, 31, 32, 63, 64, 65, 127, 128, 129, 200,
+                               256])
+@pytest.mark.parametrize("chain", [False, True])
+def test_wide_tables_tree_sizes(N, chain):
+    check(wide(Case(N + 1, 3, N, 8, 2, 128, 16, [70, 0, 1291],
+                    n=[N, N // 2, N - 1], chain=chain)))
+
+
+@pytest.mark.parametrize("page", [1, 4, 8, 64, 1024])
+@pytest.mark.parametrize("drop", [0.0, 0.5])
+def test_wide_tables_pages(page, drop):
+    check(wide(Case(page + 7, 3, 40, 4, 2, 64, page, [5, 200, 333],
+                    drop=drop)))
+
+
+def test_wide_tables_uneven_batch():
+    n = [33, -1, 0, 40, 12, -1, 32, 5, 33]
+    ctx = [0, 100, 1, 700, 64, 0, 1999, 17, 16]
+    check(wide(Case(6, 9, 40, 8, 4, 128, 32, ctx, n=n)))
+
+
+@pytest.mark.parametrize("batch", [2, 70])
+def test_wide_tables_more_row_tiles_than_runs(batch):
+    rng = np.random.default_rng(batch)
+    N, Hkv = (300, 128) if batch == 2 else (40, 4)
+    check(wide(Case(batch, batch, N, 4 * Hkv, Hkv, 16, 16,
+                    rng.integers(0, 90, batch),
+                    n=rng.integers(-1, N + 1, batch))))
+
+
+@pytest.mark.parametrize("spread,scale", [(30.0, None), (8.0, -0.3),
+                                          (200.0, 1.0)])
+def test_wide_tables_peaked_scores(spread, scale):
+    check(wide(Case(12, 2, 39, 4, 1, 128, 16, [700, 40], spread=spread,
+                    scale=scale)))
+
+
+def test_wide_tables_values_that_are_not_finite():
+    c = Case(82, 1, 180, 8, 2, 128, 16, [45])
+    bad = [0, 30, 77, 150]
+    for i in bad:
+        t = 46 + i
+        c.v[c.table[0, t // 16], :, t % 16, 64:70] = math.inf
+    wide(c)
+    want = c.want()
+    reached = c.anc[0][:, bad].any(-1)
+    h = handle(c)
+    q, k, v, table, ctx, n, mask = device_args(c)
+    announce("not finite, wide table")
+    out, lse = h.run(q, k, v, table, ctx, n, mask=mask)
+    torch.cuda.synchronize()
+    got = out[0, 1:].double().cpu().numpy()
+    o, tol = want[0][0, 1:], want[2][0, 1:]
+    at = np.zeros(128, bool)
+    at[64:70] = True
+    assert reached.any() and not reached.all()
+    assert (np.abs(got - o)[~reached] <= tol[~reached]).all()
+    assert np.isinf(got[reached][:, :, at]).all()
+    assert (np.abs(got - o)[reached][:, :, ~at] <=
+            tol[reached][:, :, ~at]).all()
