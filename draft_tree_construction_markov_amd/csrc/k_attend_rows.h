@@ -82,8 +82,6 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 
     int irow[NT];
     s16x8 qf[NT][KSTEP];
-    load_queries<C>(a, b, h, rt * C::MT, rq.M, irow, qf);
-    sign_queries<C>(a, qf);
     AttendState<C> st;
     st.clear();
 
@@ -120,9 +118,11 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
       }
     };
     load_pages(k0);
+    load_queries<C>(a, b, h, rt * C::MT, rq.M, irow, qf);
     load_rows(k0);
     if (k0 + 1 < k1) load_pages(k0 + 1);
     note_piece(a, ws, run, rq, pc, join);  // (while these are on their way)
+    sign_queries<C>(a, qf);
 
     for (int k = k0; k < k1; ++k) {
       const int t0 = tile_t0(k);
