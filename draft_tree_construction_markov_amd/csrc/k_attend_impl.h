@@ -124,7 +124,8 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
 
 // Work of one request in units: a step of a row tile.
 struct AttendReq {
-  int ctx, n, L;   // context, nodes, positions
+  int ctx, n, L;   // context, nodes, positions (of the block table)
+  int all;         // positions that every row sees: the context and the root
   int M, RT, KT;   // packed rows, row tiles, steps of a row tile
   int64_t units;   // of all heads and row tiles
 };
@@ -135,6 +136,7 @@ __device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
   r.n = n;
   r.ctx = ctx;
   r.L = min(ctx + n + 1, a.g.max_pages << a.g.shift);
+  r.all = min(ctx + 1, r.L);  // (a context may be longer than the table)
   r.M = (n + 1) * a.G;
   r.RT = (r.M + MT - 1) / MT;
   r.KT = (r.L + KS - 1) / KS;

@@ -367,7 +367,8 @@ pct_status pct_build_tree_noalloc(const pct_tree_shape* shape /*host*/,
  * A cache is [n_pages][Hkv][page_size][D], keys and values apart.  The
  * block table [batch][max_pages] gives the page of each page_size
  * positions; an entry outside [0, n_pages) stands for no page: its
- * positions are not written, attended or moved. */
+ * positions are not written, attended or moved, and neither are positions
+ * past the table's max_pages * page_size. */
 typedef struct {
   int32_t batch, N, n_pages, page_size, max_pages, Hq, Hkv, D, dtype;
 } pct_cache_shape;

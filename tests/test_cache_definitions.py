@@ -1,0 +1,59 @@
+"""CPU pins of the second 64-bit definition of attention that GPU tests compare
+with: it gives what the first one gives, and its comparison lets no wrong
+value pass."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cachestrict
+from cacheref import Case
+
+
+@pytest.mark.parametrize("kw", [{}, dict(chain=True), dict(drop=0.5),
+                                dict(dtype=torch.float16), dict(cut=3)])
+def test_both_definitions_agree(kw):
+    width = kw.pop("cut", None)
+    c = Case(3, 3, 12, 4, 2, 16, 8, [9, 0, 33], n=[12, -1, 5], **kw)
+    if width:
+        c.table = np.ascontiguousarray(c.table[:, :width])
+    a = c.want()
+    b = [x.numpy() for x in cachestrict.definition(c, "cpu")]
+    for q in range(3):
+        m = int(c.n[q]) + 1
+        assert not b[0][q, m:].any() and not b[1][q, m:].any()
+        for x, y in zip(a[:2], b[:2]):
+            assert np.allclose(x[q, :m], y[q, :m], rtol=0, atol=1e-12)
+        # no tolerance is wider than the first definition's
+        for x, y in zip(a[2:], b[2:]):
+            seen = np.isfinite(b[1][q, :m])
+            assert (y[q, :m][seen] <= x[q, :m][seen] * (1 + 1e-9)).all()
+
+
+def test_the_definition_with_values_that_are_not_finite():
+    c = Case(5, 1, 9, 2, 1, 16, 8, [20])
+    t = 20 + 1 + 4
+    c.v[c.table[0, t // 8], 0, t % 8, 3:5] = math.inf
+    o, z, tol, _ = cachestrict.definition(c, "cpu")
+    sees = torch.from_numpy(np.r_[False, c.anc[0][:, 4]])
+    assert sees.any() and not sees.all()
+    assert torch.isinf(o[0, sees][..., 3:5]).all()
+    assert torch.isfinite(o[0, ~sees]).all() and torch.isfinite(tol).all()
+    assert torch.isfinite(o[0, sees][..., 5:]).all()
+    assert torch.isfinite(z).all()
+
+
+def test_the_comparison_lets_nothing_pass():
+    want = torch.tensor([1.0, math.inf, math.nan, 0.0], dtype=torch.float64)
+    tol = torch.tensor([0.1, math.nan, math.nan, 0.0], dtype=torch.float64)
+    cachestrict.agree(want.clone(), want, tol, "same")
+    for i, x in ((0, 1.2), (0, math.nan), (0, math.inf), (1, -math.inf),
+                 (1, 3.0), (1, math.nan), (2, 0.0), (3, 1e-30)):
+        got = want.clone()
+        got[i] = x
+        with pytest.raises(AssertionError):
+            cachestrict.agree(got, want, tol, i)
+    tol[0] = math.inf  # a tolerance that is none
+    with pytest.raises(AssertionError):
+        cachestrict.agree(want, want, tol, "tolerance")
