@@ -189,7 +189,8 @@ __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
                  round_pair<BF16>(s.o.z * inv, s.o.w * inv));
   if (a.lse && c == 0)
     a.lse[row] = s.l == 0.f ? neg_inf()
-                            : (s.m + __builtin_log2f(s.l)) * (float)kLn2;
+                            : (s.m + (__builtin_log2f(s.l) - kLift<BF16>)) *
+                                  (float)kLn2;
 }
 
 template <bool BF16, int LR>

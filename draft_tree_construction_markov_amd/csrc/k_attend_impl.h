@@ -3,9 +3,15 @@
 //   out = sum_{t in S} p_t v_t / sum_{t in S} p_t,  p_t = 2^(z_t - m),
 //   z_t = |scale| log2(e) (+-q . k_t),  lse = ln(2) (m + log2 sum p_t),
 // in one pass over the positions.  m only has to be near the largest z_t: it
-// is raised (and the sums so far are scaled down) when a score comes that
-// is more than 2^kRaise above it, so p stays below 2^kRaise and most tiles
-// need neither a reduction over lanes nor a rescaling.
+// is raised (and the sums so far are scaled down) when a z_t comes that is
+// more than kRaise above it, so p stays below 2^kRaise and most tiles need
+// neither a reduction over lanes nor a rescaling.  p is rounded to the cache's
+// type for the second product (the sums of p and of p v are fp32), which
+// bf16 does to 2^-8 of every p.  fp16 rounds p below 2^-14 to its least step
+// 2^-24 instead, and p below 2^-25 to nothing, while they all count in the
+// sum: 32 k keys at 2^-25 of the largest are 2^-10 of the result.  It holds
+// 2^kLift p instead (at most 2^(kRaise + kLift) = 2^15; the largest fp16 is just below
+// 2^16), and its sums are 2^kLift times as large until they are divided.
 //
 // Both products are computed transposed, with v_mfma_f32_16x16x32:
 //   S^T[key][row] = K Q^T     A = 16 keys of the tile, B = 16 query rows
@@ -448,8 +454,8 @@ __device__ __forceinline__ uint64_t seen_keys(const AttendArgs& a, int b,
   return see;
 }
 
-// Softmax state of a wave's rows: the reference m of each row (ms: m, 0
-// while nothing was seen), this lane's part of the sum, and O^T.
+// Softmax state of a wave's rows: the reference m of each row (ms: m - kLift,
+// 0 while nothing was seen), this lane's part of the sum, and O^T.
 template <class C>
 struct AttendState {
   float mx[C::NT], ms[C::NT], l[C::NT];
@@ -490,7 +496,7 @@ __device__ __forceinline__ void raise_reference(float c,
       const float f =
           m2 == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(st.mx[nt] - m2);
       st.mx[nt] = m2;
-      st.ms[nt] = m2 == neg_inf() ? 0.f : m2;
+      st.ms[nt] = m2 == neg_inf() ? 0.f : m2 - kLift<C::BF16>;
       st.l[nt] *= f;
 #pragma unroll
       for (int d = 0; d < C::DT; ++d) st.o[nt][d] *= f;

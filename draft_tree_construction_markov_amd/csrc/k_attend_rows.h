@@ -275,7 +275,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
         if (a.lse && c == 0)
           a.lse[row] = sum == 0.f
                            ? neg_inf()
-                           : (top + __builtin_log2f(sum)) * (float)kLn2;
+                           : (top + (__builtin_log2f(sum) -
+                                     kLift<C::BF16>)) * (float)kLn2;
       } else {
         *reinterpret_cast<f32x8*>(part_o + r * C::DP + 8 * c) = acc;
         if (c == 0) part_ml[r] = make_float2(top, sum);

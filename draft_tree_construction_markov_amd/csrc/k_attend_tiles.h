@@ -437,7 +437,8 @@ __device__ __forceinline__ void tiles_piece(
       }
       if (a.lse && quad == 0)
         a.lse[row] = sum == 0.f ? neg_inf()
-                                : (st.mx[nt] + __builtin_log2f(sum)) *
+                                : (st.mx[nt] + (__builtin_log2f(sum) -
+                                                kLift<C::BF16>)) *
                                       (float)kLn2;
     } else {
       const int64_t row =

@@ -97,7 +97,10 @@ constexpr int kHalfUnits = 6144;
 constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
 constexpr int tiles_least(int mt) { return mt == 64 ? 8 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X
-// Per run two row tiles of sums that other runs continue: slot 0 of a tile
+// fp16 holds probabilities times 2^kLift (k_attend_impl.h has the reason).
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+// Per run two row tiles of sums (times 2^kLift) that other runs continue: slot 0 of a tile
 // that an earlier run began, slot 1 of one that this run began and did not
 // end.  meta {request, head << 20 | row tile, first run, last run} of a row
 // tile that is cut, w < 0: it is not; its index is the row tile's if

@@ -438,7 +438,8 @@ pct_status pct_cache_write(const pct_cache_shape* shape /*host*/,
  *   lse = ln sum_{t in S} exp(scale * q . k_t);
  * an empty S gives out = 0 and lse = -inf.  Positions outside a row's S have
  * no influence on it, whatever the cache holds there (NaN included).
- * Scores, normalisers and sums are fp32; a probability is rounded to the
+ * Scores, normalisers and sums are fp32; a probability (in fp16 2^7 times
+ * it, which keeps those down to 2^-32 of the largest) is rounded to the
  * cache's type before it meets a value.
  *
  *  q       rows of [Hq][D], q_row_stride elements from row to row

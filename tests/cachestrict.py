@@ -11,6 +11,7 @@ import torch
 from cacheref import F32, HALF_STEP
 
 LEAST_FP16 = 2.0 ** -24  # least step of fp16
+LIFT = 2.0 ** 7  # fp16 probabilities are kept as 2^7 p
 
 
 def definition(c, device="cuda"):
@@ -18,8 +19,10 @@ def definition(c, device="cuda"):
     are zero.
 
     Tolerances are those of cacheref.attention, with its term for what lies
-    below fp16's least step 2^-24 in its exact form: half a step for every
-    probability, whose values add up to sum |v|, and for the result."""
+    below fp16's least step 2^-24 in its exact form: a probability p (of at
+    most 1, for the largest score) is held as 2^7 p, so half a step is 2^-32
+    of it, and the values that it meets add up to sum |v|; the result's own
+    half step is 2^-25."""
     batch, R, Hq, D = c.q.shape
     n_pages, Hkv, page, _ = c.k.shape
     G = Hq // Hkv
@@ -77,7 +80,7 @@ def definition(c, device="cuda"):
                 tol[b, :m, g] = A * (2 * u + torch.expm1(2 * ds) + steps)
                 if c.dtype == torch.float16:
                     tol[b, :m, g] += LEAST_FP16 / 2 * (
-                        1 + see.double() @ fine.abs())
+                        1 + (see.double() @ fine.abs()) / LIFT)
                 tol_l[b, :m, g] = (ds + steps)[:, 0] + z.abs() * 8 * F32
     return out, lse, tol, tol_l
 

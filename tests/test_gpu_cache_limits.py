@@ -1,5 +1,5 @@
 """GPU checks of pct_tree_attention where a form of its kernels can go wrong by
-itself: contexts longer than the block table."""
+itself: contexts longer than the block table and many small probabilities."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +10,7 @@ from gpu_util import announce
 from test_gpu_cache_attention import device_args, handle
 
 pytestmark = pytest.mark.gpu
+BF16, FP16 = torch.bfloat16, torch.float16
 
 
 def check(c, *what):
@@ -44,3 +45,44 @@ def test_contexts_longer_than_the_table(D, N, chain, page, width):
 def test_contexts_longer_than_the_table_in_tiles_of_128_rows(width):
     check(cut(Case(width, 5, 300, 512, 64, 16, 8, [60, 95, 96, 100, 300]),
               width), "cut")
+
+
+# ---------------------------------------------------------------------------
+# many small probabilities
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("N,G", [(0, 4), (3, 4), (17, 1), (70, 2)])
+@pytest.mark.parametrize("down", [12.0, 17.4, 20.0])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+def test_many_small_probabilities(dtype, N, G, down, at):
+    # One key that takes all rows' weight and has no value; the others lie
+    # `down` below it and add up to far more than a step of the result.  64
+    # requests share their pages: with 8 heads each, no row tile is cut into
+    # runs with references of their own.
+    ctx, batch, Hkv, D = 32767, 64, 8, 16
+    c = Case(N + G, 1, N, G * Hkv, Hkv, D, 64, [ctx], dtype=dtype,
+             scale=1.0)
+    q = np.zeros((batch, N + 1, G * Hkv, D))
+    q[..., 0] = 1.0
+    q[..., 1] = c.rng.uniform(-0.05, 0.05, q.shape[:3])
+    c.q = torch.from_numpy(q).to(dtype)
+    t = np.arange(ctx + N + 1)
+    k = np.zeros((len(t), Hkv, D))
+    k[..., 1] = c.rng.uniform(-1, 1, k.shape[:2])
+    v = c.rng.uniform(0.5, 1.5, k.shape)
+    top = {"first": 0, "middle": ctx // 2, "last": ctx}[at]
+    k[top, :, 0], v[top] = down, 0.0
+    p, o = torch.from_numpy(c.table[0][t // 64].astype(np.int64)), t % 64
+    c.k[p, :, o] = torch.from_numpy(k).to(dtype)
+    c.v[p, :, o] = torch.from_numpy(v).to(dtype)
+    c.batch = batch
+    c.table, c.ctx, c.n = (np.repeat(x, batch, 0) for x in (c.table, c.ctx,
+                                                            c.n))
+    c.anc = None if c.anc is None else np.repeat(c.anc, batch, 0)
+    announce("small probabilities", (N, G), down, at)
+    q, k, v, table, ctx, n, mask = device_args(c)
+    out, lse = handle(c).run(q, k, v, table, ctx, n, mask=mask, scale=1.0)
+    torch.cuda.synchronize()
+    some = [0, 41]  # requests that are compared
+    c.batch, c.q = len(some), c.q[some]
+    compare(c, out[some], lse[some])
