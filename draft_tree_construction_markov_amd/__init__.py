@@ -98,6 +98,8 @@ def lib():
     L.pct_cache_plan_workspace.restype = sz
     L.pct_cache_plan.argtypes = [shape, P, P, P, P, P, P, P, P, P, P, P, sz,
                                  P]
+    L.pct_cache_plan_served.argtypes = [shape, P, P, P, P, P, P, P, P, P, P,
+                                        P, P, sz, P]
     L.pct_cache_write.argtypes = [shape, P, i64, P, i64, P, P, P, P]
     L.pct_tree_attention_workspace.argtypes = [shape]
     L.pct_tree_attention_workspace.restype = sz
@@ -125,7 +127,8 @@ def exported_symbols():
             "pct_build_tree_noalloc", "pct_verify_sample",
             "pct_verify_sample_workspace",
             "pct_tree_mask", "pct_verify_accept",
-            "pct_cache_plan", "pct_cache_plan_workspace", "pct_cache_write",
+            "pct_cache_plan", "pct_cache_plan_served",
+            "pct_cache_plan_workspace", "pct_cache_write",
             "pct_tree_attention", "pct_tree_attention_workspace",
             "pct_cache_commit", "pct_profile_enable",
             "pct_profile_reset", "pct_profile_read", "pct_status_string",
@@ -575,10 +578,13 @@ def _device(device) -> torch.device:
 class CacheRows:
     """Where a round's rows go: slot [batch][N+1] int64 (-1: none), pos
     [batch][N+1] int32 (place in the sequence, -1 for unused rows), missing
-    [batch] int32 (pages that the free ring could not give)."""
+    [batch] int32 (pages that the free ring could not give), n_served [batch]
+    int32 (n_nodes, -1 for the requests that miss pages: the n_nodes of the
+    round's attention and commit)."""
     slot: torch.Tensor
     pos: torch.Tensor
     missing: torch.Tensor
+    n_served: torch.Tensor
 
 
 class CachePlan:
@@ -592,18 +598,20 @@ class CachePlan:
         self.device = dev = _device(device)
         self.ws = _workspace(lib().pct_cache_plan_workspace(batch), dev)
         i32 = dict(dtype=torch.int32, device=dev)
-        # no slots before the first run
+        # no slots and no rows before the first run
         self.out = CacheRows(
             slot=torch.full((batch, N + 1), -1, dtype=torch.int64,
                             device=dev),
             pos=torch.full((batch, N + 1), -1, **i32),
-            missing=torch.zeros(batch, **i32))
+            missing=torch.zeros(batch, **i32),
+            n_served=torch.full((batch,), -1, **i32))
         o = self.out
-        self._fn, self._ref = lib().pct_cache_plan, C.byref(self.shape)
+        self._fn, self._ref = lib().pct_cache_plan_served, C.byref(self.shape)
         self._shapes = ((batch,), (batch, N), (batch, max_pages), (n_pages,),
                         (2,))
         self._tail = tuple(C.c_void_p(x.data_ptr()) for x in (
-            o.slot, o.pos, o.missing, self.ws)) + (self.ws.numel(),)
+            o.slot, o.pos, o.missing, o.n_served, self.ws)) + (
+                self.ws.numel(),)
 
     def run(self, ctx_len, n_nodes, block_table, n_held, ring, ring_state,
             depth=None) -> CacheRows:
@@ -763,6 +771,10 @@ class PagedCache:
     A round: rows = plan(n_nodes, depth); in each layer write(layer, k, v)
     and attend(layer, q, mask); then commit(tau, accept_node).  A place is
     emptied by setting its ctx_len to 0 and its n_nodes to -1 for one plan.
+
+    A request that the free ring cannot serve (rows.missing > 0) waits: it is
+    not attended, and commit leaves its length and its cache as they are
+    whatever tau and accept_node say.  It keeps its root for a later round.
     """
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
@@ -778,14 +790,13 @@ class PagedCache:
         self.ring = torch.arange(n_pages, **i32)
         self.ring_state = torch.tensor([0, n_pages], **i32)
         self.ctx_len = torch.zeros(batch, **i32)
-        self.n_nodes = None
         self._plan = CachePlan(batch, N, n_pages, page_size, max_pages,
                                device=dev)
+        self.n_nodes = self._plan.out.n_served
         self._attend = TreeAttention(batch, N, Hq, Hkv, D, n_pages, page_size,
                                      max_pages, dtype=dtype, device=dev)
 
     def plan(self, n_nodes=None, depth=None) -> CacheRows:
-        self.n_nodes = n_nodes
         return self._plan.run(self.ctx_len, n_nodes, self.block_table,
                               self.n_held, self.ring, self.ring_state,
                               depth=depth)

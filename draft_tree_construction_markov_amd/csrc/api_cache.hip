@@ -26,6 +26,12 @@ pct_status hip_fail(hipError_t e, const char* what) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// two arrays of n values each that share memory (a null pointer has none)
+bool overlap(const int32_t* x, const int32_t* y, int n) {
+  const uintptr_t p = (uintptr_t)x, q = (uintptr_t)y, bytes = (uintptr_t)n * 4;
+  return x && y && p < q + bytes && q < p + bytes;
+}
+
 int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
 
 pct_status check_pages(const pct_cache_shape* sh) {
@@ -85,18 +91,20 @@ size_t pct_cache_plan_workspace(int32_t batch) {
   return batch < 1 || batch > 65535 ? 0 : ((size_t)batch + 1) * sizeof(int4);
 }
 
-pct_status pct_cache_plan(const pct_cache_shape* shape,
-                          const int32_t* ctx_len, const int32_t* n_nodes,
-                          const int32_t* depth, int32_t* block_table,
-                          int32_t* n_held, int32_t* ring,
-                          int32_t* ring_state, int64_t* slot, int32_t* pos,
-                          int32_t* missing, void* workspace,
-                          size_t workspace_bytes, void* stream) {
+pct_status pct_cache_plan_served(
+    const pct_cache_shape* shape, const int32_t* ctx_len,
+    const int32_t* n_nodes, const int32_t* depth, int32_t* block_table,
+    int32_t* n_held, int32_t* ring, int32_t* ring_state, int64_t* slot,
+    int32_t* pos, int32_t* missing, int32_t* n_served, void* workspace,
+    size_t workspace_bytes, void* stream) {
   pct_status st = check_pages(shape);
   if (st != PCT_OK) return st;
   if (!ctx_len || !block_table || !n_held || !ring || !ring_state || !slot ||
       !missing || (pos && shape->N > 0 && !depth))
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
+  if (n_served && (overlap(n_served, n_nodes, shape->batch) ||
+                   overlap(n_served, ctx_len, shape->batch)))
+    return fail(PCT_ERR_INVALID_ARG, "n_served overlaps n_nodes or ctx_len");
   const size_t need = pct_cache_plan_workspace(shape->batch);
   if (!workspace || workspace_bytes < need)
     return fail(PCT_ERR_WORKSPACE, "workspace needs %zu bytes", need);
@@ -112,6 +120,7 @@ pct_status pct_cache_plan(const pct_cache_shape* shape,
   a.slot = slot;
   a.pos = pos;
   a.missing = missing;
+  a.served = n_served;
   a.req = static_cast<int4*>(workspace);
   a.ring0 = reinterpret_cast<int2*>(a.req + shape->batch);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -122,6 +131,18 @@ pct_status pct_cache_plan(const pct_cache_shape* shape,
   }
   if (e != hipSuccess) return hip_fail(e, "cache plan kernel");
   return PCT_OK;
+}
+
+pct_status pct_cache_plan(const pct_cache_shape* shape,
+                          const int32_t* ctx_len, const int32_t* n_nodes,
+                          const int32_t* depth, int32_t* block_table,
+                          int32_t* n_held, int32_t* ring,
+                          int32_t* ring_state, int64_t* slot, int32_t* pos,
+                          int32_t* missing, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  return pct_cache_plan_served(shape, ctx_len, n_nodes, depth, block_table,
+                               n_held, ring, ring_state, slot, pos, missing,
+                               nullptr, workspace, workspace_bytes, stream);
 }
 
 pct_status pct_cache_write(const pct_cache_shape* shape, const void* k,

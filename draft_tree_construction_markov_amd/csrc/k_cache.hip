@@ -81,11 +81,11 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
     __syncthreads();
     const int b = b0 + tid;
     const bool in = b < g.batch;
-    int held = 0;
+    int held = 0, n = -1;
     int64_t need = 0;
     if (in) {
       held = min(max(a.held[b], 0), g.max_pages);
-      const int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
+      n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
       need = pages_for((int64_t)clamp_ctx(g.ctx_len[b]) + n + 1, g.shift);
     }
     const int to = (int)min(need, (int64_t)g.max_pages);
@@ -104,6 +104,7 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a) {
                            after);
       a.held[b] = after;
       a.missing[b] = (int)(need - after);
+      if (a.served) a.served[b] = need > after ? -1 : n;
       // the last request that is served has the largest sum
       if (fits && (tid & 63) == 63 - __builtin_clzll(__ballot(fits)))
         atomicMax((unsigned long long*)&total[2], (unsigned long long)wi);

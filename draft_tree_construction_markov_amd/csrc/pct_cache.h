@@ -28,6 +28,7 @@ struct PlanArgs {
   int32_t *table, *held, *ring, *ring_state;
   int64_t* slot;
   int32_t *pos, *missing;
+  int32_t* served;  // [batch] or null
   int4* req;   // [batch] {first taken, first given back, held before, after}
   int2* ring0; // ring head and count before the call
 };

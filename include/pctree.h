@@ -396,12 +396,20 @@ typedef struct {
  *          for unused rows and for rows whose position has no page
  *  pos     [batch][R] out, optional: the row's place in its sequence,
  *          ctx_len + its depth (the root's is 0), -1 for unused rows
- *  missing [batch] out: pages needed and not held
+ *  missing [batch] out: pages needed and not held.  A request that misses
+ *          pages has rows without a slot, which are neither written nor
+ *          attended: this round must not be kept (its positions would hold
+ *          whatever their pages held before).  It waits for a later round.
+ *  n_served [batch] out (pct_cache_plan_served): the n_nodes of the round's
+ *          pct_tree_attention and pct_cache_commit, which leave out the
+ *          requests that wait: n_nodes, or -1 where missing > 0.  What the
+ *          acceptance walk answers for those is not used.  NULL: not written
  *  workspace  pct_cache_plan_workspace(batch) bytes
  * Only batch, N, n_pages, page_size and max_pages of the shape are read.
  * Precondition (not checked): ring and block_table hold every page once.
- * Errors: PCT_ERR_INVALID_ARG for a size outside its range or null required
- * pointers; PCT_ERR_UNSUPPORTED for batch > 65535; PCT_ERR_WORKSPACE. */
+ * Errors: PCT_ERR_INVALID_ARG for a size outside its range, null required
+ * pointers or an n_served that overlaps n_nodes or ctx_len;
+ * PCT_ERR_UNSUPPORTED for batch > 65535; PCT_ERR_WORKSPACE. */
 size_t pct_cache_plan_workspace(int32_t batch);
 pct_status pct_cache_plan(const pct_cache_shape* shape /*host*/,
                           const int32_t* ctx_len, const int32_t* n_nodes,
@@ -410,6 +418,12 @@ pct_status pct_cache_plan(const pct_cache_shape* shape /*host*/,
                           int32_t* ring_state, int64_t* slot, int32_t* pos,
                           int32_t* missing, void* workspace,
                           size_t workspace_bytes, void* stream);
+pct_status pct_cache_plan_served(
+    const pct_cache_shape* shape /*host*/, const int32_t* ctx_len,
+    const int32_t* n_nodes, const int32_t* depth, int32_t* block_table,
+    int32_t* n_held, int32_t* ring, int32_t* ring_state, int64_t* slot,
+    int32_t* pos, int32_t* missing, int32_t* n_served, void* workspace,
+    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * pct_cache_write -- a layer's keys and values of the round's rows into

@@ -1,6 +1,7 @@
-"""CPU pins of the second 64-bit definition of attention that GPU tests compare
-with: it gives what the first one gives, and its comparison lets no wrong
-value pass."""
+"""CPU checks beside those of the paged-cache calls: the second 64-bit
+definition of attention gives what the first one gives, its comparison lets no
+wrong value pass, and the plan's served nodes are checked."""
+import ctypes as C
 import math
 
 import numpy as np
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 import cachestrict
+import draft_tree_construction_markov_amd as pct
 from cacheref import Case
 
 
@@ -57,3 +59,24 @@ def test_the_comparison_lets_nothing_pass():
     tol[0] = math.inf  # a tolerance that is none
     with pytest.raises(AssertionError):
         cachestrict.agree(want, want, tol, "tolerance")
+
+
+def served(n_served, **kw):
+    sh = pct.CacheShape(2, 8, 10, 16, 4, 4, 2, 64, pct.PCT_BF16)
+    p = dict(ctx=4096, n=8192, depth=256, table=256, held=256, ring=256,
+             state=256, slot=256, pos=256, missing=256)
+    p.update(kw)
+    return pct.lib().pct_cache_plan_served(
+        C.byref(sh), *(C.c_void_p(x) for x in p.values()),
+        C.c_void_p(n_served), C.c_void_p(256), 16, None)
+
+
+def test_served_nodes_do_not_overlap_what_is_read():
+    # (16 bytes of workspace are too few: a call that passes the checks of
+    # its arguments ends there, before anything is enqueued)
+    for bad in (4096, 4100, 4092, 8192, 8188, 8196):
+        assert served(bad) == 1, bad
+    for good in (None, 4096 + 8, 4096 - 8, 8192 + 8, 256):
+        assert served(good) == 3, good
+    assert served(0x10000, n=None) == 3
+    assert served(0x10000, missing=None) == 1

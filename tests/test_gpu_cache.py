@@ -300,3 +300,98 @@ def test_a_write_before_the_first_plan_leaves_the_cache():
     cache.write(0, k, k)
     torch.cuda.synchronize()
     assert not cache.k.any() and not cache.v.any()
+
+
+def test_requests_without_pages_wait_and_go_on():
+    """A cache that is too small for its batch: a request that the free ring
+    cannot serve keeps its length and its root until pages are given back.
+    Whatever was not written, and every page that is given back, is NaN."""
+    rng = np.random.default_rng(31)
+    batch, N, page, P, layers, Hq, Hkv, D, V = 3, 3, 4, 8, 2, 2, 1, 32, 60
+    dtype = torch.bfloat16
+    cache = pct.PagedCache(batch, N, P, page, 6, Hq, Hkv, D, layers=layers,
+                           dtype=dtype)
+    cache.k.fill_(math.nan), cache.v.fill_(math.nan)
+    emb = torch.from_numpy(rng.standard_normal((layers, 2, V, Hkv, D)))
+    emb = emb.to(dtype).cuda()
+    depth = torch.arange(1, N + 1, device="cuda").int().repeat(batch, 1)
+    text = [[] for _ in range(batch)]
+    root = rng.integers(0, V, batch)
+    waited, went_on = np.zeros(batch, bool), 0
+    for turn in range(24):
+        n = np.full(batch, N)
+        gone = []
+        if turn % 4 == 3:  # the longest request ends, its place is free
+            b = max(range(batch), key=lambda x: len(text[x]))
+            gone = [x for x in cache.block_table[b].tolist() if x >= 0]
+            cache.ctx_len[b], n[b], text[b], waited[b] = 0, -1, [], False
+        draft = rng.integers(0, V, (batch, N))
+        announce("waiting round", turn)
+        missing = cache.plan(dev_i32(n), depth).missing.tolist()
+        if gone:
+            cache.k[:, gone], cache.v[:, gone] = math.nan, math.nan
+        tok = torch.from_numpy(np.c_[root, draft]).cuda()
+        q = torch.from_numpy(rng.standard_normal((batch, N + 1, Hq, D)))
+        q = q.to(dtype).cuda()
+        outs = []
+        for layer in range(layers):
+            cache.write(layer, emb[layer, 0][tok], emb[layer, 1][tok])
+            outs.append(cache.attend(layer, q).clone())
+        taken = rng.integers(0, N + 1, batch)  # whatever the walk answers
+        acc = np.where(np.arange(N) < taken[:, None], np.arange(N), -1)
+        cache.commit(dev_i32(taken + 1), dev_i32(acc))
+        torch.cuda.synchronize()
+        for b in range(batch):
+            if n[b] < 0:
+                continue
+            if missing[b] > 0:
+                waited[b] = True
+                continue
+            went_on += int(waited[b])
+            waited[b] = False
+            for i in range(N + 1):
+                see = text[b] + [root[b]] + draft[b, :i].tolist()
+                for layer in range(layers):
+                    kk = emb[layer, 0][see].double()[:, 0]
+                    vv = emb[layer, 1][see].double()[:, 0]
+                    for h in range(Hq):
+                        z = kk @ q[b, i, h].double() * D ** -0.5
+                        p = torch.softmax(z, 0)
+                        # two roundings; fp32 sums of some 20 terms of scores
+                        # below 16 are far below a third one
+                        tol = 3 * HALF_STEP[dtype] * (p @ vv.abs())
+                        got = outs[layer][b, i, h].double()
+                        assert ((got - p @ vv).abs() <= tol).all()
+            text[b] += [root[b]] + draft[b, :taken[b]].tolist()
+            root[b] = rng.integers(0, V)
+        assert cache.ctx_len.tolist() == [len(x) for x in text], turn
+    assert went_on >= 2
+
+
+@pytest.mark.parametrize("batch,N,P", [(5, 7, 6), (90, 30, 200),
+                                       (1030, 3, 900)])
+@pytest.mark.parametrize("given", [False, True])
+def test_served_nodes(batch, N, P, given):
+    rng = np.random.default_rng(batch)
+    h = pct.CachePlan(batch, N, P, 8, 20)
+    s = PlanState(rng, batch, 20, P)
+    some = 0
+    announce("served nodes", (batch, N, P, given))
+    for turn in range(3):
+        ctx = rng.integers(0, 200, batch)
+        n = rng.integers(-1, N + 1, batch) if given else np.full(batch, N)
+        s.step(h, ctx, n, N, 8, np.ones((batch, N), np.int32), given=given)
+        missing = h.out.missing.cpu().numpy()
+        same(h.out.n_served, np.where(missing > 0, -1, n), "n_served")
+        some += int((missing > 0).sum())
+    assert some > 0
+
+
+def test_a_round_without_a_plan_attends_and_keeps_nothing():
+    cache = pct.PagedCache(2, 3, 8, 16, 4, 4, 2, 32)
+    q = torch.ones(2, 4, 4, 32, dtype=torch.bfloat16, device="cuda")
+    announce("no plan")
+    assert not cache.attend(0, q).any()
+    cache.commit(dev_i32([3, 1]), dev_i32([[0, 1, -1], [-1, -1, -1]]))
+    torch.cuda.synchronize()
+    assert cache.ctx_len.tolist() == [0, 0]
