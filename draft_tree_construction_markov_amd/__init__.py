@@ -676,7 +676,7 @@ class TreeAttention:
         if nbytes == 0:
             raise PCTError(1, lib().pct_last_error().decode())
         self.ws = _workspace(nbytes, dev)
-        # unused rows are never written: they stay zero
+        # a call writes the rows it uses: those that none has used stay zero
         self.out = torch.zeros(batch, N + 1, Hq, D, dtype=dtype, device=dev)
         self.lse = (torch.zeros(batch, N + 1, Hq, dtype=torch.float32,
                                 device=dev) if lse else None)
@@ -693,7 +693,11 @@ class TreeAttention:
         """q [batch][N+1][Hq][D] (a view with evenly spaced rows allowed),
         mask [batch][N][ceil(N/64)] int64 or None (straight drafts); scale
         defaults to 1/sqrt(D).  Returns (out, lse), lse None unless the
-        handle keeps it; out: another tensor for the outputs."""
+        handle keeps it; out: another tensor for the outputs.
+
+        The handle's tensors are written by every call: clone what is needed
+        past the next one.  Rows past n_nodes are left as they were: they
+        hold what an earlier call wrote there, or zeros."""
         dev, dt, i32 = self.device.index, self.dtype, torch.int32
         rows, cache, pages, one, words = self._shapes
         if out is None:
@@ -805,6 +809,9 @@ class PagedCache:
         cache_write(k, v, self._plan.out.slot, self.k[layer], self.v[layer])
 
     def attend(self, layer: int, q, mask=None, scale=None, out=None):
+        """The layer's attention, in `out` when given, else in a tensor that
+        every call without `out` writes, whatever its layer.  Unused rows,
+        and those of requests that wait, are left as they were there."""
         return self._attend.run(q, self.k[layer], self.v[layer],
                                 self.block_table, self.ctx_len, self.n_nodes,
                                 mask=mask, scale=scale, out=out)[0]

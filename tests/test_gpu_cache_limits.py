@@ -1,5 +1,5 @@
 """GPU checks of pct_tree_attention where a form of its kernels can go wrong by
-itself: contexts longer than the block table and many small probabilities."""
+itself: contexts longer than the block table, many small probabilities, rows that a later call does not use."""
 import numpy as np
 import pytest
 import torch
@@ -86,3 +86,38 @@ def test_many_small_probabilities(dtype, N, G, down, at):
     some = [0, 41]  # requests that are compared
     c.batch, c.q = len(some), c.q[some]
     compare(c, out[some], lse[some])
+
+
+# ---------------------------------------------------------------------------
+# one handle, call after call
+
+@pytest.mark.parametrize("N,G", [(3, 2), (12, 4), (40, 4)])
+def test_rows_that_a_later_call_does_not_use_keep_the_earlier_values(N, G):
+    first = Case(1, 2, N, 2 * G, 2, 64, 16, [70, 33])
+    then = Case(2, 2, N, 2 * G, 2, 64, 16, [70, 33], n=[N // 3, -1])
+    width = first.table.shape[1]
+    then.table = np.pad(then.table, ((0, 0), (0, width - then.table.shape[1])),
+                        constant_values=-1)
+    h = handle(first)
+    announce("fewer rows", (N, G))
+    q, k, v, table, ctx, n, mask = device_args(first)
+    out, lse = h.run(q, k, v, table, ctx, n, mask=mask)
+    torch.cuda.synchronize()
+    compare(first, out, lse)
+    kept = out.clone(), lse.clone()
+    # the second case's pages behind the first one's
+    q, k2, v2, table2, ctx, n, mask = device_args(then)
+    P = first.n_pages
+    kv = [x.clone() for x in (k, v)]
+    assert then.n_pages <= P
+    for x, y in zip(kv, (k2, v2)):
+        x[:then.n_pages] = y
+    again, lse2 = h.run(q, *kv, table2, ctx, n, mask=mask)
+    torch.cuda.synchronize()
+    assert again is out and lse2 is lse
+    for b in range(2):
+        m = int(then.n[b]) + 1
+        assert torch.equal(out[b, m:], kept[0][b, m:])
+        assert torch.equal(lse[b, m:], kept[1][b, m:])
+        out[b, m:], lse[b, m:] = 0, 0
+    compare(then, out, lse)
