@@ -213,8 +213,10 @@ pct_status pct_tree_attention(const pct_cache_shape* shape, float scale,
   if (st != PCT_OK) return st;
   if (!q || !k_cache || !v_cache || !block_table || !ctx_len || !out)
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
-  if (!isfinite(scale))
-    return fail(PCT_ERR_INVALID_ARG, "scale must be finite");
+  // (infinite for the largest scales: every score would be infinite or NaN)
+  const float c = fabsf(scale) * 1.44269504f;
+  if (!isfinite(c))
+    return fail(PCT_ERR_INVALID_ARG, "scale * log2(e) must be finite");
   if (q_row_stride < (int64_t)shape->Hq * shape->D || q_row_stride % 8 != 0)
     return fail(PCT_ERR_INVALID_ARG,
                 "q_row_stride must be a multiple of 8 and at least Hq * D");
@@ -232,7 +234,7 @@ pct_status pct_tree_attention(const pct_cache_shape* shape, float scale,
   a.Hq = shape->Hq;
   a.G = shape->Hq / shape->Hkv;
   a.bf16 = shape->dtype == PCT_BF16;
-  a.c = scale == 0.f ? 1.f : fabsf(scale) * 1.44269504f;
+  a.c = scale == 0.f ? 1.f : c;
   a.qand = scale == 0.f ? 0u : ~0u;
   a.qxor = scale < 0.f ? 0x80008000u : 0u;
   a.q = q;

@@ -462,9 +462,9 @@ pct_status pct_cache_write(const pct_cache_shape* shape /*host*/,
  *  out     [batch][R][Hq][D]; lse [batch][R][Hq] optional.  Unused rows
  *          are left as they were.
  *  workspace  pct_tree_attention_workspace(shape) bytes
- * Errors: PCT_ERR_INVALID_ARG for sizes, null pointers, a scale that is not
- * finite, a stride below Hq * D or not a multiple of 8, pointers that are
- * not 16-byte aligned; PCT_ERR_UNSUPPORTED for batch > 65535;
+ * Errors: PCT_ERR_INVALID_ARG for sizes, null pointers, a scale whose
+ * product with log2(e) is not finite, a stride below Hq * D or not a multiple
+ * of 8, pointers that are not 16-byte aligned; PCT_ERR_UNSUPPORTED for batch > 65535;
  * PCT_ERR_WORKSPACE. */
 size_t pct_tree_attention_workspace(const pct_cache_shape* shape /*host*/);
 pct_status pct_tree_attention(const pct_cache_shape* shape /*host*/,

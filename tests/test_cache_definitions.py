@@ -1,6 +1,6 @@
 """CPU checks beside those of the paged-cache calls: the second 64-bit
 definition of attention gives what the first one gives, its comparison lets no
-wrong value pass, and the plan's served nodes are checked."""
+wrong value pass, and refusals of arguments."""
 import ctypes as C
 import math
 
@@ -80,3 +80,19 @@ def test_served_nodes_do_not_overlap_what_is_read():
         assert served(good) == 3, good
     assert served(0x10000, n=None) == 3
     assert served(0x10000, missing=None) == 1
+
+
+def attend(scale):
+    sh = pct.CacheShape(2, 8, 10, 16, 4, 4, 2, 64, pct.PCT_BF16)
+    p = C.c_void_p(256)
+    return pct.lib().pct_tree_attention(
+        C.byref(sh), scale, p, 256, p, p, p, p, None, None, p, None, p, 16,
+        None)
+
+
+def test_scales_whose_product_with_log2_e_is_not_finite():
+    # scores are taken to base 2: 3.4e38 / 1.4427 = 2.36e38
+    for bad in (2.4e38, -2.4e38, 3.4e38):
+        assert attend(bad) == 1, bad
+    for good in (2.3e38, -2.3e38, 0.0, 1e-45):
+        assert attend(good) == 3, good  # (too little workspace)
