@@ -26,10 +26,10 @@ pct_status hip_fail(hipError_t e, const char* what) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// two arrays of n values each that share memory (a null pointer has none)
-bool overlap(const int32_t* x, const int32_t* y, int n) {
-  const uintptr_t p = (uintptr_t)x, q = (uintptr_t)y, bytes = (uintptr_t)n * 4;
-  return x && y && p < q + bytes && q < p + bytes;
+// arrays of n and m values that share memory (a null pointer has none)
+bool overlap(const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
+  const uintptr_t p = (uintptr_t)x, q = (uintptr_t)y;
+  return x && y && p < q + 4 * (uintptr_t)m && q < p + 4 * (uintptr_t)n;
 }
 
 int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
@@ -102,8 +102,8 @@ pct_status pct_cache_plan_served(
   if (!ctx_len || !block_table || !n_held || !ring || !ring_state || !slot ||
       !missing || (pos && shape->N > 0 && !depth))
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
-  if (n_served && (overlap(n_served, n_nodes, shape->batch) ||
-                   overlap(n_served, ctx_len, shape->batch)))
+  if (overlap(n_served, shape->batch, n_nodes, shape->batch) ||
+      overlap(n_served, shape->batch, ctx_len, shape->batch))
     return fail(PCT_ERR_INVALID_ARG, "n_served overlaps n_nodes or ctx_len");
   const size_t need = pct_cache_plan_workspace(shape->batch);
   if (!workspace || workspace_bytes < need)
@@ -273,11 +273,16 @@ pct_status pct_cache_commit(const pct_cache_shape* shape, int32_t layers,
   if (layer_stride % 8 != 0 || (layers > 1 && layer_stride < layer))
     return fail(PCT_ERR_INVALID_ARG,
                 "layer_stride must be a multiple of 8 and hold a layer");
+  const int64_t n = shape->batch;
+  if (ctx_out != ctx_len && overlap(ctx_out, n, ctx_len, n))
+    return fail(PCT_ERR_INVALID_ARG, "ctx_out overlaps ctx_len");
+  // (workgroups of a request read these after one of them wrote its length)
+  if (overlap(ctx_out, n, tau, n) || overlap(ctx_out, n, n_nodes, n) ||
+      overlap(ctx_out, n, accept_node, n * B))
+    return fail(PCT_ERR_INVALID_ARG,
+                "ctx_out overlaps tau, accept_node or n_nodes");
   if (!aligned16(k_cache) || !aligned16(v_cache))
     return fail(PCT_ERR_INVALID_ARG, "caches must be 16-byte aligned");
-  if (ctx_out != ctx_len && ctx_out < ctx_len + shape->batch &&
-      ctx_len < ctx_out + shape->batch)
-    return fail(PCT_ERR_INVALID_ARG, "ctx_out overlaps ctx_len");
   CommitArgs a{};
   a.g = geom(shape, block_table, ctx_len, n_nodes);
   a.layers = layers;

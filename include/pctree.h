@@ -493,8 +493,8 @@ pct_status pct_tree_attention(const pct_cache_shape* shape /*host*/,
  * Needs no workspace.
  * Errors: PCT_ERR_INVALID_ARG for sizes, null pointers, caches that are not
  * 16-byte aligned, a layer_stride that is too short or not a multiple of 8,
- * a ctx_out that overlaps ctx_len without being it; PCT_ERR_UNSUPPORTED for
- * batch > 65535. */
+ * a ctx_out that overlaps ctx_len without being it, or tau, accept_node or
+ * n_nodes; PCT_ERR_UNSUPPORTED for batch > 65535. */
 pct_status pct_cache_commit(const pct_cache_shape* shape /*host*/,
                             int32_t layers, int64_t layer_stride, int32_t B,
                             const int32_t* tau, const int32_t* accept_node,

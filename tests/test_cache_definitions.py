@@ -96,3 +96,26 @@ def test_scales_whose_product_with_log2_e_is_not_finite():
         assert attend(bad) == 1, bad
     for good in (2.3e38, -2.3e38, 0.0, 1e-45):
         assert attend(good) == 3, good  # (too little workspace)
+
+
+def commit(out, ctx=4096, n=8192, tau=0x10000, accept=0x20000, B=4):
+    sh = pct.CacheShape(2, 8, 10, 16, 4, 4, 2, 64, pct.PCT_BF16)
+    p = C.c_void_p
+    return pct.lib().pct_cache_commit(
+        C.byref(sh), 1, 0, B, p(tau), p(accept), p(n), p(256), p(ctx),
+        p(0x1001), p(256), p(out), None)
+
+
+def test_new_lengths_do_not_overlap_what_is_read():
+    # (the cache's address is odd: a call that passes the overlaps' checks
+    # would still be refused, so the messages tell them apart)
+    def refused(*a, **kw):
+        assert commit(*a, **kw) == 1
+        return b"overlaps" in pct.lib().pct_last_error()
+
+    for bad in (8192, 8188, 8196, 0x10000, 0x10004, 0xfffc, 0x20000, 0x2001c,
+                0x1fffc, 4092, 4100):
+        assert refused(bad), hex(bad)
+    for good in (4096, 8184, 8200, 0x10008, 0xfff8, 0x20020, 0x1fff8):
+        assert not refused(good), hex(good)
+    assert not refused(8192, n=None)
