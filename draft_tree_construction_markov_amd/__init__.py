@@ -733,10 +733,11 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes=None,
 
 
 def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
-                 v_cache, out=None):
+                 v_cache, out=None, N: int = 8192):
     """Keep the accepted paths: tau [batch] and accept_node [batch][B] as
-    verify_accept returns them, n_nodes [batch] or None (no padded request),
-    k_cache, v_cache [layers][n_pages][Hkv][page_size][D] (or one layer).
+    verify_accept returns them, n_nodes [batch] or None (N in every request),
+    N the trees' largest size (the first accepted node outside a tree ends
+    the moves), k_cache, v_cache [layers][n_pages][Hkv][page_size][D] (or one layer).
     Returns the new context lengths, in `out` when given (which may be
     ctx_len itself)."""
     dev = k_cache.get_device()
@@ -750,9 +751,7 @@ def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
     dt, i32, one = k_cache.dtype, torch.int32, (batch,)
     if out is None:
         out = torch.empty_like(ctx_len)
-    # the rows are not read: any number of nodes up to the largest may be
-    # accepted
-    sh = _shape_ref(batch, 8192, n_pages, page, width, Hkv, Hkv, D,
+    sh = _shape_ref(batch, N, n_pages, page, width, Hkv, Hkv, D,
                     _cache_dtype(dt))
     _enqueue(lib().pct_cache_commit, dev, sh, layers,
              n_pages * Hkv * page * D, B, _want("tau", tau, i32, one, dev),
@@ -819,7 +818,7 @@ class PagedCache:
     def commit(self, tau, accept_node):
         return cache_commit(tau, accept_node, self.ctx_len, self.n_nodes,
                             self.block_table, self.k, self.v,
-                            out=self.ctx_len)
+                            out=self.ctx_len, N=self._plan.shape.N)
 
 
 def bf16_tensor(bits, device="cuda") -> torch.Tensor:

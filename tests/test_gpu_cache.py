@@ -395,3 +395,21 @@ def test_a_round_without_a_plan_attends_and_keeps_nothing():
     cache.commit(dev_i32([3, 1]), dev_i32([[0, 1, -1], [-1, -1, -1]]))
     torch.cuda.synchronize()
     assert cache.ctx_len.tolist() == [0, 0]
+
+
+def test_commit_stops_at_a_node_outside_trees_of_equal_size():
+    rng = np.random.default_rng(10)
+    ctx = np.array([3, 6])
+    table, k, v, tau, acc = commit_inputs(rng, 2, 30, 5, 8, 2, 2, 32, ctx)
+    tau[:] = 5, 6
+    acc[0] = [1, 4, 9, 10, -1]  # of trees of 9 nodes: the first two
+    acc[1] = [0, 2, 5, 8, 29]   # all but the last
+    k, v = k.half().cuda(), v.half().cuda()
+    wk, wv, _ = committed(table, k, v, np.array([3, 5]), acc, ctx,
+                          np.array([9, 9]), 8)
+    announce("commit outside, equal sizes")
+    got = pct.cache_commit(dev_i32(tau), dev_i32(acc), dev_i32(ctx), None,
+                           dev_i32(table), k, v, N=9)
+    torch.cuda.synchronize()
+    assert got.tolist() == [8, 12]
+    assert torch.equal(k, wk) and torch.equal(v, wv)
