@@ -450,7 +450,8 @@ pct_status pct_cache_write(const pct_cache_shape* shape /*host*/,
  * set of seen positions that have a page,
  *   out = sum_{t in S} softmax_S(scale * q . k_t) v_t,
  *   lse = ln sum_{t in S} exp(scale * q . k_t);
- * an empty S gives out = 0 and lse = -inf.  Positions outside a row's S have
+ * an empty S, and one whose scores are all -inf, gives out = 0 and lse =
+ * -inf.  Positions outside a row's S have
  * no influence on it, whatever the cache holds there (NaN included).
  * Scores, normalisers and sums are fp32; a probability (in fp16 2^7 times
  * it, which keeps those down to 2^-32 of the largest) is rounded to the

@@ -1,5 +1,9 @@
 """GPU checks of pct_tree_attention where a form of its kernels can go wrong by
-itself: contexts longer than the block table, many small probabilities, rows that a later call does not use."""
+itself: contexts longer than the block table, many small probabilities, rows that a later call does not use,
+values and scores that are not finite in every form of the kernels, long
+drafts and large trees."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -7,7 +11,7 @@ import torch
 from cacheref import Case
 from cachestrict import compare
 from gpu_util import announce
-from test_gpu_cache_attention import device_args, handle
+from test_gpu_cache_attention import device_args, handle, wide
 
 pytestmark = pytest.mark.gpu
 BF16, FP16 = torch.bfloat16, torch.float16
@@ -121,3 +125,114 @@ def test_rows_that_a_later_call_does_not_use_keep_the_earlier_values(N, G):
         assert torch.equal(lse[b, m:], kept[1][b, m:])
         out[b, m:], lse[b, m:] = 0, 0
     compare(then, out, lse)
+
+
+# ---------------------------------------------------------------------------
+# values and keys that are not finite, in every form of the kernels
+
+# at most 16 rows of a head; row tiles of 64; of 128
+FORMS = [(7, 2, False), (3, 4, False), (15, 1, False), (30, 2, False),
+         (75, 4, False), (75, 4, True)]
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("N,G,long_table", FORMS)
+def test_nodes_that_are_not_finite_reach_their_descendants_only(
+        what, dtype, D, N, G, long_table):
+    c = Case(D + N, 2, N, 2 * G, 2, D, 16, [45, 127], n=[N, N - 2],
+             dtype=dtype)
+    nodes = sorted({N // 2, N - 1})  # the first nodes do not see them
+    for b in range(2):
+        for i in nodes:
+            t = int(c.ctx[b]) + 1 + i
+            c.v[c.table[b, t // 16], i % 2, t % 16, 5 + i % 8:19] = what
+    reached = c.anc[0][:, nodes].any(-1)
+    assert reached.any() and not reached.all()
+    check(wide(c) if long_table else c, "values", what)
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("N,G,long_table", FORMS)
+def test_keys_that_are_not_finite_reach_their_descendants_only(
+        what, D, N, G, long_table):
+    c = Case(D + N, 2, N, 2 * G, 2, D, 16, [45, 127], n=[N, N - 2])
+    for b in range(2):
+        t = int(c.ctx[b]) + 1 + N // 2
+        c.k[c.table[b, t // 16], :, t % 16, 3] = what
+    # (an infinite key gives scores of either sign: exp(inf - inf) where it
+    # is the largest, weight 0 where it is the least)
+    check(wide(c) if long_table else c, "keys", what)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("N,G,long_table", FORMS)
+@pytest.mark.parametrize("ctx", [40, 4000])  # in one run; over several
+def test_scores_of_minus_infinity(D, N, G, long_table, ctx):
+    # rows that see such scores only are as rows that see nothing; one key
+    # with another score takes all the weight
+    c = Case(D + N, 2, N, 2 * G, 2, D, 16, [ctx, ctx])
+    c.q[..., 0] = 1.0
+    t = np.arange(ctx + N + 1)
+    for b in range(2):
+        p = torch.from_numpy(c.table[b][t // 16].astype(np.int64))
+        c.k[p, :, t % 16, 0] = -math.inf
+    key = ctx // 3
+    p, o = c.table[1, key // 16], key % 16
+    c.k[p, :, o, 0] = 0.5
+    h = handle(wide(c) if long_table else c)
+    q, k, v, table, n_ctx, n, mask = device_args(c)
+    announce("scores of -inf", (D, N, G, long_table, ctx))
+    out, lse = h.run(q, k, v, table, n_ctx, n, mask=mask)
+    torch.cuda.synchronize()
+    assert not out[0].any()
+    assert (lse[0] == -math.inf).all()
+    want = v[p, :, o].repeat_interleave(G, 0).expand_as(out[1])
+    assert torch.equal(out[1], want)
+    assert torch.isfinite(lse[1]).all()
+
+
+@pytest.mark.parametrize("where", [0, 50, 100])
+@pytest.mark.parametrize("D", [64, 192])
+@pytest.mark.parametrize("N,G,long_table", FORMS)
+def test_context_values_that_are_not_finite_reach_every_row(where, D, N, G,
+                                                            long_table):
+    c = Case(D + N, 1, N, 2 * G, 2, D, 16, [100])
+    c.v[c.table[0, where // 16], :, where % 16, 9] = math.inf
+    check(wide(c) if long_table else c, "context", where)
+
+
+@pytest.mark.parametrize("D", [160, 192, 256])
+@pytest.mark.parametrize("N", [0, 6, 30, 150])
+@pytest.mark.parametrize("page,drop", [(1, 0.3), (4, 0.5), (16, 0.4),
+                                       (64, 1.0)])
+def test_wide_heads_with_missing_and_small_pages(D, N, page, drop):
+    check(Case(page + D, 3, N, 4, 2, D, page, [3, 90, 270], drop=drop),
+          "pages")
+
+
+@pytest.mark.parametrize("page", [1, 2, 4])
+@pytest.mark.parametrize("N", [5, 60])
+def test_nodes_that_are_not_finite_in_small_pages(N, page):
+    c = Case(page, 2, N, 4, 2, 192, page, [45, 127])
+    for b in range(2):
+        t = int(c.ctx[b]) + 1 + 2
+        c.v[c.table[b, t // page], :, t % page, 7:9] = math.nan
+    check(c, "small pages")
+
+
+# ---------------------------------------------------------------------------
+# long drafts, pieces of prompts and large trees
+
+@pytest.mark.parametrize("N", [1000, 4096, 8192])
+@pytest.mark.parametrize("chain", [False, True])
+@pytest.mark.parametrize("ctx", [0, 777])
+def test_many_rows(N, chain, ctx):
+    check(Case(N, 1, N, 2, 1, 64, 16, [ctx], chain=chain), "many rows")
+
+
+def test_many_rows_of_several_requests():
+    check(Case(7, 3, 2500, 4, 2, 128, 16, [100, 0, 2000],
+               n=[2500, -1, 1311], dtype=FP16), "many rows")
