@@ -413,3 +413,78 @@ def test_commit_stops_at_a_node_outside_trees_of_equal_size():
     torch.cuda.synchronize()
     assert got.tolist() == [8, 12]
     assert torch.equal(k, wk) and torch.equal(v, wv)
+
+
+def test_replayed_rounds_equal_eager_ones():
+    # a round captured once, with the lengths, the pages and the requests that
+    # wait for pages changing from replay to replay
+    rng = np.random.default_rng(44)
+    batch, N, page, P, layers, Hq, Hkv, D, B = 5, 20, 8, 26, 2, 4, 2, 64, 6
+    make = lambda: pct.PagedCache(batch, N, P, page, 12, Hq, Hkv, D,  # noqa: E731
+                                  layers=layers)
+    eager, graph = make(), make()
+    dt = torch.bfloat16
+    buf = dict(n=dev_i32(np.full(batch, N)),
+               depth=dev_i32(np.ones((batch, N))),
+               mask=torch.zeros(batch, N, 1, dtype=torch.int64, device="cuda"),
+               kv=torch.zeros(layers, 2, batch, N + 1, Hkv, D, dtype=dt,
+                              device="cuda"),
+               q=torch.zeros(batch, N + 1, Hq, D, dtype=dt, device="cuda"),
+               tau=dev_i32(np.ones(batch)),
+               acc=dev_i32(np.full((batch, B), -1)))
+
+    def one_round(cache):
+        rows = cache.plan(buf["n"], buf["depth"])
+        out = torch.empty(layers, batch, N + 1, Hq, D, dtype=dt,
+                          device="cuda").zero_()
+        for layer in range(layers):
+            cache.write(layer, *buf["kv"][layer])
+            cache.attend(layer, buf["q"], mask=buf["mask"], out=out[layer])
+        cache.commit(buf["tau"], buf["acc"])
+        return rows, out
+
+    announce("captured rounds")
+    with torch.cuda.stream(torch.cuda.Stream()):
+        one_round(make())  # what is loaded at the first call
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rows2, out2 = one_round(graph)
+    waits = 0
+    for turn in range(12):
+        n = rng.integers(0, N + 1, batch)
+        if turn % 3 == 2:  # a place is emptied
+            b = int(rng.integers(batch))
+            n[b] = -1
+            for cache in (eager, graph):
+                cache.ctx_len[b] = 0
+        _, depth, anc = random_trees(rng, batch, N, n)
+        taken = [int(rng.integers(0, min(B, max(x, 0)) + 1)) for x in n]
+        acc = np.full((batch, B), -1, np.int32)
+        for b, m in enumerate(taken):
+            if m:
+                acc[b, :m] = np.sort(rng.choice(n[b], m, replace=False))
+        for name, x in (("n", dev_i32(n)), ("depth", dev_i32(depth)),
+                        ("mask", torch.from_numpy(pack(anc))),
+                        ("kv", torch.from_numpy(rng.standard_normal(
+                            tuple(buf["kv"].shape)))),
+                        ("q", torch.from_numpy(rng.standard_normal(
+                            tuple(buf["q"].shape)))),
+                        ("tau", dev_i32(np.array(taken) + 1)),
+                        ("acc", dev_i32(acc))):
+            buf[name].copy_(x)
+        rows, out = one_round(eager)
+        g.replay()
+        torch.cuda.synchronize()
+        waits += int((rows.missing > 0).sum())
+        for x, y in ((rows.slot, rows2.slot), (rows.pos, rows2.pos),
+                     (rows.missing, rows2.missing),
+                     (rows.n_served, rows2.n_served), (out, out2),
+                     (eager.ctx_len, graph.ctx_len),
+                     (eager.block_table, graph.block_table),
+                     (eager.ring, graph.ring), (eager.k, graph.k),
+                     (eager.ring_state, graph.ring_state),
+                     (eager.v, graph.v)):
+            assert torch.equal(x, y), turn
+        assert torch.isfinite(out.float()).all()
+    assert waits > 0 and int(eager.ctx_len.max()) > 8
