@@ -130,8 +130,7 @@ __device__ __forceinline__ uint64_t low_bits(int n) {
 
 // Work of one request in units: a step of a row tile.
 struct AttendReq {
-  int ctx, n, L;   // context, nodes, positions (of the block table)
-  int all;         // positions that every row sees: the context and the root
+  int ctx, n, L;   // context, nodes, positions
   int M, RT, KT;   // packed rows, row tiles, steps of a row tile
   int64_t units;   // of all heads and row tiles
 };
@@ -139,10 +138,12 @@ template <int MT, int KS>
 __device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
                                                     int ctx, int n) {
   AttendReq r;
+  // A context that does not fit the block table ends with it: its last
+  // position stands in for the root, and the nodes are past the end.
+  const int cap = a.g.max_pages << a.g.shift;
   r.n = n;
-  r.ctx = ctx;
-  r.L = min(ctx + n + 1, a.g.max_pages << a.g.shift);
-  r.all = min(ctx + 1, r.L);  // (a context may be longer than the table)
+  r.ctx = min(ctx, cap - 1);
+  r.L = min(r.ctx + n + 1, cap);
   r.M = (n + 1) * a.G;
   r.RT = (r.M + MT - 1) / MT;
   r.KT = (r.L + KS - 1) / KS;

@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 
     for (int k = k0; k < k1; ++k) {
       const int t0 = tile_t0(k);
-      const bool tail = t0 + KB > rq.all;  // nodes, or past the end
+      const bool tail = t0 + KB > ctx + 1;  // nodes, or past the end
 
       // ---- the tile from registers to LDS
       uint64_t dead_keys = 0, odd_keys = 0;

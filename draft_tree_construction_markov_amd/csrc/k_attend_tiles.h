@@ -404,7 +404,7 @@ __device__ __forceinline__ void tiles_piece(
   constexpr std::true_type edge{};
   for (int k = k0, par = 0; k < k1;) {
     // tiles of context that every row sees, in a loop of their own
-    while (k < k1 && !holes && (k + 1) * KB <= rq.all) {
+    while (k < k1 && !holes && (k + 1) * KB <= ctx + 1) {
       tile(plain, k, par);
       ++k;
       par ^= 1;
