@@ -6,10 +6,10 @@
 // ahead (its pages two ahead) and past the caches (nothing reads them again),
 // written to the wave's LDS region and read back as operands.  32 rows per
 // wave left no registers for the tile ahead (3.9 TB/s).  Measured with the
-// join: 64 requests of one token over up to 32 k positions (2.0 GB) 322 us,
-// 6.3 TB/s; one over 131 k positions (0.54 GB) 89 us, 6.0 TB/s.  Over 700
-// positions 10 us, none of it bandwidth: schedule 3.6 us with the launch,
-// one tile 4, join 2.3.
+// join: 64 requests of one token over up to 32 k positions (2.0 GB) 321 us,
+// 6.3 TB/s; one over 131 k positions (0.54 GB) 89 us, 6.0 TB/s (loads that do
+// nothing else reach 7.1 on either).  Over 700 positions 10 us, none of it
+// bandwidth: schedule 3.6 us with the launch, one tile 4, join 2.3.
 #pragma once
 #include "k_attend_impl.h"
 

@@ -12,9 +12,9 @@
 // never loaded and stay zero.
 //
 // Measured, D = 128, 4 query heads per key-value head, with the join: 8
-// requests of 256 rows over 33 k positions 1190 us, 924 TFLOP/s (a library's
+// requests of 256 rows over 33 k positions 1144 us, 968 TFLOP/s (a library's
 // 8192^3 product reaches 1160); 32 trees of 257 rows over 512 .. 8192
-// positions 626 us, 597 TFLOP/s of work that counts: the ninth row tile of a
+// positions 633 us, 591 TFLOP/s of work that counts: the ninth row tile of a
 // head has 4 rows, and a tile with nodes takes almost twice the 2.3 us of one
 // without (masks, the search for values that are not finite).  A step of a
 // wave is a chain of products, exponentials and products that two waves per
@@ -41,7 +41,8 @@ struct TilesCfg {
   // Waves, and 16-row blocks of each: two per operand read from LDS, and two
   // waves per SIMD, as long as the registers hold the sums.  (Wide heads: 16
   // requests of 256 rows over 4352 positions, D = 256, 1130 us with 4 waves
-  // of two blocks, one per SIMD, 865 with 8 waves of one; D = 192, 829, 685.)
+  // of two blocks, one per SIMD, 865 (later 814) with 8 waves of one; D = 192,
+  // 829, 685.)
   static constexpr int W = DP > 128 && MT > 64 ? 8 : 4, NT = MT / 16 / W;
   static constexpr bool BF16 = BF16_;
   static constexpr int SL = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;

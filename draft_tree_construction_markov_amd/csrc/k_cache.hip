@@ -21,7 +21,7 @@ namespace pct {
 // for its pages.  Both are bound by the latency of a few dependent loads:
 // 3.5 and 5 us for 128 requests of 513 rows, whose 1 MB takes 0.2.  Plans of
 // few rows and requests run in plan_small, one workgroup that does both (65
-// rows of one request 3.4 us instead of 4.2 for the two launches, 16 x 65
+// rows of one request 3.2 us instead of 4.2 for the two launches, 16 x 65
 // rows 5.2 and 5.8, 64 x 64 rows 9.6 and 6.4; the host's part of a launch is
 // 2.5 us more).
 
@@ -211,7 +211,7 @@ hipError_t launch_cache_plan(const PlanArgs& a, hipStream_t s) {
 // value; consecutive threads take consecutive pieces of a row, so a wave's
 // loads and stores are whole rows.  Bound by memory: 65,664 rows of 8 heads
 // of 128 (538 MB read and written) in 105 us, 5.1 TB/s, what a copy of 1 GiB
-// reaches; 64 rows 2.4 us, the latency of the slot, the row and the store.
+// reaches; 64 rows 2.2 us, the latency of the slot, the row and the store.
 __global__ __launch_bounds__(256) void cache_write_kernel(WriteArgs a) {
   const int hc = a.D / 8, rc = a.Hkv * hc;  // pieces of a head, of a row
   const int64_t total = a.rows * rc;
@@ -249,7 +249,7 @@ hipError_t launch_cache_write(const WriteArgs& a, hipStream_t s) {
 // each other.  Moves onto themselves are left out.  A path of the usual
 // depth is one round of loads: the time is the latency of the chain lengths
 // and nodes -> pages -> rows -> stores, then the bytes (one request of 32
-// layers 3.5 us, 32 requests of 16 layers 7.0 us, 32 MB read and written: 4.6
+// layers 3.2 us, 32 requests of 16 layers 7.0 us, 32 MB read and written: 4.6
 // TB/s).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kMove = 16;
