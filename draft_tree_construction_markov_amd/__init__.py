@@ -584,7 +584,7 @@ class CacheRows:
     slot: torch.Tensor
     pos: torch.Tensor
     missing: torch.Tensor
-    n_served: torch.Tensor
+    n_served: torch.Tensor | None = None
 
 
 class CachePlan:
@@ -774,10 +774,12 @@ class PagedCache:
     A round: rows = plan(n_nodes, depth); in each layer write(layer, k, v)
     and attend(layer, q, mask); then commit(tau, accept_node).  A place is
     emptied by setting its ctx_len to 0 and its n_nodes to -1 for one plan.
+    Before the first plan nothing is written, attended or kept.
 
     A request that the free ring cannot serve (rows.missing > 0) waits: it is
     not attended, and commit leaves its length and its cache as they are
     whatever tau and accept_node say.  It keeps its root for a later round.
+    n_nodes is what the last plan was given, n_served what was served of it.
     """
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
@@ -795,11 +797,13 @@ class PagedCache:
         self.ctx_len = torch.zeros(batch, **i32)
         self._plan = CachePlan(batch, N, n_pages, page_size, max_pages,
                                device=dev)
-        self.n_nodes = self._plan.out.n_served
+        self.n_nodes = None
+        self.n_served = self._plan.out.n_served
         self._attend = TreeAttention(batch, N, Hq, Hkv, D, n_pages, page_size,
                                      max_pages, dtype=dtype, device=dev)
 
     def plan(self, n_nodes=None, depth=None) -> CacheRows:
+        self.n_nodes = n_nodes
         return self._plan.run(self.ctx_len, n_nodes, self.block_table,
                               self.n_held, self.ring, self.ring_state,
                               depth=depth)
@@ -812,11 +816,11 @@ class PagedCache:
         every call without `out` writes, whatever its layer.  Unused rows,
         and those of requests that wait, are left as they were there."""
         return self._attend.run(q, self.k[layer], self.v[layer],
-                                self.block_table, self.ctx_len, self.n_nodes,
+                                self.block_table, self.ctx_len, self.n_served,
                                 mask=mask, scale=scale, out=out)[0]
 
     def commit(self, tau, accept_node):
-        return cache_commit(tau, accept_node, self.ctx_len, self.n_nodes,
+        return cache_commit(tau, accept_node, self.ctx_len, self.n_served,
                             self.block_table, self.k, self.v,
                             out=self.ctx_len, N=self._plan.shape.N)
 

@@ -488,3 +488,16 @@ def test_replayed_rounds_equal_eager_ones():
             assert torch.equal(x, y), turn
         assert torch.isfinite(out.float()).all()
     assert waits > 0 and int(eager.ctx_len.max()) > 8
+
+
+def test_the_next_round_may_be_given_the_last_one_s_nodes():
+    cache = pct.PagedCache(3, 2, 2, 4, 4, 4, 2, 32)
+    n = dev_i32([2, 2, 1])
+    depth = dev_i32([[1, 2]] * 3)
+    announce("same nodes")
+    assert cache.plan(n, depth).missing.tolist() == [0, 0, 1]
+    assert cache.n_nodes is n and cache.n_served.tolist() == [2, 2, -1]
+    rows = cache.plan(cache.n_nodes, depth)
+    torch.cuda.synchronize()
+    assert rows.missing.tolist() == [0, 0, 1] and n.tolist() == [2, 2, 1]
+    assert cache.n_served.tolist() == [2, 2, -1]
