@@ -50,6 +50,14 @@ class CacheShape(C.Structure):
                 ("Hkv", C.c_int32), ("D", C.c_int32), ("dtype", C.c_int32)]
 
 
+class RotaryDesc(C.Structure):
+    _fields_ = [("rot", C.c_int32), ("layout", C.c_int32),
+                ("scaling", C.c_int32), ("original", C.c_int32),
+                ("base", C.c_double), ("factor", C.c_double),
+                ("low", C.c_double), ("high", C.c_double),
+                ("amplitude", C.c_double)]
+
+
 _lib = None
 
 
@@ -101,6 +109,10 @@ def lib():
     L.pct_cache_plan_served.argtypes = [shape, P, P, P, P, P, P, P, P, P, P,
                                         P, P, sz, P]
     L.pct_cache_write.argtypes = [shape, P, i64, P, i64, P, P, P, P]
+    L.pct_rotary_table.argtypes = [C.POINTER(RotaryDesc), P]
+    L.pct_cache_write_rotary.argtypes = [
+        shape, C.POINTER(RotaryDesc), P, C.c_float, P, P, P, i64, P, i64, P,
+        i64, P, P, P, i64, P, P, P]
     L.pct_tree_attention_workspace.argtypes = [shape]
     L.pct_tree_attention_workspace.restype = sz
     L.pct_tree_attention.argtypes = [shape, C.c_float, P, i64, P, P, P, P, P,
@@ -129,6 +141,7 @@ def exported_symbols():
             "pct_tree_mask", "pct_verify_accept",
             "pct_cache_plan", "pct_cache_plan_served",
             "pct_cache_plan_workspace", "pct_cache_write",
+            "pct_rotary_table", "pct_cache_write_rotary",
             "pct_tree_attention", "pct_tree_attention_workspace",
             "pct_cache_commit", "pct_profile_enable",
             "pct_profile_reset", "pct_profile_read", "pct_status_string",
@@ -138,7 +151,7 @@ def exported_symbols():
 PROF_MARKOV, PROF_EXPAND, PROF_TOPN, PROF_MASK, PROF_ACCEPT, PROF_ROWTOP, \
     PROF_INIT, PROF_ROWSTATS, PROF_BESTFIRST, PROF_FINALIZE, PROF_STOP, \
     PROF_SAMPLE, PROF_PLAN, PROF_CACHE_WRITE, PROF_ATTEND, PROF_JOIN, \
-    PROF_COMMIT = range(17)
+    PROF_COMMIT, PROF_ROTARY = range(18)
 
 
 def profile_enable(on: bool = True):
@@ -659,6 +672,111 @@ def cache_write(k, v, slot, k_cache, v_cache):
              _want("v_cache", v_cache, dt, cache, dev))
 
 
+class Rotary:
+    """Rotary positions of heads of D elements: which are rotated and how
+    fast, with the table of frequencies on the device.
+
+    rot: rotated elements, the first of each head (default: all; 0: none).
+    layout: "half" (pairs i, i + rot/2) or "interleaved" (2i, 2i + 1).
+    Pair i turns by base^(-2i/rot) radians per position, for long contexts
+    scaled by `factor`: "linear" (all pairs), "base" (a larger base), "ramp"
+    (slow pairs, by a ramp over the pairs between those that make `high` and
+    `low` turns over `original` positions; 32 and 1), "bands" (slow pairs, by
+    a ramp over their turns; 4 and 1).  amplitude: factor of the rotated
+    elements (default 1; 1 + 0.1 ln(factor) for a "ramp" of factor > 1)."""
+
+    LAYOUTS = ("half", "interleaved")
+    SCALINGS = ("none", "linear", "base", "ramp", "bands")
+
+    def __init__(self, D: int, rot: int | None = None, base: float = 10000.0,
+                 layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original: int = 0,
+                 low: float | None = None, high: float | None = None,
+                 amplitude: float | None = None, device="cuda"):
+        if layout not in self.LAYOUTS:
+            raise ValueError(f"layout must be one of {self.LAYOUTS}")
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {self.SCALINGS}")
+        rot = D if rot is None else rot
+        if rot > D:
+            raise ValueError(f"rot = {rot} exceeds D = {D}")
+        if low is None:
+            low = 1.0
+        if high is None:
+            high = 32.0 if scaling == "ramp" else 4.0
+        if amplitude is None:
+            amplitude = (1.0 + 0.1 * math.log(factor)
+                         if scaling == "ramp" and factor > 1.0 else 1.0)
+        self.D = D
+        self.desc = RotaryDesc(rot, self.LAYOUTS.index(layout),
+                               self.SCALINGS.index(scaling), original, base,
+                               factor, low, high, amplitude)
+        self._ref = C.byref(self.desc)
+        table = torch.zeros(max(rot, 0) // 2, dtype=torch.int64)
+        _check(lib().pct_rotary_table(self._ref, table.data_ptr()))
+        self.table = table.to(_device(device))
+        self._dev = self.table.get_device()
+        self._table = self.table.data_ptr()
+
+
+def cache_write_rotary(rotary: Rotary, q, k, v, pos, slot, k_cache, v_cache,
+                       q_weight=None, k_weight=None, eps: float = 1e-6,
+                       out=None):
+    """Queries q [batch][R][Hq][D] and keys k [batch][R][Hkv][D] (views with
+    evenly spaced rows allowed), normalised if weights [D] (float32) are
+    given, rotated to positions pos [batch][R] int32: keys, with the values
+    v as they are, into slots slot [batch][R] of k_cache, v_cache
+    [n_pages][Hkv][page_size][D], queries into `out` (may be q itself;
+    default: a new tensor of zeros), which is returned.  Rows of negative
+    positions are left out, and `out` keeps what it held there.  q, or k and
+    v, may be None."""
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise ValueError("libpctree needs device tensors")
+    if rotary._dev != dev:
+        raise ValueError(f"the rotary table is on {rotary.table.device}, not "
+                         f"on device {dev}")
+    cache = k_cache.shape
+    n_pages, Hkv, page, D = cache
+    if D != rotary.D:
+        raise ValueError(f"the rotary table is for heads of {rotary.D} "
+                         f"elements, the cache has {D}")
+    if (k is None) != (v is None) or (q is None and k is None):
+        raise ValueError("need q, or k and v, or all of them")
+    batch, R = pos.shape
+    dt = k_cache.dtype
+    kp = vp = qp = op = None
+    ks = vs = qs = os_ = 0
+    Hq = Hkv
+    if q is not None:
+        Hq = q.shape[-2]
+        rows = (batch, R, Hq, D)
+        qp, qs = _rows("q", q, dt, rows, dev)
+        if out is None:
+            out = torch.zeros(rows, dtype=dt, device=q.device)
+        op, os_ = _rows("out", out, dt, rows, dev)
+    if k is not None:
+        rows = (batch, R, Hkv, D)
+        kp, ks = _rows("k", k, dt, rows, dev)
+        vp, vs = _rows("v", v, dt, rows, dev)
+    f32, wide = torch.float32, (D,)
+    _enqueue(lib().pct_cache_write_rotary, dev,
+             _shape_ref(batch, R - 1, n_pages, page, 1, Hq, Hkv, D,
+                        _cache_dtype(dt)),
+             rotary._ref, rotary._table, eps,
+             None if q_weight is None else
+             _want("q_weight", q_weight, f32, wide, dev),
+             None if k_weight is None else
+             _want("k_weight", k_weight, f32, wide, dev),
+             qp, qs, kp, ks, vp, vs,
+             _want("pos", pos, torch.int32, (batch, R), dev),
+             None if k is None else
+             _want("slot", slot, torch.int64, (batch, R), dev),
+             op, os_, _want("k_cache", k_cache, dt, cache, dev),
+             _want("v_cache", v_cache, dt, cache, dev))
+    return out if q is not None else None
+
+
 class TreeAttention:
     """Attention of a round's rows over a paged cache, fixed shape, with its
     workspace and outputs allocated once; run() only enqueues kernels.  Its
@@ -810,6 +928,18 @@ class PagedCache:
 
     def write(self, layer: int, k, v):
         cache_write(k, v, self._plan.out.slot, self.k[layer], self.v[layer])
+
+    def write_rotary(self, layer: int, rotary: Rotary, q, k, v,
+                     q_weight=None, k_weight=None, eps: float = 1e-6,
+                     out=None):
+        """write() of a layer whose queries and keys are normalised (with
+        weights) and rotated to the rows' places on the way; returns the
+        rotated queries (cache_write_rotary)."""
+        o = self._plan.out
+        return cache_write_rotary(rotary, q, k, v, o.pos, o.slot,
+                                  self.k[layer], self.v[layer],
+                                  q_weight=q_weight, k_weight=k_weight,
+                                  eps=eps, out=out)
 
     def attend(self, layer: int, q, mask=None, scale=None, out=None):
         """The layer's attention, in `out` when given, else in a tensor that

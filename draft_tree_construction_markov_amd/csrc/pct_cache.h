@@ -8,7 +8,7 @@ namespace pct {
 
 // profiler kinds after those of ProfKind
 constexpr int PROF_PLAN = 12, PROF_CACHE_WRITE = 13, PROF_ATTEND = 14,
-              PROF_JOIN = 15, PROF_COMMIT = 16;
+              PROF_JOIN = 15, PROF_COMMIT = 16, PROF_ROTARY = 17;
 
 constexpr int kMaxTokens = 1 << 30;  // positions of a request at most
 
@@ -44,6 +44,23 @@ struct WriteArgs {
   uint4 *kc, *vc;
 };
 hipError_t launch_cache_write(const WriteArgs& a, hipStream_t s);
+
+// Rotation of rows on their way into the cache.
+struct RotaryArgs {
+  int64_t rows, n_slots;
+  int shift, Hq, Hkv, D, bf16;
+  int rot;            // rotated elements of a head
+  int pairs;          // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+  const uint64_t* freq;  // [rot / 2] turns per position in units of 2^-64
+  float amp, eps;
+  const float *qw, *kw;  // [D] norm weights or null
+  const void *q, *k, *v;
+  int64_t qs, ks, vs, os;  // row strides in elements
+  const int32_t* pos;
+  const int64_t* slot;
+  void *out, *kc, *vc;
+};
+hipError_t launch_cache_rotary(const RotaryArgs& a, hipStream_t s);
 
 struct CommitArgs {
   PageGeom g;

@@ -443,6 +443,82 @@ pct_status pct_cache_write(const pct_cache_shape* shape /*host*/,
                            void* stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions.  A rotary description says which elements of a head are
+ * rotated and how fast:
+ *  rot      rotated elements, the first ones of each head, even; 0: none
+ *  layout   PCT_ROTARY_HALF: pair i is (i, i + rot/2),
+ *           PCT_ROTARY_INTERLEAVED: (2i, 2i + 1)
+ *  base     pair i turns by f_i = base^(-2i/rot) radians per position
+ *  scaling, factor  for long contexts, with s = factor:
+ *           PCT_ROTARY_PLAIN   f_i
+ *           PCT_ROTARY_LINEAR  f_i / s
+ *           PCT_ROTARY_BASE    base * s^(rot/(rot - 2)) in base's place
+ *           PCT_ROTARY_RAMP    w f_i + (1 - w) f_i / s; w falls linearly with
+ *                              i, from 1 at the pair (rounded down) that makes
+ *                              `high` turns over `original` positions to 0 at
+ *                              the pair (rounded up) that makes `low`
+ *           PCT_ROTARY_BANDS   the same with w = (turns of pair i over
+ *                              `original` positions - low) / (high - low)
+ *           w is taken as at least 0 and at most 1
+ *  amplitude  factor of the rotated elements (1: none)
+ *
+ * pct_rotary_table -- frequencies of a description.
+ *  table  [rot/2] (host) out: turns per position in units of 2^-64 (a whole
+ *         number of turns counts as none), which the caller keeps on the
+ *         device for the calls below
+ * Errors: PCT_ERR_INVALID_ARG for fields outside their ranges (base > 1,
+ * factor > 0, original >= 1, 0 < low < high, as far as the scaling reads
+ * them; rot = 2 with a scaled base). */
+typedef enum { PCT_ROTARY_HALF = 0, PCT_ROTARY_INTERLEAVED = 1 }
+    pct_rotary_layout;
+typedef enum {
+  PCT_ROTARY_PLAIN = 0,
+  PCT_ROTARY_LINEAR = 1,
+  PCT_ROTARY_BASE = 2,
+  PCT_ROTARY_RAMP = 3,
+  PCT_ROTARY_BANDS = 4
+} pct_rotary_scaling;
+typedef struct {
+  int32_t rot, layout, scaling, original;
+  double base, factor, low, high, amplitude;
+} pct_rotary;
+pct_status pct_rotary_table(const pct_rotary* rotary /*host*/,
+                            uint64_t* table /*host*/);
+
+/* ------------------------------------------------------------------------
+ * pct_cache_write_rotary -- a layer's queries, keys and values on their way
+ * to the attention: queries and keys are normalised (if weights are given)
+ * and rotated to their rows' positions, queries go to q_out, keys and values
+ * (as they are) into their slots:
+ *   x <- x / sqrt(sum_D x^2 / D + eps) * weight     (over the whole head)
+ *   (x0, x1) <- amplitude (x0 cos - x1 sin, x1 cos + x0 sin)  (its pairs)
+ * in fp32, rounded once.  Angles are exact to 2^-32 turns at any position.
+ *  table   [rot/2] as pct_rotary_table makes it (may be NULL if rot = 0);
+ *          of the description, rot, layout and amplitude are read
+ *  q_weight, k_weight  [D] fp32, NULL: no norm
+ *  q       rows of [Hq][D], k and v rows of [Hkv][D], *_row_stride elements
+ *          from row to row (views of a joint projection).  q (with q_out) or
+ *          k and v may be NULL: these rows are then left out
+ *  pos     [batch * R] position of each row; rows with a negative one are
+ *          left out altogether: q_out and the cache stay as they were
+ *  slot    [batch * R] as for pct_cache_write (not read without k and v)
+ *  q_out   rows of [Hq][D]; may be q itself with its stride
+ *  k_cache, v_cache  as for pct_cache_write
+ * Only batch, N, n_pages, page_size, Hq (with q), Hkv, D and dtype of the
+ * shape are read.
+ * Errors: PCT_ERR_INVALID_ARG for sizes, rot > D, an eps that is negative or
+ * not finite, null pointers, strides that do not hold a row or are not a
+ * multiple of 8, pointers to elements that are not 16-byte aligned, a q_out
+ * that overlaps q, k or v (first to last row) without being q. */
+pct_status pct_cache_write_rotary(
+    const pct_cache_shape* shape /*host*/, const pct_rotary* rotary /*host*/,
+    const uint64_t* table, float eps, const float* q_weight,
+    const float* k_weight, const void* q, int64_t q_row_stride, const void* k,
+    int64_t k_row_stride, const void* v, int64_t v_row_stride,
+    const int32_t* pos, const int64_t* slot, void* q_out,
+    int64_t q_out_row_stride, void* k_cache, void* v_cache, void* stream);
+
+/* ------------------------------------------------------------------------
  * pct_tree_attention -- softmax attention of the round's rows over the
  * cache.  A row sees the request's context, the root and, of the nodes,
  * those of its mask row (itself and its ancestors); without a mask node i
@@ -514,7 +590,7 @@ pct_status pct_cache_commit(const pct_cache_shape* shape /*host*/,
  * init, 7 adaptive row statistics (units = rows), 8 adaptive best-first +
  * stop, 9 standalone per-parent results, 10 throughput stop / curve scan,
  * 11 sampled target tokens, 12 cache plan, 13 cache write, 14 tree
- * attention (units = rows), 15 its join, 16 cache commit.
+ * attention (units = rows), 15 its join, 16 cache commit, 17 rotary write.
  *  pct_profile_enable  turns recording on or off (the event pool, 8192
  *                      launches, is created on the first enable)
  *  pct_profile_reset   forgets recorded launches
