@@ -58,6 +58,11 @@ class RotaryDesc(C.Structure):
                 ("amplitude", C.c_double)]
 
 
+class _PageState(C.Structure):
+    _fields_ = [(x, C.c_void_p) for x in (
+        "ctx_len", "block_table", "n_held", "ring", "ring_state", "extra")]
+
+
 _lib = None
 
 
@@ -113,6 +118,17 @@ def lib():
     L.pct_cache_write_rotary.argtypes = [
         shape, C.POINTER(RotaryDesc), P, C.c_float, P, P, P, i64, P, i64, P,
         i64, P, P, P, i64, P, P, P]
+    state = C.POINTER(_PageState)
+    for name in ("free", "compact"):
+        f = getattr(L, f"pct_cache_{name}_workspace")
+        f.argtypes, f.restype = [shape], sz
+    L.pct_cache_fork_workspace.argtypes = [shape, i32]
+    L.pct_cache_fork_workspace.restype = sz
+    L.pct_cache_free.argtypes = [shape, i32, P, state, P, sz, P]
+    L.pct_cache_trim.argtypes = [shape, P, state, P, sz, P]
+    L.pct_cache_fork.argtypes = [shape, i32, i64, i32, P, P, P, state, P, P,
+                                 P, P, sz, P]
+    L.pct_cache_compact.argtypes = [shape, i32, i64, state, P, P, P, P, sz, P]
     L.pct_tree_attention_workspace.argtypes = [shape]
     L.pct_tree_attention_workspace.restype = sz
     L.pct_tree_attention.argtypes = [shape, C.c_float, P, i64, P, P, P, P, P,
@@ -142,6 +158,9 @@ def exported_symbols():
             "pct_cache_plan", "pct_cache_plan_served",
             "pct_cache_plan_workspace", "pct_cache_write",
             "pct_rotary_table", "pct_cache_write_rotary",
+            "pct_cache_free", "pct_cache_trim", "pct_cache_free_workspace",
+            "pct_cache_fork", "pct_cache_fork_workspace",
+            "pct_cache_compact", "pct_cache_compact_workspace",
             "pct_tree_attention", "pct_tree_attention_workspace",
             "pct_cache_commit", "pct_profile_enable",
             "pct_profile_reset", "pct_profile_read", "pct_status_string",
@@ -151,7 +170,8 @@ def exported_symbols():
 PROF_MARKOV, PROF_EXPAND, PROF_TOPN, PROF_MASK, PROF_ACCEPT, PROF_ROWTOP, \
     PROF_INIT, PROF_ROWSTATS, PROF_BESTFIRST, PROF_FINALIZE, PROF_STOP, \
     PROF_SAMPLE, PROF_PLAN, PROF_CACHE_WRITE, PROF_ATTEND, PROF_JOIN, \
-    PROF_COMMIT, PROF_ROTARY = range(18)
+    PROF_COMMIT, PROF_ROTARY, PROF_RELEASE, PROF_FORK, \
+    PROF_COMPACT = range(21)
 
 
 def profile_enable(on: bool = True):
@@ -882,6 +902,117 @@ def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
              _want("v_cache", v_cache, dt, cache, dev),
              _want("out", out, i32, one, dev))
     return out
+
+
+@dataclass
+class PageState:
+    """The state of a cache's pages, int32: ctx_len [batch], block_table
+    [batch][max_pages], n_held [batch], ring [n_pages] and ring_state [2] as
+    CachePlan has them, extra [n_pages]: holders of a page beyond the
+    first."""
+    ctx_len: torch.Tensor
+    block_table: torch.Tensor
+    n_held: torch.Tensor
+    ring: torch.Tensor
+    ring_state: torch.Tensor
+    extra: torch.Tensor
+
+
+class CachePages:
+    """Pages that several requests hold: places freed, trimmed and forked,
+    and pages in use moved to the front, for a cache of fixed shape, with the
+    workspace allocated once; the calls only enqueue kernels.  Where requests
+    share pages, trim() comes before CachePlan.run(), which then has nothing
+    to give back."""
+
+    def __init__(self, batch: int, n_pages: int, page_size: int,
+                 max_pages: int, Hkv: int, D: int, layers: int = 1,
+                 dtype=torch.bfloat16, N: int = 0, device="cuda"):
+        self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, Hkv,
+                                Hkv, D, _cache_dtype(dtype))
+        self.layers, self.dtype = layers, dtype
+        self.device = dev = _device(device)
+        L, self._ref = lib(), C.byref(self.shape)
+        nbytes = L.pct_cache_free_workspace(self._ref)
+        if nbytes == 0:
+            raise PCTError(1, L.pct_last_error().decode())
+        self.ws = _workspace(max(
+            nbytes, L.pct_cache_compact_workspace(self._ref),
+            L.pct_cache_fork_workspace(self._ref, batch)), dev)
+        self._layer = n_pages * Hkv * page_size * D
+        self._cache = (layers, n_pages, Hkv, page_size, D)
+        self._shapes = dict(ctx_len=(batch,), block_table=(batch, max_pages),
+                            n_held=(batch,), ring=(n_pages,), ring_state=(2,),
+                            extra=(n_pages,))
+
+    def _state(self, state: PageState):
+        dev, i32 = self.device.index, torch.int32
+        return C.byref(_PageState(*(
+            _want(name, getattr(state, name), i32, shape, dev)
+            for name, shape in self._shapes.items())))
+
+    def _caches(self, k_cache, v_cache):
+        dev, cache = self.device.index, self._cache
+        if self.layers == 1 and k_cache.dim() == 4:
+            cache = cache[1:]
+        return (_want("k_cache", k_cache, self.dtype, cache, dev),
+                _want("v_cache", v_cache, self.dtype, cache, dev))
+
+    def free(self, state: PageState, places):
+        """Empty places [m] int32 (entries outside the batch are left out):
+        pages that nobody else holds go back to the ring."""
+        dev = self.device.index
+        _enqueue(lib().pct_cache_free, dev, self._ref, places.numel(),
+                 _want("places", places, torch.int32, (places.numel(),), dev),
+                 self._state(state), self.ws.data_ptr(), self.ws.numel())
+
+    def trim(self, state: PageState, n_nodes=None):
+        """Every request keeps the pages of its ctx_len + n_nodes + 1
+        positions (n_nodes None: the N of this handle) and lets go of the
+        rest."""
+        dev = self.device.index
+        _enqueue(lib().pct_cache_trim, dev, self._ref,
+                 None if n_nodes is None else
+                 _want("n_nodes", n_nodes, torch.int32,
+                       self._shapes["n_held"], dev),
+                 self._state(state), self.ws.data_ptr(), self.ws.numel())
+
+    def fork(self, state: PageState, src, dst, k_cache, v_cache, length=None,
+             out=None):
+        """Place dst[i] becomes a copy of the first length[i] positions
+        (default: all) of src[i]'s context; m pairs of int32, at most as many
+        as places.  k_cache, v_cache [layers][n_pages][Hkv][page_size][D]
+        (or one layer).  Returns done [m] int32 (into `out` when given): 0
+        where a pair is left out, since dst holds pages, src lacks some, or
+        the ring has none left."""
+        dev, i32, m = self.device.index, torch.int32, src.numel()
+        if m > self.shape.batch:
+            raise PCTError(1, f"{m} pairs for {self.shape.batch} places")
+        if out is None:
+            out = torch.empty(m, dtype=i32, device=src.device)
+        kp, vp = self._caches(k_cache, v_cache)
+        _enqueue(lib().pct_cache_fork, dev, self._ref, self.layers,
+                 self._layer, m, _want("src", src, i32, (m,), dev),
+                 _want("dst", dst, i32, (m,), dev),
+                 None if length is None else
+                 _want("length", length, i32, (m,), dev),
+                 self._state(state), kp, vp, _want("out", out, i32, (m,), dev),
+                 self.ws.data_ptr(), self.ws.numel())
+        return out
+
+    def compact(self, state: PageState, k_cache, v_cache, out=None):
+        """Move the pages in use to the first ones of the cache; ring,
+        ring_state and extra are made anew from the table, which is changed
+        in place or, given `out`, written there.  Slots and share plans of
+        before are void."""
+        table = state.block_table if out is None else out
+        kp, vp = self._caches(k_cache, v_cache)
+        dev = self.device.index
+        _enqueue(lib().pct_cache_compact, dev, self._ref, self.layers,
+                 self._layer, self._state(state),
+                 _want("out", table, torch.int32, self._shapes["block_table"],
+                       dev), kp, vp, self.ws.data_ptr(), self.ws.numel())
+        return table
 
 
 class PagedCache:

@@ -8,7 +8,8 @@ namespace pct {
 
 // profiler kinds after those of ProfKind
 constexpr int PROF_PLAN = 12, PROF_CACHE_WRITE = 13, PROF_ATTEND = 14,
-              PROF_JOIN = 15, PROF_COMMIT = 16, PROF_ROTARY = 17;
+              PROF_JOIN = 15, PROF_COMMIT = 16, PROF_ROTARY = 17, PROF_RELEASE = 18,
+              PROF_FORK = 19, PROF_COMPACT = 20;
 
 constexpr int kMaxTokens = 1 << 30;  // positions of a request at most
 
@@ -71,6 +72,38 @@ struct CommitArgs {
   int32_t* ctx_out;
 };
 hipError_t launch_cache_commit(const CommitArgs& a, hipStream_t s);
+
+// Pages that several requests hold.
+struct PagesArgs {
+  PageGeom g;  // n_nodes: of a trim; table and ctx_len unused
+  int32_t *ctx, *table, *held, *ring, *ring_state, *extra;
+  int m;                  // places of a free or pairs of a fork, else batch
+  const int32_t* places;  // [m] of a free, null: a trim
+  int layers;
+  int64_t layer_stride;   // in 8-element chunks
+  uint4 *kc, *vc;
+  int32_t* count;         // scratch of the scans, per segment of pages
+};
+hipError_t launch_release(const PagesArgs& a, hipStream_t s);
+size_t release_workspace(const pct_cache_shape& sh);
+
+struct ForkArgs {
+  PagesArgs a;
+  const int32_t *src, *dst, *length;  // [m]; length or null
+  int32_t* done;
+  int4* req;       // [m] {source or -1, place, positions, page of the rest}
+  int32_t* claim;  // [batch] first pair that names the place
+};
+hipError_t launch_fork(const ForkArgs& f, hipStream_t s);
+
+struct CompactArgs {
+  PagesArgs a;
+  int32_t* table_out;
+  int32_t *hole, *high, *rank;  // [n_pages] moves: high[k] to hole[k]
+  int32_t* info;                // pages in use, moves
+};
+hipError_t launch_compact(const CompactArgs& c, hipStream_t s);
+size_t compact_workspace(const pct_cache_shape& sh);
 
 struct AttendArgs {
   PageGeom g;

@@ -581,6 +581,94 @@ pct_status pct_cache_commit(const pct_cache_shape* shape /*host*/,
                             void* v_cache, int32_t* ctx_out, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Pages that several requests hold.  The state of a cache's pages is that of
+ * pct_cache_plan with a count of holders per page:
+ *  ctx_len [batch], block_table [batch][max_pages], n_held [batch],
+ *  ring [n_pages], ring_state [2]  as for pct_cache_plan
+ *  extra   [n_pages] holders of a page beyond the first: 0 for pages that one
+ *          request holds, and for free ones (all 0 at first)
+ * pct_cache_plan takes pages from the ring, which leaves extra as it is, but
+ * gives pages back without a look at their holders: where requests share
+ * pages, pct_cache_trim comes before it and leaves it nothing to give back.
+ * A shared page is in use by all of its holders: a request's context length
+ * must not be lowered into its shared pages other than by pct_cache_free.
+ * A request holds a page once.  Results do not depend on timing. */
+typedef struct {
+  int32_t *ctx_len, *block_table, *n_held, *ring, *ring_state, *extra;
+} pct_page_state; /* (host) of device pointers */
+
+/* ------------------------------------------------------------------------
+ * pct_cache_free -- places become empty: ctx_len 0, n_held 0, their table
+ * entries -1.  A page whose last holder lets go is free: such pages go to
+ * the ring's tail in ascending order, the others' extra goes down.
+ *  m, places  [m] places; entries outside [0, batch) are left out, a place
+ *          may be named more than once
+ *  workspace  pct_cache_free_workspace(shape) bytes
+ * pct_cache_trim -- every request keeps the pages of its ctx_len + n_nodes + 1
+ * positions and lets go of the rest in the same way (n_nodes NULL = N).
+ * Only batch, N (trim), n_pages, page_size and max_pages are read.
+ * Errors: PCT_ERR_INVALID_ARG for sizes, m < 0, null pointers, arrays that
+ * overlap; PCT_ERR_UNSUPPORTED for batch or m > 65535; PCT_ERR_WORKSPACE. */
+size_t pct_cache_free_workspace(const pct_cache_shape* shape /*host*/);
+pct_status pct_cache_free(const pct_cache_shape* shape /*host*/, int32_t m,
+                          const int32_t* places,
+                          const pct_page_state* state /*host*/,
+                          void* workspace, size_t workspace_bytes,
+                          void* stream);
+pct_status pct_cache_trim(const pct_cache_shape* shape /*host*/,
+                          const int32_t* n_nodes,
+                          const pct_page_state* state /*host*/,
+                          void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * pct_cache_fork -- place dst[i] becomes a copy of the first length[i]
+ * positions of src[i]'s context (at most ctx_len of it; length NULL: all of
+ * it): it holds the same whole pages (extra goes up), and a page of its own
+ * from the ring's head, in the order of the pairs, for the positions of a
+ * last page in part, whose rows are copied in all layers.
+ *  done    [m] out: 1, or 0 for a pair that is left out: src or dst outside
+ *          [0, batch) or the same, dst holds pages or is named by an earlier
+ *          pair, src does not hold the pages of its positions, or the ring
+ *          has no page left (from then on no pair gets one)
+ *  layers, layer_stride, k_cache, v_cache  as for pct_cache_commit
+ *  workspace  pct_cache_fork_workspace(shape, m) bytes
+ * All pairs see the state of before the call; a src may be named in many.
+ * Only batch, n_pages, page_size, max_pages, Hkv, D and dtype are read.
+ * Errors: as pct_cache_free, and as pct_cache_commit for the caches. */
+size_t pct_cache_fork_workspace(const pct_cache_shape* shape /*host*/,
+                                int32_t m);
+pct_status pct_cache_fork(const pct_cache_shape* shape /*host*/,
+                          int32_t layers, int64_t layer_stride, int32_t m,
+                          const int32_t* src, const int32_t* dst,
+                          const int32_t* length,
+                          const pct_page_state* state /*host*/, void* k_cache,
+                          void* v_cache, int32_t* done, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pct_cache_compact -- the pages in use become the first ones of the cache:
+ * with T pages in the tables (the first n_held entries of each row), those
+ * from T on move, in ascending order, to the unused ones below T, in
+ * ascending order, in all layers; the others stay where they are.
+ *  state   block_table and n_held are read; ring, ring_state and extra are
+ *          written from them alone (so that pages that got lost are free
+ *          again): ring[i] = (T + i) mod n_pages, ring_state = {0, n_pages - T}
+ *  table_out [batch][max_pages] the new table, may be block_table itself
+ *  layers, layer_stride, k_cache, v_cache  as for pct_cache_commit
+ *  workspace  pct_cache_compact_workspace(shape) bytes
+ * Slots, share plans and tables of before the call are void.
+ * Only batch, n_pages, page_size, max_pages, Hkv, D and dtype are read.
+ * Errors: as pct_cache_fork. */
+size_t pct_cache_compact_workspace(const pct_cache_shape* shape /*host*/);
+pct_status pct_cache_compact(const pct_cache_shape* shape /*host*/,
+                             int32_t layers, int64_t layer_stride,
+                             const pct_page_state* state /*host*/,
+                             int32_t* table_out, void* k_cache, void* v_cache,
+                             void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ------------------------------------------------------------------------
  * Profiling (not from the pages; for measuring kernels against the
  * hardware roofline).  When enabled, every kernel launch of the calls above
  * is bracketed by two HIP events recorded on its stream, tagged with a kind
@@ -590,7 +678,8 @@ pct_status pct_cache_commit(const pct_cache_shape* shape /*host*/,
  * init, 7 adaptive row statistics (units = rows), 8 adaptive best-first +
  * stop, 9 standalone per-parent results, 10 throughput stop / curve scan,
  * 11 sampled target tokens, 12 cache plan, 13 cache write, 14 tree
- * attention (units = rows), 15 its join, 16 cache commit, 17 rotary write.
+ * attention (units = rows), 15 its join, 16 cache commit, 17 rotary write,
+ * 18 cache free and trim, 19 fork, 20 compaction.
  *  pct_profile_enable  turns recording on or off (the event pool, 8192
  *                      launches, is created on the first enable)
  *  pct_profile_reset   forgets recorded launches
