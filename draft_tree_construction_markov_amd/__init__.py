@@ -129,6 +129,13 @@ def lib():
     L.pct_cache_fork.argtypes = [shape, i32, i64, i32, P, P, P, state, P, P,
                                  P, P, sz, P]
     L.pct_cache_compact.argtypes = [shape, i32, i64, state, P, P, P, P, sz, P]
+    for name in ("cache_share_size", "cache_share_workspace",
+                 "shared_attention_workspace"):
+        f = getattr(L, f"pct_{name}")
+        f.argtypes, f.restype = [shape], sz
+    L.pct_cache_share.argtypes = [shape, i32, P, P, P, P, P, P, P, sz, P]
+    L.pct_shared_attention.argtypes = [shape, C.c_float, P, i64, P, P, P, P,
+                                       P, P, P, P, sz, P]
     L.pct_tree_attention_workspace.argtypes = [shape]
     L.pct_tree_attention_workspace.restype = sz
     L.pct_tree_attention.argtypes = [shape, C.c_float, P, i64, P, P, P, P, P,
@@ -161,6 +168,9 @@ def exported_symbols():
             "pct_cache_free", "pct_cache_trim", "pct_cache_free_workspace",
             "pct_cache_fork", "pct_cache_fork_workspace",
             "pct_cache_compact", "pct_cache_compact_workspace",
+            "pct_cache_share", "pct_cache_share_size",
+            "pct_cache_share_workspace", "pct_shared_attention",
+            "pct_shared_attention_workspace",
             "pct_tree_attention", "pct_tree_attention_workspace",
             "pct_cache_commit", "pct_profile_enable",
             "pct_profile_reset", "pct_profile_read", "pct_status_string",
@@ -171,7 +181,7 @@ PROF_MARKOV, PROF_EXPAND, PROF_TOPN, PROF_MASK, PROF_ACCEPT, PROF_ROWTOP, \
     PROF_INIT, PROF_ROWSTATS, PROF_BESTFIRST, PROF_FINALIZE, PROF_STOP, \
     PROF_SAMPLE, PROF_PLAN, PROF_CACHE_WRITE, PROF_ATTEND, PROF_JOIN, \
     PROF_COMMIT, PROF_ROTARY, PROF_RELEASE, PROF_FORK, \
-    PROF_COMPACT = range(21)
+    PROF_COMPACT, PROF_SHARE = range(22)
 
 
 def profile_enable(on: bool = True):
@@ -868,6 +878,120 @@ def tree_attention(q, k_cache, v_cache, block_table, ctx_len, n_nodes=None,
                       device=_dev(k_cache))
     return h.run(q, k_cache, v_cache, block_table, ctx_len, n_nodes, mask,
                  scale)
+
+
+@dataclass
+class CacheShare:
+    """Who shares what in a round, int32: leader [batch] (the lowest request
+    of the group, the request itself without one) and shared [batch] (the
+    group's shared positions, 0 without one); plan: what SharedAttention
+    reads, the round's lengths among it; key: the sizes it was made for."""
+    leader: torch.Tensor
+    shared: torch.Tensor
+    plan: torch.Tensor
+    key: tuple
+
+
+class SharePlan:
+    """Plan of the prefixes that requests of a round share, found from their
+    block tables; fixed shape, with its workspace and outputs allocated once;
+    run() only enqueues kernels.  least: positions that a group must save to
+    be one."""
+
+    def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
+                 max_pages: int, least: int = 128, device="cuda"):
+        self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, 1, 1,
+                                16, PCT_BF16)
+        self.device = dev = _device(device)
+        self.least = least
+        self._fn, self._ref = lib().pct_cache_share, C.byref(self.shape)
+        size = lib().pct_cache_share_size(self._ref)
+        if size == 0:
+            raise PCTError(2 if batch > 1024 else 1,
+                           lib().pct_last_error().decode())
+        self.ws = _workspace(lib().pct_cache_share_workspace(self._ref), dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        # no rows before the first run
+        plan = torch.zeros(size // 4, **i32)
+        req = plan[:4 * batch].view(batch, 4)
+        req[:, 1] = -1
+        req[:, 3] = -1
+        plan[8 * batch:9 * batch] = -1
+        self.out = CacheShare(
+            leader=torch.arange(batch, **i32), shared=torch.zeros(batch, **i32),
+            plan=plan, key=(batch, N, n_pages, page_size, max_pages))
+        o = self.out
+        self._tail = tuple(C.c_void_p(x.data_ptr()) for x in (
+            o.leader, o.shared, o.plan, self.ws)) + (self.ws.numel(),)
+
+    def run(self, ctx_len, n_nodes, block_table) -> CacheShare:
+        """n_nodes None = N everywhere.  The outputs are written by every
+        call."""
+        dev, i32 = self.device.index, torch.int32
+        batch, width = self.shape.batch, self.shape.max_pages
+        _enqueue(self._fn, dev, self._ref, self.least,
+                 _want("ctx_len", ctx_len, i32, (batch,), dev),
+                 None if n_nodes is None else
+                 _want("n_nodes", n_nodes, i32, (batch,), dev),
+                 _want("block_table", block_table, i32, (batch, width), dev),
+                 *self._tail)
+        return self.out
+
+
+class SharedAttention:
+    """TreeAttention that reads the keys a group of requests shares once for
+    all of its rows: fixed shape, workspace and outputs allocated once; run()
+    only enqueues kernels.  Its outputs carry no gradient."""
+
+    def __init__(self, batch: int, N: int, Hq: int, Hkv: int, D: int,
+                 n_pages: int, page_size: int, max_pages: int,
+                 dtype=torch.bfloat16, lse: bool = False, device="cuda"):
+        self.dtype = dtype
+        self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, Hq,
+                                Hkv, D, _cache_dtype(dtype))
+        self.device = dev = _device(device)
+        self._fn, self._ref = lib().pct_shared_attention, C.byref(self.shape)
+        nbytes = lib().pct_shared_attention_workspace(self._ref)
+        if nbytes == 0:
+            raise PCTError(2 if batch > 1024 else 1,
+                           lib().pct_last_error().decode())
+        self.ws = _workspace(nbytes, dev)
+        # a call writes the rows it uses: those that none has used stay zero
+        self.out = torch.zeros(batch, N + 1, Hq, D, dtype=dtype, device=dev)
+        self.lse = (torch.zeros(batch, N + 1, Hq, dtype=torch.float32,
+                                device=dev) if lse else None)
+        self._key = (batch, N, n_pages, page_size, max_pages)
+        self._shapes = ((batch, N + 1, Hq, D), (n_pages, Hkv, page_size, D),
+                        (batch, max_pages), (batch, N, (N + 63) // 64))
+        self._op = C.c_void_p(self.out.data_ptr())
+        self._tail = (None if self.lse is None else
+                      C.c_void_p(self.lse.data_ptr()),
+                      C.c_void_p(self.ws.data_ptr()), self.ws.numel())
+
+    def run(self, q, k_cache, v_cache, block_table, share: CacheShare,
+            mask=None, scale=None, out=None):
+        """As TreeAttention.run, with the lengths of the round in `share`, as
+        SharePlan.run returned it from the same block_table."""
+        dev, dt, i32 = self.device.index, self.dtype, torch.int32
+        rows, cache, pages, words = self._shapes
+        if share.key != self._key:
+            raise ValueError(f"the share plan is for sizes {share.key}, not "
+                             f"{self._key}")
+        if out is None:
+            out, op = self.out, self._op
+        else:
+            op = _want("out", out, dt, rows, dev)
+        qp, qs = _rows("q", q, dt, rows, dev)
+        _enqueue(self._fn, dev, self._ref,
+                 rows[3] ** -0.5 if scale is None else scale, qp, qs,
+                 _want("k_cache", k_cache, dt, cache, dev),
+                 _want("v_cache", v_cache, dt, cache, dev),
+                 _want("block_table", block_table, i32, pages, dev),
+                 _want("share.plan", share.plan, i32, share.plan.shape, dev),
+                 None if mask is None or words[1] == 0 else
+                 _want("mask", mask, torch.int64, words, dev),
+                 op, *self._tail)
+        return out, self.lse
 
 
 def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,

@@ -20,7 +20,9 @@ SOURCES = ["api.hip", "k_markov.hip",
            "api_cache.hip", "api_rotary.hip", "k_rotary.hip",
            "api_pages.hip", "k_pages.hip", "k_cache.hip", "k_attend.hip", "k_attend_d64.hip",
            "k_attend_d96.hip", "k_attend_d128.hip", "k_attend_d192.hip",
-           "k_attend_d256.hip"]
+           "k_attend_d256.hip", "api_share.hip", "k_share.hip", "k_shared.hip",
+           "k_shared_d64.hip", "k_shared_d96.hip", "k_shared_d128.hip",
+           "k_shared_d192.hip", "k_shared_d256.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,6 +1,7 @@
 // api_cache.h -- argument checks that the cache's entry points share.
 #pragma once
 
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -78,6 +79,45 @@ inline PageGeom geom(const pct_cache_shape* sh, const int32_t* table,
   g.ctx_len = ctx_len;
   g.n_nodes = n_nodes;
   return g;
+}
+
+// Checks the pointers and numbers of an attention call, and its arguments.
+inline pct_status attend_args(const pct_cache_shape* shape, float scale,
+                              const void* q, int64_t q_row_stride,
+                              const void* k_cache, const void* v_cache,
+                              const int32_t* block_table,
+                              const int32_t* ctx_len, const int32_t* n_nodes,
+                              const uint64_t* mask, void* out, float* lse,
+                              AttendArgs& a) {
+  if (!q || !k_cache || !v_cache || !block_table || !out)
+    return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
+  // (infinite for the largest scales: every score would be infinite or NaN)
+  const float c = fabsf(scale) * 1.44269504f;
+  if (!isfinite(c))
+    return fail(PCT_ERR_INVALID_ARG, "scale * log2(e) must be finite");
+  if (q_row_stride < (int64_t)shape->Hq * shape->D || q_row_stride % 8 != 0)
+    return fail(PCT_ERR_INVALID_ARG,
+                "q_row_stride must be a multiple of 8 and at least Hq * D");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(out))
+    return fail(PCT_ERR_INVALID_ARG,
+                "q, caches and out must be 16-byte aligned");
+  a.g = geom(shape, block_table, ctx_len, n_nodes);
+  a.Hq = shape->Hq;
+  a.G = shape->Hq / shape->Hkv;
+  a.bf16 = shape->dtype == PCT_BF16;
+  a.c = scale == 0.f ? 1.f : c;
+  a.qand = scale == 0.f ? 0u : ~0u;
+  a.qxor = scale < 0.f ? 0x80008000u : 0u;
+  a.q = q;
+  a.qs = q_row_stride;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.mask = shape->N > 0 ? mask : nullptr;
+  a.words = (shape->N + 63) / 64;
+  a.out = out;
+  a.lse = lse;
+  return PCT_OK;
 }
 
 }  // namespace pct

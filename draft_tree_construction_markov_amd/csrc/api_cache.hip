@@ -1,8 +1,6 @@
 // api_cache.hip -- the C-ABI of the paged key-value cache: argument checks
 // and launches of the page plan, row writes, tree attention and the commit
 // of accepted paths.
-#include <math.h>
-
 #include "api_cache.h"
 
 using namespace pct;
@@ -133,40 +131,17 @@ pct_status pct_tree_attention(const pct_cache_shape* shape, float scale,
   if (st != PCT_OK) return st;
   st = check_heads(shape, true);
   if (st != PCT_OK) return st;
-  if (!q || !k_cache || !v_cache || !block_table || !ctx_len || !out)
+  if (!ctx_len)
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
-  // (infinite for the largest scales: every score would be infinite or NaN)
-  const float c = fabsf(scale) * 1.44269504f;
-  if (!isfinite(c))
-    return fail(PCT_ERR_INVALID_ARG, "scale * log2(e) must be finite");
-  if (q_row_stride < (int64_t)shape->Hq * shape->D || q_row_stride % 8 != 0)
-    return fail(PCT_ERR_INVALID_ARG,
-                "q_row_stride must be a multiple of 8 and at least Hq * D");
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
-      !aligned16(out))
-    return fail(PCT_ERR_INVALID_ARG,
-                "q, caches and out must be 16-byte aligned");
+  AttendArgs a{};
+  st = attend_args(shape, scale, q, q_row_stride, k_cache, v_cache,
+                   block_table, ctx_len, n_nodes, mask, out, lse, a);
+  if (st != PCT_OK) return st;
   const size_t need = tree_attention_workspace(*shape);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(PCT_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (need > 0 && !aligned16(workspace))
     return fail(PCT_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  AttendArgs a{};
-  a.g = geom(shape, block_table, ctx_len, n_nodes);
-  a.Hq = shape->Hq;
-  a.G = shape->Hq / shape->Hkv;
-  a.bf16 = shape->dtype == PCT_BF16;
-  a.c = scale == 0.f ? 1.f : c;
-  a.qand = scale == 0.f ? 0u : ~0u;
-  a.qxor = scale < 0.f ? 0x80008000u : 0u;
-  a.q = q;
-  a.qs = q_row_stride;
-  a.kc = k_cache;
-  a.vc = v_cache;
-  a.mask = shape->N > 0 ? mask : nullptr;
-  a.words = (shape->N + 63) / 64;
-  a.out = out;
-  a.lse = lse;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = launch_tree_attention(a, workspace, s);
   if (e != hipSuccess) return hip_fail(e, "tree attention kernel");

@@ -2,8 +2,7 @@
 // join of row tiles whose keys were split over workgroups.
 #include <type_traits>
 
-#include "pct_cache.h"
-#include "pct_device.h"
+#include "k_attend_join.h"
 
 namespace pct {
 
@@ -13,18 +12,18 @@ int padded(int D) {
   return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256;
 }
 
-struct WsLayout {
-  size_t o, ml, meta, total;
-};
+}  // namespace
 
-AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
+// rows: packed rows of a request and key-value head, at most
+AttendPlan plan_attend(int requests, int64_t rows, int64_t cap, int Hkv,
+                       int D) {
+  const int64_t batch = requests, M = rows;
   AttendPlan p{};
   p.dp = padded(D);
   // The smallest row tile that holds a request's rows of one head, or 64 rows
   // for little work; waves with keys of their own up to 16 rows (with 32, 64
   // requests of 8 rows over up to 8 k positions took 205 us, with shared
   // tiles 166).
-  const int64_t M = (int64_t)(N + 1) * (Hq / Hkv);
   p.mt = M <= 16 ? 16 : M <= 64 ? 64 : 128;
   // (bounded, so that no shape overflows the products below)
   const auto bounded = [](int64_t x) { return x < 1 << 30 ? x : 1 << 30; };
@@ -51,6 +50,12 @@ AttendPlan plan_attend(int batch, int N, int64_t cap, int Hq, int Hkv, int D) {
   return p;
 }
 
+namespace {
+
+struct WsLayout {
+  size_t o, ml, meta, total;
+};
+
 WsLayout layout(const AttendPlan& p) {
   WsLayout w{};
   const size_t rows = (size_t)2 * p.n_wg * p.mt;
@@ -74,40 +79,6 @@ WsLayout layout(const AttendPlan& p) {
 // runs, else for every run; the others leave at once, but 8192 of them took
 // 3 us.  Bound by the sums' read: 32 trees of 257 rows 16 us for 66 MB.
 constexpr int kJoinThreads = 256, kInFlight = 8;
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t round_pair(float x, float y) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-  const f32x2 v = {x, y};
-  if constexpr (BF16)
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-  else
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
-}
-
-struct JoinSum {
-  float m, l;
-  float4 o;
-  __device__ __forceinline__ void scale(float m2) {
-    const float f = m2 == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(m - m2);
-    m = m2;
-    l *= f;
-    o.x *= f;
-    o.y *= f;
-    o.z *= f;
-    o.w *= f;
-  }
-  __device__ __forceinline__ void add(float2 ml, const float4& v) {
-    const float f = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
-    l += f * ml.y;
-    o.x += f * v.x;
-    o.y += f * v.y;
-    o.z += f * v.z;
-    o.w += f * v.w;
-  }
-};
 
 template <bool BF16, int LR, int PG>
 __global__ __launch_bounds__(kJoinThreads) void attend_join_kernel(
@@ -217,17 +188,18 @@ hipError_t launch_join_type(const AttendArgs& a, const AttendPlan& p,
 }
 
 size_t tree_attention_workspace(const pct_cache_shape& sh) {
-  return layout(plan_attend(sh.batch, sh.N,
-                            (int64_t)sh.max_pages * sh.page_size, sh.Hq,
-                            sh.Hkv, sh.D))
+  return layout(plan_attend(sh.batch, (int64_t)(sh.N + 1) * (sh.Hq / sh.Hkv),
+                            (int64_t)sh.max_pages * sh.page_size, sh.Hkv,
+                            sh.D))
       .total;
 }
 
 hipError_t launch_tree_attention(const AttendArgs& a, void* workspace,
                                  hipStream_t s) {
   const PageGeom& g = a.g;
-  const AttendPlan p = plan_attend(
-      g.batch, g.N, (int64_t)g.max_pages << g.shift, a.Hq, g.Hkv, g.D);
+  const AttendPlan p =
+      plan_attend(g.batch, (int64_t)(g.N + 1) * a.G,
+                  (int64_t)g.max_pages << g.shift, g.Hkv, g.D);
   const WsLayout w = layout(p);
   char* base = static_cast<char*>(workspace);
   AttendWs ws{reinterpret_cast<float*>(base + w.o),

@@ -134,17 +134,25 @@ struct AttendReq {
   int M, RT, KT;   // packed rows, row tiles, steps of a row tile
   int64_t units;   // of all heads and row tiles
 };
-template <int MT, int KS>
+// before: the request's shared positions (own keys); rows: of a group (shared
+// keys, all of which are context)
+template <int MT, int KS, int PART = kAllKeys>
 __device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
-                                                    int ctx, int n) {
+                                                    int ctx, int n,
+                                                    int before = 0,
+                                                    int rows = 0) {
   AttendReq r;
   // A context that does not fit the block table ends with it: its last
   // position stands in for the root, and the nodes are past the end.
-  const int cap = a.g.max_pages << a.g.shift;
+  int cap = a.g.max_pages << a.g.shift;
+  if constexpr (PART == kOwnKeys) {
+    cap -= before;
+    ctx -= before;
+  }
   r.n = n;
   r.ctx = min(ctx, cap - 1);
   r.L = min(r.ctx + n + 1, cap);
-  r.M = (n + 1) * a.G;
+  r.M = (PART == kSharedKeys ? rows : n + 1) * a.G;
   r.RT = (r.M + MT - 1) / MT;
   r.KT = (r.L + KS - 1) / KS;
   r.units = (int64_t)a.g.Hkv * r.RT * r.KT;
@@ -152,10 +160,21 @@ __device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
 }
 // Lengths of request b; uniform: b is the same in every lane, and the lengths
 // are held in scalar registers.
-template <int MT, int KS>
+template <int MT, int KS, int PART = kAllKeys>
 __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
                                                 bool uniform = false) {
   const PageGeom& g = a.g;
+  if constexpr (PART != kAllKeys) {
+    int4 x = PART == kSharedKeys ? a.share.groups[b] : a.share.req[b];
+    if (uniform) {
+      x.x = __builtin_amdgcn_readfirstlane(x.x);
+      x.y = __builtin_amdgcn_readfirstlane(x.y);
+      x.z = __builtin_amdgcn_readfirstlane(x.z);
+    }
+    return PART == kSharedKeys
+               ? attend_lengths<MT, KS, PART>(a, x.y - 1, 0, 0, x.z)
+               : attend_lengths<MT, KS, PART>(a, x.x, x.y, x.z << g.shift);
+  }
   int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
   int ctx = clamp_ctx(g.ctx_len[b]);
   if (uniform) {
@@ -250,12 +269,12 @@ __device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
 }
 
 // Moves on to the request that holds unit u.
-template <int MT, int KS>
+template <int MT, int KS, int PART = kAllKeys>
 __device__ __forceinline__ void next_request(const AttendArgs& a,
                                              AttendRun& run, AttendReq& rq) {
   while (run.u >= run.b_off + run.units(a, rq)) {
     run.b_off += run.units(a, rq);
-    rq = attend_req<MT, KS>(a, ++run.b, true);
+    rq = attend_req<MT, KS, PART>(a, ++run.b, true);
   }
 }
 
@@ -263,7 +282,7 @@ __device__ __forceinline__ void next_request(const AttendArgs& a,
 // the join is then empty).  Every wave does this by itself: lane l goes
 // through requests l per .. (l + 1) per - 1, and the sums over lanes need no
 // LDS.
-template <int MT, int KS, int FEW, int LEAST>
+template <int MT, int KS, int FEW, int LEAST, int PART = kAllKeys>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
                                                 const AttendWs& ws,
                                                 AttendRun& r, AttendReq& rq) {
@@ -277,7 +296,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   AttendReq q{};
 #pragma unroll 4
   for (int b = b0; b < b1; ++b) {
-    q = attend_req<MT, KS>(a, b);
+    q = attend_req<MT, KS, PART>(a, b);
     mine += q.units;
     if (q.M > 0) {
       mine1 += (int64_t)g.Hkv * q.KT;
@@ -353,24 +372,51 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   const int l = __builtin_ctzll(__ballot(r.u < incl));
   r.b = l * per;
   r.b_off = lane_value(incl - mine, l);
-  if (per == 1) {
+  if (PART == kAllKeys && per == 1) {
     // (already loaded)
     rq = attend_lengths<MT, KS>(
         a, __builtin_amdgcn_readlane(q.ctx, l),
         __builtin_amdgcn_readlane(q.n, l));
   } else {
-    rq = attend_req<MT, KS>(a, r.b, true);
-    next_request<MT, KS>(a, r, rq);
+    rq = attend_req<MT, KS, PART>(a, r.b, true);
+    next_request<MT, KS, PART>(a, r, rq);
   }
   return true;
 }
 
-__device__ __forceinline__ void store_meta(const AttendWs& ws, int at,
+__device__ __forceinline__ void store_meta(const AttendWs& ws, int64_t at,
                                            i32x4 x) {
   reinterpret_cast<i32x4*>(ws.meta)[at] = x;
 }
 
+// Block table of a request's (or group's) positions.
+template <int PART>
+__device__ __forceinline__ const int32_t* attend_table(const AttendArgs& a,
+                                                       int b) {
+  const PageGeom& g = a.g;
+  if constexpr (PART == kSharedKeys)
+    return g.table + (int64_t)__builtin_amdgcn_readfirstlane(
+                         a.share.groups[b].x) * g.max_pages;
+  const int32_t* t = g.table + (int64_t)b * g.max_pages;
+  if constexpr (PART == kOwnKeys)
+    t += __builtin_amdgcn_readfirstlane(a.share.req[b].z);
+  return t;
+}
+
+// Index of a row tile in two parts; mt: rows of a row tile.
+template <int PART>
+__device__ __forceinline__ int64_t part_tile(const AttendArgs& a,
+                                             const AttendWs& ws, int b, int h,
+                                             int rt, int mt) {
+  if constexpr (PART == kSharedKeys) {
+    const int first = __builtin_amdgcn_readfirstlane(a.share.groups[b].w);
+    return (int64_t)h * ws.row_tiles + first * a.G / mt + b + rt;
+  }
+  return ((int64_t)b * a.g.Hkv + h) * ws.row_tiles + rt;
+}
+
 // Notes for the join that the run has the piece pc.
+template <int PART = kAllKeys, int MT = 0>
 __device__ __forceinline__ void note_piece(const AttendArgs& a,
                                            const AttendWs& ws,
                                            const AttendRun& run,
@@ -380,6 +426,12 @@ __device__ __forceinline__ void note_piece(const AttendArgs& a,
   if (pc.k0 != 0) return;
   // the join adds the runs up to the one that holds the last step
   const int last = pc.k1 < rq.KT ? run.owner(pc.s0 + rq.KT - 1) : -1;
+  if constexpr (PART != kAllKeys) {
+    if (threadIdx.x == 0)
+      store_meta(ws, part_tile<PART>(a, ws, run.b, pc.h, pc.rt, MT),
+                 i32x4{run.run, last, 0, 0});
+    return;
+  }
   const i32x4 j = {run.b, pc.h << 20 | pc.rt, run.run, last};
   if (ws.row_tiles == 0)
     join = j;
@@ -402,9 +454,11 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int h,
     const int i = m / a.G;
     irow[nt] = i;
     const bool ok = m < M;
+    int64_t row = (int64_t)b * (a.g.N + 1) + (ok ? i : 0);
+    if constexpr (C::PART == kSharedKeys)
+      row = a.share.rows[a.share.groups[b].w + (ok ? i : 0)];
     const uint4* q = reinterpret_cast<const uint4*>(
-        static_cast<const uint16_t*>(a.q) +
-        ((int64_t)b * (a.g.N + 1) + (ok ? i : 0)) * a.qs +
+        static_cast<const uint16_t*>(a.q) + row * a.qs +
         (h * a.G + (ok ? m - i * a.G : 0)) * a.g.D);
 #pragma unroll
     for (int s = 0; s < C::KSTEP; ++s) {

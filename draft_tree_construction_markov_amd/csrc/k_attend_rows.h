@@ -15,8 +15,9 @@
 
 namespace pct {
 
-template <int DP_, bool BF16_>
+template <int DP_, bool BF16_, int PART_ = kAllKeys>
 struct RowsCfg {
+  static constexpr int PART = PART_;
   static constexpr int DP = DP_;  // head size, padded
   static constexpr int NT = 1;     // 16-row blocks
   static constexpr bool BF16 = BF16_;
@@ -62,7 +63,9 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 
   AttendRun run;
   AttendReq rq;
-  if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST>(a, ws, run, rq)) return;
+  if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST, C::PART>(a, ws, run,
+                                                                rq))
+    return;
   i32x4 join = {0, 0, 0, -1};
 
   const uint4* kc = static_cast<const uint4*>(a.kc);
@@ -73,12 +76,12 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   uint4* vt = kt + KB * C::KROW;
 
   while (run.u < run.end) {
-    next_request<C::MT, C::KS>(a, run, rq);
+    next_request<C::MT, C::KS, C::PART>(a, run, rq);
     const int b = run.b;
     const AttendPiece pc = attend_piece(rq, run);
     const int h = pc.h, rt = pc.rt, k0 = pc.k0, k1 = pc.k1;
     const int ctx = rq.ctx, L = rq.L;
-    const int32_t* table = g.table + (int64_t)b * g.max_pages;
+    const int32_t* table = attend_table<C::PART>(a, b);
 
     int irow[NT];
     s16x8 qf[NT][KSTEP];
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     load_queries<C>(a, b, h, rt * C::MT, rq.M, irow, qf);
     load_rows(k0);
     if (k0 + 1 < k1) load_pages(k0 + 1);
-    note_piece(a, ws, run, rq, pc, join);  // (while these are on their way)
+    note_piece<C::PART, C::MT>(a, ws, run, rq, pc, join);  // (while these are on their way)
     sign_queries<C>(a, qf);
 
     for (int k = k0; k < k1; ++k) {
@@ -241,9 +244,13 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == rq.KT;
-    const int slot = 2 * run.run + (k0 == 0 ? 1 : 0);
-    float* part_o = ws.o + (int64_t)slot * C::MT * C::DP;
-    float2* part_ml = ws.ml + (int64_t)slot * C::MT;
+    int64_t slot = 2 * run.run + (k0 == 0 ? 1 : 0);
+    if constexpr (C::PART != kAllKeys)
+      if (whole)
+        slot = 2 * (int64_t)gridDim.x +
+               part_tile<C::PART>(a, ws, b, h, rt, C::MT);
+    float* part_o = ws.o + slot * C::MT * C::DP;
+    float2* part_ml = ws.ml + slot * C::MT;
     for (int x = tid; x < C::MT * CH; x += 256) {
       const int r = x / CH, c = x - r * CH;  // row of the tile, piece
       const int m = rt * C::MT + r;
@@ -264,7 +271,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += f * from[e >> 2][e & 3];
       }
-      if (whole) {
+      if (C::PART == kAllKeys && whole) {
         const int i = m / a.G;
         const int64_t row = ((int64_t)b * (g.N + 1) + i) * a.Hq + h * a.G +
                             (m - i * a.G);

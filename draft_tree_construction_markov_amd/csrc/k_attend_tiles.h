@@ -34,8 +34,9 @@
 
 namespace pct {
 
-template <int DP_, int MT_, bool BF16_>
+template <int DP_, int MT_, bool BF16_, int PART_ = kAllKeys>
 struct TilesCfg {
+  static constexpr int PART = PART_;
   static constexpr int DP = DP_;  // head size, padded
   static constexpr int MT = MT_;  // rows of the workgroup: 64 or 128
   // Waves, and 16-row blocks of each: two per operand read from LDS, and two
@@ -109,7 +110,7 @@ __device__ __forceinline__ void tiles_piece(
   const int page_mask = (1 << g.shift) - 1;
   const bool small = g.shift < 3;  // pages end inside the 8-key groups
   const int ctx = rq.ctx, L = rq.L;
-  const int32_t* table = g.table + (int64_t)b * g.max_pages;
+  const int32_t* table = attend_table<C::PART>(a, b);
 
   // direct loads: this lane's row of load 0 and its pieces there.  Load i
   // reads rows i RPI further; the bits of a row and of i RPI are distinct, so
@@ -418,12 +419,18 @@ __device__ __forceinline__ void tiles_piece(
 
   // ---- finished rows, or sums for the join
   const bool whole = k0 == 0 && k1 == rq.KT;
+  int64_t to_slot = slot;
+  if constexpr (C::PART != kAllKeys)
+    if (whole)
+      to_slot = 2 * (int64_t)gridDim.x +
+                part_tile<C::PART>(a, ws, b, h, (m0 - 16 * NT * wave) / C::MT,
+                                   C::MT);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float sum = row_sum(st.l[nt]);
     const int m = m0 + 16 * nt + col;
     if (m >= rq.M) continue;
-    if (whole) {
+    if (C::PART == kAllKeys && whole) {
       const int i = irow[nt];
       const int64_t row = ((int64_t)b * (g.N + 1) + i) * a.Hq + h * a.G +
                           (m - i * a.G);
@@ -443,7 +450,7 @@ __device__ __forceinline__ void tiles_piece(
                                       (float)kLn2;
     } else {
       const int64_t row =
-          (int64_t)slot * C::MT + (wave * NT + nt) * 16 + col;
+          to_slot * C::MT + (wave * NT + nt) * 16 + col;
       float* to = ws.o + row * C::DP + 4 * quad;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
@@ -462,7 +469,8 @@ __global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
 
   AttendRun run;
   AttendReq rq;
-  if (!attend_schedule<MT, KB, C::FEW, C::LEAST>(a, ws, run, rq)) return;
+  if (!attend_schedule<MT, KB, C::FEW, C::LEAST, C::PART>(a, ws, run, rq))
+    return;
   i32x4 join = {0, 0, 0, -1};
   if ((a.g.D >> 3) < SL) {
     // slots past the head size are read and never loaded
@@ -471,7 +479,7 @@ __global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
       tiles[i] = zero;
   }
   while (run.u < run.end) {
-    next_request<MT, KB>(a, run, rq);
+    next_request<MT, KB, C::PART>(a, run, rq);
     const int b = run.b;
     const AttendPiece pc = attend_piece(rq, run);
     // (the same in every lane, which the compiler cannot see)
@@ -481,7 +489,7 @@ __global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
     const int k1 = __builtin_amdgcn_readfirstlane(pc.k1);
     tiles_piece<C>(a, ws, rq, b, h, m0, k0, k1, 2 * run.run + (k0 == 0),
                    tiles, odd_s);
-    note_piece(a, ws, run, rq, pc, join);
+    note_piece<C::PART, MT>(a, ws, run, rq, pc, join);
     run.u += pc.k1 - pc.k0;
   }
   if (threadIdx.x == 0 && ws.row_tiles == 0) store_meta(ws, run.run, join);

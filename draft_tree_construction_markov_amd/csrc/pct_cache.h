@@ -9,7 +9,7 @@ namespace pct {
 // profiler kinds after those of ProfKind
 constexpr int PROF_PLAN = 12, PROF_CACHE_WRITE = 13, PROF_ATTEND = 14,
               PROF_JOIN = 15, PROF_COMMIT = 16, PROF_ROTARY = 17, PROF_RELEASE = 18,
-              PROF_FORK = 19, PROF_COMPACT = 20;
+              PROF_FORK = 19, PROF_COMPACT = 20, PROF_SHARE = 21;
 
 constexpr int kMaxTokens = 1 << 30;  // positions of a request at most
 
@@ -105,6 +105,26 @@ struct CompactArgs {
 hipError_t launch_compact(const CompactArgs& c, hipStream_t s);
 size_t compact_workspace(const pct_cache_shape& sh);
 
+// What a share plan leaves for the round's attention.
+constexpr int kMaxShareBatch = 1024;
+struct ShareView {
+  int4* req;          // [batch] {context, nodes, shared pages, packed rows of
+                      // its group before its own, or -1: no group}
+  int4* groups;       // [batch] {leader, shared positions, rows (0: no such
+                      // group), first packed row}
+  int32_t* group_of;  // [batch] or -1
+  int32_t* rows;      // [batch * (N + 1)] row of each packed row
+};
+struct ShareArgs {
+  PageGeom g;
+  int least;                      // positions that a group must save
+  int32_t *count, *lead;          // [n_pages]
+  int32_t *place, *size, *joined; // [batch]
+  int32_t *leader, *shared;       // [batch]
+  ShareView view;
+};
+hipError_t launch_share(const ShareArgs& a, hipStream_t s);
+
 struct AttendArgs {
   PageGeom g;
   int Hq, G;        // query heads, query heads per key-value head
@@ -118,7 +138,12 @@ struct AttendArgs {
   int words;        // 64-bit words of a mask row
   void* out;
   float* lse;
+  ShareView share;  // of attention in two parts
 };
+// Which positions a launch goes through: all of a request's, or, where
+// requests share a prefix, the shared ones of a group (whose rows are packed
+// as if they were one request's) or a request's own ones behind them.
+constexpr int kAllKeys = 0, kSharedKeys = 1, kOwnKeys = 2;
 // Tile of a call: heads padded to dp elements, mt rows per workgroup (16: all
 // waves hold these rows and have keys of their own; 64, 128: they hold
 // different ones and share the keys), steps of ks keys, n_wg runs at most (a multiple of 8); the join
@@ -156,11 +181,17 @@ constexpr float kLift = BF16 ? 0.f : 7.f;
 // end.  meta {request, head << 20 | row tile, first run, last run} of a row
 // tile that is cut, w < 0: it is not; its index is the row tile's if
 // row_tiles > 0, else the first run's.
+//
+// In two parts every row tile leaves sums, those that are not cut in a slot
+// of their own behind the runs' (2 n_wg + index).  meta {first run, last run
+// or -1: not cut}.  A group's row tiles begin at index first packed row * G /
+// mt + group within those of a head: no fewer than it has lie before the next
+// group's.
 struct AttendWs {
-  float* o;    // [2 n_wg][mt][dp]
-  float2* ml;  // [2 n_wg][mt] {m, sum}
-  int4* meta;  // [n_wg]
-  int row_tiles;
+  float* o;    // [2 n_wg (+ tiles)][mt][dp]
+  float2* ml;  // [2 n_wg (+ tiles)][mt] {m, sum}
+  int4* meta;  // [n_wg] or [tiles]
+  int row_tiles;  // of a request at most (shared keys: of all groups)
 };
 hipError_t launch_attend_d64(const AttendArgs&, const AttendPlan&,
                              const AttendWs&, hipStream_t);
@@ -172,9 +203,24 @@ hipError_t launch_attend_d192(const AttendArgs&, const AttendPlan&,
                               const AttendWs&, hipStream_t);
 hipError_t launch_attend_d256(const AttendArgs&, const AttendPlan&,
                               const AttendWs&, hipStream_t);
+hipError_t launch_share_d64(const AttendArgs&, const AttendPlan&,
+                            const AttendWs&, int part, hipStream_t);
+hipError_t launch_share_d96(const AttendArgs&, const AttendPlan&,
+                            const AttendWs&, int part, hipStream_t);
+hipError_t launch_share_d128(const AttendArgs&, const AttendPlan&,
+                            const AttendWs&, int part, hipStream_t);
+hipError_t launch_share_d192(const AttendArgs&, const AttendPlan&,
+                            const AttendWs&, int part, hipStream_t);
+hipError_t launch_share_d256(const AttendArgs&, const AttendPlan&,
+                            const AttendWs&, int part, hipStream_t);
 hipError_t launch_tree_attention(const AttendArgs& a, void* ws,
                                  hipStream_t s);
 size_t tree_attention_workspace(const pct_cache_shape& sh);
+AttendPlan plan_attend(int requests, int64_t rows, int64_t cap, int Hkv,
+                       int D);
+hipError_t launch_shared_attention(const AttendArgs& a, void* ws,
+                                   hipStream_t s);
+size_t shared_attention_workspace(const pct_cache_shape& sh);
 
 // A request's lengths, clamped to what the calls accept.
 __host__ __device__ inline int clamp_ctx(int c) {

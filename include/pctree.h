@@ -669,6 +669,56 @@ pct_status pct_cache_compact(const pct_cache_shape* shape /*host*/,
                              void* stream);
 
 /* ------------------------------------------------------------------------
+ * pct_cache_share -- which requests of a round share a prefix, found from
+ * their tables.  With full_b the whole pages of request b's context (none if
+ * n_nodes = -1; its root's page is never among them) and c(p) the number of
+ * table entries j < full_b, over all b, that are page p, each request picks
+ * its entry j of largest gain (j + 1) (c(block_table[b][j]) - 1), the first
+ * such (gains from 2^33 on count as alike), or none if gain * page_size <
+ * least.  Requests that picked the same page at the same j, and whose
+ * tables agree in the entries 0..j with those of the lowest of them, are a
+ * group, if they are two or more.
+ *  least   positions that a group must save to be one (>= 1)
+ *  ctx_len, n_nodes (NULL = N), block_table  as for pct_tree_attention
+ *  leader  [batch] out: lowest request of the group, b itself without one
+ *  shared  [batch] out: positions that the group shares, 0 without one
+ *  share   pct_cache_share_size(shape) bytes out, 16-byte aligned: the plan
+ *          for pct_shared_attention, which holds the lengths too
+ *  workspace  pct_cache_share_workspace(shape) bytes
+ * Only batch, N, n_pages, page_size and max_pages of the shape are read.
+ * Errors: PCT_ERR_INVALID_ARG for sizes, least < 1, null pointers, outputs
+ * that overlap each other or an input; PCT_ERR_UNSUPPORTED for batch > 1024;
+ * PCT_ERR_WORKSPACE. */
+size_t pct_cache_share_size(const pct_cache_shape* shape /*host*/);
+size_t pct_cache_share_workspace(const pct_cache_shape* shape /*host*/);
+pct_status pct_cache_share(const pct_cache_shape* shape /*host*/,
+                           int32_t least, const int32_t* ctx_len,
+                           const int32_t* n_nodes, const int32_t* block_table,
+                           int32_t* leader, int32_t* shared, void* share,
+                           void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * pct_shared_attention -- pct_tree_attention that reads what a group of
+ * requests shares once for all of its rows.  Arguments, results and errors
+ * are those of pct_tree_attention, but
+ *  share   as pct_cache_share wrote it for the same shape (precondition, not
+ *          checked) from the same block_table; the lengths are the ones that
+ *          it was given
+ *  workspace  pct_shared_attention_workspace(shape) bytes: fp32 sums of all
+ *          rows, twice
+ *  PCT_ERR_UNSUPPORTED for batch > 1024 or batch * (N + 1) * Hq / Hkv > 2^30 */
+size_t pct_shared_attention_workspace(const pct_cache_shape* shape /*host*/);
+pct_status pct_shared_attention(const pct_cache_shape* shape /*host*/,
+                                float scale, const void* q,
+                                int64_t q_row_stride, const void* k_cache,
+                                const void* v_cache,
+                                const int32_t* block_table, const void* share,
+                                const uint64_t* mask, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* ------------------------------------------------------------------------
  * Profiling (not from the pages; for measuring kernels against the
  * hardware roofline).  When enabled, every kernel launch of the calls above
  * is bracketed by two HIP events recorded on its stream, tagged with a kind
@@ -679,7 +729,8 @@ pct_status pct_cache_compact(const pct_cache_shape* shape /*host*/,
  * stop, 9 standalone per-parent results, 10 throughput stop / curve scan,
  * 11 sampled target tokens, 12 cache plan, 13 cache write, 14 tree
  * attention (units = rows), 15 its join, 16 cache commit, 17 rotary write,
- * 18 cache free and trim, 19 fork, 20 compaction.
+ * 18 cache free and trim, 19 fork, 20 compaction, 21 share plan.
+ * The parts of shared attention count as tree attention and its join.
  *  pct_profile_enable  turns recording on or off (the event pool, 8192
  *                      launches, is created on the first enable)
  *  pct_profile_reset   forgets recorded launches
