@@ -14,12 +14,15 @@ namespace pct {
 // positions).  Sums of squares and products are fp32; an element is rounded
 // once, when it is stored.
 //
-// LH lanes hold a head, 8 elements (16 bytes) each, so a wave has 64 / LH
-// heads at a time and goes through those of one row: cosines and sines are
-// computed once per lane and used for all of its heads.  The other element of
-// a pair is in another lane's piece, which is loaded a second time (from the
-// L1; both are whole pieces if rot / 2 is a multiple of 8).
-enum { kHalf = 0, kPairs = 1, kHalfOdd = 2 };
+// LH lanes hold a head, 4 pairs each: pairs i >= rot / 2 are the elements
+// behind the rotated ones, two by two, and are not rotated.  A wave has
+// 64 / LH heads at a time and goes through those of one row, the next ones on
+// their way while it computes: cosines and sines are computed once per lane
+// and used for all of its heads, and a pair needs no other lane.
+//
+// Where a lane's pairs are: in 16 bytes (interleaved), in twice 8 (halves; rot
+// a multiple of 8), or element by element (halves, other rot).
+enum { kPairs = 0, kHalf = 1, kHalfOdd = 2 };
 
 template <bool BF16>
 __device__ __forceinline__ float from_bits(uint32_t b) {
@@ -27,21 +30,34 @@ __device__ __forceinline__ float from_bits(uint32_t b) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)b);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+// The first and second elements of a lane's 4 pairs, from and to its 16 bytes.
+template <bool BF16, int LAYOUT>
+__device__ __forceinline__ void unpack_pairs(const uint4& v, float (&x)[4],
+                                             float (&y)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    x[2 * e] = from_bits<BF16>(w[e] & 0xffffu);
-    x[2 * e + 1] = from_bits<BF16>(w[e] >> 16);
+    f[2 * e] = from_bits<BF16>(w[e] & 0xffffu);
+    f[2 * e + 1] = from_bits<BF16>(w[e] >> 16);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[e] = f[LAYOUT == kPairs ? 2 * e : e];
+    y[e] = f[LAYOUT == kPairs ? 2 * e + 1 : 4 + e];
   }
 }
-
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+template <bool BF16, int LAYOUT>
+__device__ __forceinline__ uint4 pack_pairs(const float (&x)[4],
+                                            const float (&y)[4]) {
   typedef float f32x8 __attribute__((ext_vector_type(8)));
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-  const f32x8 v = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+  f32x8 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[LAYOUT == kPairs ? 2 * e : e] = x[e];
+    v[LAYOUT == kPairs ? 2 * e + 1 : 4 + e] = y[e];
+  }
   if constexpr (BF16)
     return __builtin_bit_cast(uint4, __builtin_convertvector(v, bf16x8));
   else
@@ -78,188 +94,197 @@ __device__ __forceinline__ void turn(uint64_t phase, float amp, float& c,
 // sum over the LH lanes of a head
 template <int LH>
 __device__ __forceinline__ float head_sum(float x) {
-#pragma unroll
-  for (int d = 1; d < LH; d <<= 1) x += __shfl_xor(x, d, kWave);
+  const auto plus = [](float x, int y) {
+    return x + __builtin_bit_cast(float, y);
+  };
+  x = plus(x, dpp_i<kDppXor1>(__builtin_bit_cast(int, x)));
+  if constexpr (LH >= 4)
+    x = plus(x, dpp_i<kDppXor2>(__builtin_bit_cast(int, x)));
+  if constexpr (LH == 8) x += __shfl_xor(x, 4, kWave);
+  if constexpr (LH >= 16) {
+    x = plus(x, dpp_i<kDppRor4>(__builtin_bit_cast(int, x)));
+    x = plus(x, dpp_i<kDppRor8>(__builtin_bit_cast(int, x)));
+  }
+  if constexpr (LH == 32) x += __shfl_xor(x, 16, kWave);
   return x;
 }
 
+// x or y, as values: a conditional expression of two variables is one of their
+// addresses, which keeps both in memory.
+template <typename T>
+__device__ __forceinline__ T pick(bool c, T x, T y) {
+  return c ? x : y;
+}
+
 constexpr int kRotaryThreads = 256;
-constexpr int kAhead = 4;  // heads of a lane loaded before the first is used
+constexpr int kAhead = 4;  // heads of a lane that are loaded together
 
 template <int LH, bool BF16, int LAYOUT>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(
     RotaryArgs a, int splits, int per) {
   constexpr int HW = kWave / LH;  // heads of a wave at a time
   const int lane = threadIdx.x & 63;
-  const int64_t wave = (int64_t)blockIdx.x * (kRotaryThreads / kWave) +
-                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = wave / splits;
+  const int64_t wave =
+      (int64_t)blockIdx.x * (kRotaryThreads / kWave) +
+      __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = splits == 1       ? wave
+                      : wave >> 31 == 0 ? (uint32_t)wave / (uint32_t)splits
+                                        : wave / splits;
   if (row >= a.rows) return;
-  const int p = a.pos[row];
-  if (p < 0) return;
-  // units of this wave: the query heads in groups of HW, then keys and values
-  const int nq = a.q ? (a.Hq + HW - 1) / HW : 0;
-  const int nkv = a.k ? (2 * a.Hkv + HW - 1) / HW : 0;
+  const int l = lane % LH, sub = lane / LH;
+  const int half = a.rot >> 1, Hq = a.Hq, Hkv = a.Hkv, D = a.D;
+  const bool q_norm = a.qw != nullptr, k_norm = a.kw != nullptr;
+  uint16_t* const out_row = static_cast<uint16_t*>(a.out) + row * a.os;
+  uint16_t *const kc = static_cast<uint16_t*>(a.kc),
+                 *const vc = static_cast<uint16_t*>(a.vc);
+  const bool in = 8 * l < D;
+  // units of this wave: HW query heads each, then keys, then values
+  const int nq = a.q ? (Hq + HW - 1) / HW : 0;
+  const int nk = a.k ? (Hkv + HW - 1) / HW : 0;
   const int u0 = (int)(wave - row * splits) * per;
-  const int u1 = min(u0 + per, nq + nkv);
-  const int c = lane % LH, sub = lane / LH;
-  const int chd = a.D >> 3, half = a.rot >> 1;
-  const bool in = c < chd;
-  // the piece with the other elements of this lane's pairs
-  const int other = LAYOUT == kPairs ? c
-                    : c * 8 < half   ? c + half / 8
-                    : c * 8 < a.rot  ? c - half / 8
-                                     : c;
+  int u1 = min(u0 + per, nq + 2 * nk);
+  if (u0 >= u1) return;
 
-  float cs[8], sn[8];
+  // elements of the lane's pair e, and its two 8-byte pieces
+  auto first_of = [&](int e) {
+    const int i = 4 * l + e;
+    return LAYOUT == kPairs || i >= half ? 2 * i : i;
+  };
+  auto second_of = [&](int e) {
+    const int i = 4 * l + e;
+    return LAYOUT == kPairs || i >= half ? 2 * i + 1 : i + half;
+  };
+  // (kHalf: behind the rotated elements a piece is two pairs; which of its
+  // elements make a pair does not matter there)
+  const bool pieces = LAYOUT == kHalf && 4 * l < half;
+  const int lo = !in ? 0 : pieces ? 4 * l : 8 * l;
+  const int hi = !in ? 4 : pieces ? 4 * l + half : 8 * l + 4;
+
+  const uint16_t* q_row = static_cast<const uint16_t*>(a.q) + row * a.qs;
+  const uint16_t* k_row = static_cast<const uint16_t*>(a.k) + row * a.ks;
+  const uint16_t* v_row = static_cast<const uint16_t*>(a.v) + row * a.vs;
+  // Loads are not conditional (the compiler would wait for each before the
+  // next): what is past the row's end reads its last head, or the first
+  // pairs, once more.
+  auto load = [&](int u) __attribute__((always_inline)) {
+    u = min(u, u1 - 1);
+    const int kind = u < nq ? 0 : u < nq + nk ? 1 : 2;
+    const int h = (kind == 0 ? u : u - nq - (kind == 2 ? nk : 0)) * HW + sub;
+    const uint16_t* from =
+        pick(kind == 0, q_row, pick(kind == 1, k_row, v_row)) +
+        min(h, pick(kind == 0, Hq, Hkv) - 1) * D;
+    if constexpr (LAYOUT == kPairs) {
+      return *reinterpret_cast<const uint4*>(from + lo);
+    } else if constexpr (LAYOUT == kHalf) {
+      const uint2 y = *reinterpret_cast<const uint2*>(from + lo);
+      const uint2 z = *reinterpret_cast<const uint2*>(from + hi);
+      return make_uint4(y.x, y.y, z.x, z.y);
+    } else {
+      uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = 8 * c + e;
+      for (int e = 0; e < 4; ++e) {
+        w[e] = from[in ? first_of(e) : e];
+        w[4 + e] = from[in ? second_of(e) : e];
+      }
+      return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16,
+                        w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+  };
+
+  const int p = a.pos[row];
+  const int64_t slot = a.k ? a.slot[row] : -1;
+  uint4 next[kAhead];
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x) next[x] = load(u0 + x);
+  uint64_t f[4] = {0, 0, 0, 0};
+  if (half > 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = a.freq[min(4 * l + e, half - 1)];
+  }
+  // norm weights of queries and keys
+  float w[2][8];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float* from = y == 0 ? a.qw : a.kw;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[y][e] = 1.f;
+    if (!from) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[y][e] = from[LAYOUT == kHalf ? lo + e : in ? first_of(e) : 0];
+      w[y][4 + e] = from[LAYOUT == kHalf ? hi + e : in ? second_of(e) : 0];
+    }
+  }
+  if (p < 0) return;
+  if (slot < 0 || slot >= a.n_slots) u1 = min(u1, nq);
+  const int64_t page = slot >> a.shift, off = slot & ((1 << a.shift) - 1);
+  float cs[4], sn[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
     cs[e] = 1.f;
     sn[e] = 0.f;
-    if (at < a.rot) {
-      if constexpr (LAYOUT == kPairs) {
-        if (e % 2 == 0)
-          turn((uint64_t)p * a.freq[at >> 1], a.amp, cs[e], sn[e]);
-        else
-          cs[e] = cs[e - 1], sn[e] = sn[e - 1];
-      } else {
-        turn((uint64_t)p * a.freq[at < half ? at : at - half], a.amp, cs[e],
-             sn[e]);
-      }
-    }
-  }
-  // the sign of the other element's product
-  if constexpr (LAYOUT == kPairs) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) sn[e] = -sn[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (8 * c + e < half) sn[e] = -sn[e];
+    if (4 * l + e < half) turn((uint64_t)p * f[e], a.amp, cs[e], sn[e]);
   }
 
-  // the eight elements of the pairs' other halves, where these are not one
-  // piece
-  auto gather = [&](const uint16_t* head) {
-    uint32_t w[8];
+  for (int ub = u0; ub < u1; ub += kAhead) {
+    uint4 mine[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int at = 8 * c + e;
-      const int o = at < half ? at + half : at < a.rot ? at - half : at;
-      w[e] = head[o];
-    }
-    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
-                      w[6] | w[7] << 16);
-  };
-  auto weights = [&](const float* w, float (&own)[8], float (&oth)[8]) {
+    for (int x = 0; x < kAhead; ++x) mine[x] = next[x];
+    if (ub + kAhead < u1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int at = 8 * c + e;
-      own[e] = oth[e] = 1.f;
-      if (w && in) {
-        own[e] = w[at];
-        int o = at;
-        if (LAYOUT == kPairs)
-          o = at < a.rot ? at ^ 1 : at;
-        else
-          o = at < half ? at + half : at < a.rot ? at - half : at;
-        oth[e] = w[o];
-      }
-    }
-  };
-  auto rotated = [&](const uint4& mine, const uint4& theirs, bool norm,
-                     const float (&wo)[8], const float (&wt)[8]) {
-    float x[8], z[8], y[8];
-    unpack8<BF16>(mine, x);
-    if constexpr (LAYOUT == kPairs) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = x[e ^ 1];
-    } else {
-      unpack8<BF16>(theirs, z);
-    }
-    float inv = 1.f;
-    if (norm) {
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(x[e], x[e], sum);
-      sum = head_sum<LH>(in ? sum : 0.f);
-      inv = 1.f / __builtin_sqrtf(sum / (float)a.D + a.eps);
+      for (int x = 0; x < kAhead; ++x) next[x] = load(ub + kAhead + x);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float xo = norm ? x[e] * inv * wo[e] : x[e];
-      const float xt = norm ? z[e] * inv * wt[e] : z[e];
-      y[e] = 8 * c + e < a.rot ? __builtin_fmaf(xo, cs[e], xt * sn[e]) : xo;
-    }
-    return pack8<BF16>(y);
-  };
-
-  float wo[8], wt[8];
-  if (u0 < nq) {
-    weights(a.qw, wo, wt);
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.qs;
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.os;
-    const int end = min(u1, nq);
-    for (int u = u0; u < end; u += kAhead) {
-      uint4 mine[kAhead], theirs[kAhead];
+    for (int x = 0; x < kAhead; ++x) {
+      const int u = ub + x;
+      if (u >= u1) break;
+      const int kind = u < nq ? 0 : u < nq + nk ? 1 : 2;
+      const int h = (kind == 0 ? u : u - nq - (kind == 2 ? nk : 0)) * HW + sub;
+      const bool live = in && h < pick(kind == 0, Hq, Hkv);
+      uint16_t* to =
+          kind == 0
+              ? out_row + h * D
+              : pick(kind == 1, kc, vc) +
+                    (((page * Hkv + h) << a.shift) + off) * D;
+      float x0[4], x1[4], y0[4], y1[4];
+      uint4 y = mine[x];
+      if (!in) y = make_uint4(0, 0, 0, 0);
+      unpack_pairs<BF16, LAYOUT>(y, x0, x1);
+      float inv = 1.f;
+      if (pick(kind == 0, q_norm, k_norm)) {
+        float sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const int h = (u + x) * HW + sub;
-        mine[x] = theirs[x] = make_uint4(0, 0, 0, 0);
-        if (u + x < end && h < a.Hq && in) {
-          const uint16_t* head = src + h * a.D;
-          mine[x] = reinterpret_cast<const uint4*>(head)[c];
-          if constexpr (LAYOUT == kHalf)
-            theirs[x] = reinterpret_cast<const uint4*>(head)[other];
-          else if constexpr (LAYOUT == kHalfOdd)
-            theirs[x] = gather(head);
+        for (int e = 0; e < 4; ++e)
+          sum = __builtin_fmaf(x1[e], x1[e], __builtin_fmaf(x0[e], x0[e], sum));
+        sum = head_sum<LH>(sum);
+        inv = 1.f / __builtin_sqrtf(sum / (float)D + a.eps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x0[e] *= inv * pick(kind == 0, w[0][e], w[1][e]);
+          x1[e] *= inv * pick(kind == 0, w[0][4 + e], w[1][4 + e]);
         }
       }
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const int h = (u + x) * HW + sub;
-        if (u + x >= end) break;
-        const uint4 y = rotated(mine[x], theirs[x], a.qw != nullptr, wo, wt);
-        if (h < a.Hq && in) reinterpret_cast<uint4*>(dst + h * a.D)[c] = y;
+      for (int e = 0; e < 4; ++e) {
+        const bool turns = 4 * l + e < half;
+        const float s1 = x1[e] * sn[e], s0 = x0[e] * sn[e];
+        y0[e] = turns ? __builtin_fmaf(x0[e], cs[e], -s1) : x0[e];
+        y1[e] = turns ? __builtin_fmaf(x1[e], cs[e], s0) : x1[e];
       }
-    }
-  }
-  if (u1 <= nq) return;
-  const int64_t slot = a.slot[row];
-  if (slot < 0 || slot >= a.n_slots) return;
-  const int64_t page = slot >> a.shift, off = slot & ((1 << a.shift) - 1);
-  weights(a.kw, wo, wt);
-  for (int u = max(u0, nq); u < u1; u += kAhead) {
-    uint4 mine[kAhead], theirs[kAhead];
+      if (kind != 2) y = pack_pairs<BF16, LAYOUT>(y0, y1);
+      if (!live) continue;
+      if constexpr (LAYOUT == kPairs) {
+        reinterpret_cast<uint4*>(to)[l] = y;
+      } else if constexpr (LAYOUT == kHalf) {
+        *reinterpret_cast<uint2*>(to + lo) = make_uint2(y.x, y.y);
+        *reinterpret_cast<uint2*>(to + hi) = make_uint2(y.z, y.w);
+      } else {
+        const uint32_t v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int j = (u + x - nq) * HW + sub;  // key heads, then value heads
-      mine[x] = theirs[x] = make_uint4(0, 0, 0, 0);
-      if (u + x < u1 && j < 2 * a.Hkv && in) {
-        const uint16_t* head =
-            j < a.Hkv
-                ? static_cast<const uint16_t*>(a.k) + row * a.ks + j * a.D
-                : static_cast<const uint16_t*>(a.v) + row * a.vs +
-                      (j - a.Hkv) * a.D;
-        mine[x] = reinterpret_cast<const uint4*>(head)[c];
-        if constexpr (LAYOUT == kHalf)
-          theirs[x] = reinterpret_cast<const uint4*>(head)[other];
-        else if constexpr (LAYOUT == kHalfOdd)
-          theirs[x] = gather(head);
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int j = (u + x - nq) * HW + sub;
-      if (u + x >= u1) break;
-      const uint4 y = rotated(mine[x], theirs[x], a.kw != nullptr, wo, wt);
-      if (j < 2 * a.Hkv && in) {
-        const bool key = j < a.Hkv;
-        const int h = key ? j : j - a.Hkv;
-        uint4* to = reinterpret_cast<uint4*>(key ? a.kc : a.vc) +
-                    (((page * a.Hkv + h) << a.shift) + off) * chd + c;
-        *to = key ? y : mine[x];
+        for (int e = 0; e < 4; ++e) {
+          to[first_of(e)] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+          to[second_of(e)] = (uint16_t)(v[2 + (e >> 1)] >> (16 * (e & 1)));
+        }
       }
     }
   }
@@ -269,7 +294,7 @@ template <int LH, bool BF16>
 hipError_t launch_rotary_lh(const RotaryArgs& a, hipStream_t s) {
   constexpr int HW = kWave / LH;
   const int units = (a.q ? (a.Hq + HW - 1) / HW : 0) +
-                    (a.k ? (2 * a.Hkv + HW - 1) / HW : 0);
+                    (a.k ? 2 * ((a.Hkv + HW - 1) / HW) : 0);
   // a wave per row, or several while these are few
   int64_t splits = 16384 / a.rows;
   splits = splits < 1 ? 1 : splits > units ? units : splits;
@@ -280,7 +305,7 @@ hipError_t launch_rotary_lh(const RotaryArgs& a, hipStream_t s) {
   if (a.pairs)
     hipLaunchKernelGGL((rotary_kernel<LH, BF16, kPairs>), grid, block, 0, s, a,
                        (int)splits, per);
-  else if (a.rot % 16 == 0)
+  else if (a.rot % 8 == 0)
     hipLaunchKernelGGL((rotary_kernel<LH, BF16, kHalf>), grid, block, 0, s, a,
                        (int)splits, per);
   else
