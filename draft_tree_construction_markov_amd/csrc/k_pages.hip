@@ -21,7 +21,9 @@ constexpr int kSmallPlaces = 64;      // places, that one workgroup goes through
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// A value that other waves of this launch may have written by atomics.
+// A value that other waves of this workgroup may have written before a
+// barrier: read past the L1, as atomics write.  (The barrier waits for them; a
+// fence for the whole GPU in its place writes back the L2, 2 .. 5 us each.)
 __device__ __forceinline__ int fresh(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -131,7 +133,6 @@ __global__ __launch_bounds__(kThreads) void release_small_kernel(PagesArgs a) {
     if (b >= 0) let_go(a, b, keep, held, lane, kWave);
   }
   const int2 ring = ring_now(a);
-  __threadfence();
   __syncthreads();
   int more = 0;
   for (int seg = 0; seg * kSeg < a.g.n_pages; ++seg)
@@ -210,13 +211,11 @@ __global__ __launch_bounds__(kThreads) void fork_plan_kernel(ForkArgs f) {
     const int d = f.dst[i];
     if (d >= 0 && d < g.batch) f.claim[d] = a.m;
   }
-  __threadfence();
   __syncthreads();
   for (int i = tid; i < a.m; i += kThreads) {
     const int d = f.dst[i];
     if (d >= 0 && d < g.batch) atomicMin(&f.claim[d], i);
   }
-  __threadfence();
   __syncthreads();
   int base = 0;
   for (int i0 = 0; i0 < a.m; i0 += kThreads) {
@@ -254,7 +253,6 @@ __global__ __launch_bounds__(kThreads) void fork_plan_kernel(ForkArgs f) {
       f.done[i] = ok ? 1 : 0;
     }
   }
-  __threadfence();
   __syncthreads();
   // the state, once every pair has been decided on the one of before
   for (int i = tid; i < a.m; i += kThreads) {
@@ -383,11 +381,9 @@ __global__ __launch_bounds__(kThreads) void compact_small_kernel(
   const PagesArgs& a = c.a;
   const int P = a.g.n_pages;
   for (int p = threadIdx.x; p < P; p += kThreads) a.extra[p] = -1;
-  __threadfence();
   __syncthreads();
   for (int b = threadIdx.x >> 6; b < a.g.batch; b += kThreads / kWave)
     count_pages(a, b, threadIdx.x & 63, kWave);
-  __threadfence();
   __syncthreads();
   int total = 0, low = 0;
   for (int seg = 0; seg * kSeg < P; ++seg)

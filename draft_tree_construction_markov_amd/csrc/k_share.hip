@@ -34,6 +34,8 @@ __device__ __forceinline__ int share_pages(const ShareArgs& a, int b) {
   return len.y < 0 ? 0 : min(len.x, cap - 1) >> g.shift;
 }
 
+// A value that other waves of this workgroup may have written before a
+// barrier: read past the L1, as atomics write.
 __device__ __forceinline__ int fresh(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -229,7 +231,6 @@ __global__ __launch_bounds__(kPackThreads) void share_pack_kernel(
   __shared__ PackLds s;
   share_pack(a, s.lead, s.rows, s.at, s.wave_sum);
   if (!with_rows) return;
-  __threadfence();
   __syncthreads();
   for (int b = threadIdx.x >> 6; b < a.g.batch; b += kPackThreads / kWave)
     share_rows(a, b, threadIdx.x & 63, kWave);
@@ -249,17 +250,14 @@ __global__ __launch_bounds__(kPackThreads) void share_small_kernel(
     a.count[p] = 0;
     a.lead[p] = 0x7fffffff;
   }
-  __threadfence();
   __syncthreads();
   for (int b = wave; b < a.g.batch; b += kWaves)
     share_count(a, b, lane, kWave);
-  __threadfence();
   __syncthreads();
   for (int b = wave; b < a.g.batch; b += kWaves) {
     const uint64_t best = wave_max64(share_best(a, b, lane, kWave));
     if (lane == 0) share_pick(a, b, best);
   }
-  __threadfence();
   __syncthreads();
   for (int b = wave; b < a.g.batch; b += kWaves) {
     int lead = share_lead(a, b);
@@ -272,10 +270,8 @@ __global__ __launch_bounds__(kPackThreads) void share_small_kernel(
       if (lead >= 0) atomicAdd(&a.size[lead], 1);
     }
   }
-  __threadfence();
   __syncthreads();
   share_pack(a, s.lead, s.rows, s.at, s.wave_sum);
-  __threadfence();
   __syncthreads();
   for (int b = wave; b < a.g.batch; b += kWaves) share_rows(a, b, lane, kWave);
 }

@@ -50,27 +50,37 @@ __global__ __launch_bounds__(kJoinThreads) void shared_join_kernel(
   const int m = blockIdx.y * ROWS + threadIdx.x / LR, c = threadIdx.x % LR;
   if (m >= (rq.y + 1) * a.G || 4 * c >= g.D) return;
   JoinSum s{neg_inf(), 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  auto add_slots = [&](auto count, const RowSums& r, int dp, int x0)
+      __attribute__((always_inline)) {
+    constexpr int IN = decltype(count)::value;
+    float2 ml[IN];
+    float4 o[IN];
+#pragma unroll
+    for (int k = 0; k < IN; ++k) {
+      // (past the last run: that one again, without weight)
+      const int x = min(x0 + k, r.count - 1);
+      const int64_t slot =
+          r.first + r.step * x + (r.count > 1 && x == 0 ? 1 : 0);
+      const int64_t row = slot * r.mt + r.row;
+      ml[k] = r.ml[row];
+      o[k] = reinterpret_cast<const float4*>(r.o + row * dp)[c];
+    }
+    float m2 = s.m;
+#pragma unroll
+    for (int k = 0; k < IN; ++k) m2 = fmaxf(m2, ml[k].x);
+    s.scale(m2);
+#pragma unroll
+    for (int k = 0; k < IN; ++k)
+      if (x0 + k < r.count) s.add(ml[k], o[k]);
+  };
   auto add = [&](const RowSums& r, int dp) __attribute__((always_inline)) {
-    for (int x0 = 0; x0 < r.count; x0 += kInFlight) {
-      float2 ml[kInFlight];
-      float4 o[kInFlight];
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        // (past the last run: that one again, without weight)
-        const int x = min(x0 + k, r.count - 1);
-        const int64_t slot =
-            r.first + r.step * x + (r.count > 1 && x == 0 ? 1 : 0);
-        const int64_t row = slot * r.mt + r.row;
-        ml[k] = r.ml[row];
-        o[k] = reinterpret_cast<const float4*>(r.o + row * dp)[c];
-      }
-      float m2 = s.m;
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) m2 = fmaxf(m2, ml[k].x);
-      s.scale(m2);
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k)
-        if (x0 + k < r.count) s.add(ml[k], o[k]);
+    if (r.count == 1) {
+      add_slots(std::integral_constant<int, 1>{}, r, dp, 0);
+    } else if (r.count <= 3) {
+      add_slots(std::integral_constant<int, 3>{}, r, dp, 0);
+    } else {
+      for (int x0 = 0; x0 < r.count; x0 += kInFlight)
+        add_slots(std::integral_constant<int, kInFlight>{}, r, dp, x0);
     }
   };
   if (rq.w >= 0) {
@@ -144,6 +154,7 @@ Parts parts_of(int batch, int N, int64_t cap, int G, int Hkv, int D) {
   int64_t rt = all / p.mt + batch / 2 + 1;
   x.shared = part_of(p, rt, rt * Hkv, 0);
   p = plan_attend(batch, M, cap, Hkv, D);
+  if (p.mt == 128 && p.dp <= 128) p.mt = 64;
   rt = (M + p.mt - 1) / p.mt;
   x.own = part_of(p, rt, rt * Hkv * batch, x.shared.end);
   return x;
