@@ -916,7 +916,7 @@ class SharePlan:
         req = plan[:4 * batch].view(batch, 4)
         req[:, 1] = -1
         req[:, 3] = -1
-        plan[8 * batch:9 * batch] = -1
+        plan[8 * batch:10 * batch] = -1
         self.out = CacheShare(
             leader=torch.arange(batch, **i32), shared=torch.zeros(batch, **i32),
             plan=plan, key=(batch, N, n_pages, page_size, max_pages))

@@ -29,13 +29,13 @@ ShareView view_of(const pct_cache_shape* sh, const void* share) {
   ShareView v{};
   v.req = static_cast<int4*>(const_cast<void*>(share));
   v.groups = v.req + sh->batch;
-  v.group_of = reinterpret_cast<int32_t*>(v.groups + sh->batch);
-  v.rows = v.group_of + sh->batch;
+  v.group_of = reinterpret_cast<int2*>(v.groups + sh->batch);
+  v.rows = reinterpret_cast<int32_t*>(v.group_of + sh->batch);
   return v;
 }
 
 size_t share_size(const pct_cache_shape* sh) {
-  return (size_t)sh->batch * (2 * sizeof(int4) + sizeof(int32_t)) +
+  return (size_t)sh->batch * (2 * sizeof(int4) + sizeof(int2)) +
          (size_t)sh->batch * (sh->N + 1) * sizeof(int32_t);
 }
 

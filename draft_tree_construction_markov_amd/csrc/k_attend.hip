@@ -204,7 +204,7 @@ hipError_t launch_tree_attention(const AttendArgs& a, void* workspace,
   char* base = static_cast<char*>(workspace);
   AttendWs ws{reinterpret_cast<float*>(base + w.o),
               reinterpret_cast<float2*>(base + w.ml),
-              reinterpret_cast<int4*>(base + w.meta), p.row_tiles};
+              reinterpret_cast<int4*>(base + w.meta), p.row_tiles, p.n_wg};
   hipError_t e;
   {
     ProfScope ps(PROF_ATTEND, (int64_t)g.batch * (g.N + 1), s);

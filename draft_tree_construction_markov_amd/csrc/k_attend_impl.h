@@ -136,7 +136,7 @@ struct AttendReq {
 };
 // before: the request's shared positions (own keys); rows: of a group (shared
 // keys, all of which are context)
-template <int MT, int KS, int PART = kAllKeys>
+template <int MT, int KS, int PART = kAllKeys, int EXTRA = 0>
 __device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
                                                     int ctx, int n,
                                                     int before = 0,
@@ -155,12 +155,12 @@ __device__ __forceinline__ AttendReq attend_lengths(const AttendArgs& a,
   r.M = (PART == kSharedKeys ? rows : n + 1) * a.G;
   r.RT = (r.M + MT - 1) / MT;
   r.KT = (r.L + KS - 1) / KS;
-  r.units = (int64_t)a.g.Hkv * r.RT * r.KT;
+  r.units = (int64_t)a.g.Hkv * r.RT * (r.KT + EXTRA);
   return r;
 }
 // Lengths of request b; uniform: b is the same in every lane, and the lengths
 // are held in scalar registers.
-template <int MT, int KS, int PART = kAllKeys>
+template <int MT, int KS, int PART = kAllKeys, int EXTRA = 0>
 __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
                                                 bool uniform = false) {
   const PageGeom& g = a.g;
@@ -172,8 +172,9 @@ __device__ __forceinline__ AttendReq attend_req(const AttendArgs& a, int b,
       x.z = __builtin_amdgcn_readfirstlane(x.z);
     }
     return PART == kSharedKeys
-               ? attend_lengths<MT, KS, PART>(a, x.y - 1, 0, 0, x.z)
-               : attend_lengths<MT, KS, PART>(a, x.x, x.y, x.z << g.shift);
+               ? attend_lengths<MT, KS, PART, EXTRA>(a, x.y - 1, 0, 0, x.z)
+               : attend_lengths<MT, KS, PART, EXTRA>(a, x.x, x.y,
+                                                     x.z << g.shift);
   }
   int n = g.n_nodes ? clamp_nodes(g.n_nodes[b], g.N) : g.N;
   int ctx = clamp_ctx(g.ctx_len[b]);
@@ -242,25 +243,30 @@ struct AttendRun {
     const int j = (int)div_up_to_64((x + 1) * blocks - 1, total);
     return level < 0 ? j : level * blocks + j;
   }
+  template <int EXTRA>
   __device__ __forceinline__ int64_t units(const AttendArgs& a,
                                            const AttendReq& rq) const {
-    return level < 0 ? rq.units
-                     : (rq.M > 0 ? (int64_t)a.g.Hkv * rq.KT : (int64_t)0);
+    return level < 0
+               ? rq.units
+               : (rq.M > 0 ? (int64_t)a.g.Hkv * (rq.KT + EXTRA) : (int64_t)0);
   }
 };
 
 // The steps [k0, k1) of head h and row tile rt that a run has from unit u on;
-// s0: the row tile's first unit.
+// s0: the row tile's first unit.  EXTRA: units that a row tile counts beyond
+// its steps, behind them, for what beginning and ending it costs; a run that
+// begins among them has none of its steps (k0 >= KT).
 struct AttendPiece {
   int h, rt, k0, k1;
   int64_t s0;
 };
+template <int EXTRA = 0>
 __device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
                                                     const AttendRun& run) {
   AttendPiece p;
   const int64_t in = run.u - run.b_off;
-  const int seg = (int)div_up_to_64(in, rq.KT);
-  p.k0 = (int)(in - (int64_t)seg * rq.KT);
+  const int seg = (int)div_up_to_64(in, rq.KT + EXTRA);
+  p.k0 = (int)(in - (int64_t)seg * (rq.KT + EXTRA));
   p.k1 = (int)min((int64_t)rq.KT, p.k0 + run.end - run.u);
   p.s0 = run.u - p.k0;
   p.h = run.level < 0 ? seg / rq.RT : seg;
@@ -269,22 +275,23 @@ __device__ __forceinline__ AttendPiece attend_piece(const AttendReq& rq,
 }
 
 // Moves on to the request that holds unit u.
-template <int MT, int KS, int PART = kAllKeys>
+template <int MT, int KS, int PART = kAllKeys, int EXTRA = 0>
 __device__ __forceinline__ void next_request(const AttendArgs& a,
                                              AttendRun& run, AttendReq& rq) {
-  while (run.u >= run.b_off + run.units(a, rq)) {
-    run.b_off += run.units(a, rq);
-    rq = attend_req<MT, KS, PART>(a, ++run.b, true);
+  while (run.u >= run.b_off + run.units<EXTRA>(a, rq)) {
+    run.b_off += run.units<EXTRA>(a, rq);
+    rq = attend_req<MT, KS, PART, EXTRA>(a, ++run.b, true);
   }
 }
 
-// Fills in the run of this workgroup; false when it has none (its entry of
-// the join is then empty).  Every wave does this by itself: lane l goes
+// Fills in the run of workgroup `block` of n_wg; false when it has none (its
+// entry of the join is then empty).  Every wave does this by itself: lane l goes
 // through requests l per .. (l + 1) per - 1, and the sums over lanes need no
 // LDS.
-template <int MT, int KS, int FEW, int LEAST, int PART = kAllKeys>
+template <int MT, int KS, int FEW, int LEAST, int PART = kAllKeys,
+          int EXTRA = 0>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
-                                                const AttendWs& ws,
+                                                const AttendWs& ws, int block,
                                                 AttendRun& r, AttendReq& rq) {
   const PageGeom& g = a.g;
   const int lane = threadIdx.x & 63;
@@ -296,10 +303,10 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   AttendReq q{};
 #pragma unroll 4
   for (int b = b0; b < b1; ++b) {
-    q = attend_req<MT, KS, PART>(a, b);
+    q = attend_req<MT, KS, PART, EXTRA>(a, b);
     mine += q.units;
     if (q.M > 0) {
-      mine1 += (int64_t)g.Hkv * q.KT;
+      mine1 += (int64_t)g.Hkv * (q.KT + EXTRA);
       least = min(least, q.RT);
       most = max(most, q.RT);
       tiles += (float)(g.Hkv * q.RT);
@@ -323,8 +330,10 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   // steps of a row tile, on average
   const int steps = max(1, (int)((float)total / fmaxf(wave_sum(tiles), 1.f)));
   const bool same = __ballot(least != 0x7fffffff && least != RT) == 0;
-  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
-  const int n_wg = gridDim.x, per_xcd = n_wg >> 3;
+  if (PART == kAllKeys) block = blockIdx.x;
+  const int xcd = block & 7, at = block >> 3;
+  const int n_wg = PART == kAllKeys ? (int)gridDim.x : ws.n_wg;
+  const int per_xcd = n_wg >> 3;
   // levels, if they keep at least 4 of 5 workgroups busy
   int bx = RT > 0 ? per_xcd / RT : 0;  // blocks of an XCD
   const int fit =
@@ -378,8 +387,8 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
         a, __builtin_amdgcn_readlane(q.ctx, l),
         __builtin_amdgcn_readlane(q.n, l));
   } else {
-    rq = attend_req<MT, KS, PART>(a, r.b, true);
-    next_request<MT, KS, PART>(a, r, rq);
+    rq = attend_req<MT, KS, PART, EXTRA>(a, r.b, true);
+    next_request<MT, KS, PART, EXTRA>(a, r, rq);
   }
   return true;
 }

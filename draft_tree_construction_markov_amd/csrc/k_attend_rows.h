@@ -39,6 +39,7 @@ struct RowsCfg {
   static constexpr int LDS = LDS_TILES > LDS_DUMP ? LDS_TILES : LDS_DUMP;
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
   static constexpr int FEW = kRowsFew, LEAST = kRowsLeast;  // of a run
+  static constexpr int EXTRA = PART == kAllKeys ? 0 : kRowsExtra;
 };
 
 // 16 bytes that nothing reads again soon
@@ -49,12 +50,20 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
 }
 
 template <class C>
-__global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
-    AttendArgs a, AttendWs ws) {
+struct RowsLds {
+  __align__(16) uint4 tiles[C::LDS / 16];
+  float dump_m[4][C::MT], dump_l[4][C::MT];
+};
+
+template <class C>
+__device__ __forceinline__ void attend_rows(const AttendArgs& a,
+                                            const AttendWs& ws, int block,
+                                            RowsLds<C>& mem) {
   constexpr int NT = C::NT, KB = C::KB, CH = C::CH, NL = C::NL;
   constexpr int DT = C::DT, KSTEP = C::KSTEP;
-  __shared__ __align__(16) uint4 lds[C::LDS / 16];
-  __shared__ float dump_m[4][C::MT], dump_l[4][C::MT];
+  uint4* const lds = mem.tiles;
+  float(*const dump_m)[C::MT] = mem.dump_m;
+  float(*const dump_l)[C::MT] = mem.dump_l;
 
   const PageGeom& g = a.g;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -63,8 +72,8 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
 
   AttendRun run;
   AttendReq rq;
-  if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST, C::PART>(a, ws, run,
-                                                                rq))
+  if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST, C::PART, C::EXTRA>(
+          a, ws, block, run, rq))
     return;
   i32x4 join = {0, 0, 0, -1};
 
@@ -76,9 +85,13 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
   uint4* vt = kt + KB * C::KROW;
 
   while (run.u < run.end) {
-    next_request<C::MT, C::KS, C::PART>(a, run, rq);
+    next_request<C::MT, C::KS, C::PART, C::EXTRA>(a, run, rq);
     const int b = run.b;
-    const AttendPiece pc = attend_piece(rq, run);
+    const AttendPiece pc = attend_piece<C::EXTRA>(rq, run);
+    if (C::EXTRA > 0 && pc.k0 >= rq.KT) {
+      run.u = pc.s0 + rq.KT + C::EXTRA;
+      continue;
+    }
     const int h = pc.h, rt = pc.rt, k0 = pc.k0, k1 = pc.k1;
     const int ctx = rq.ctx, L = rq.L;
     const int32_t* table = attend_table<C::PART>(a, b);
@@ -247,7 +260,7 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     int64_t slot = 2 * run.run + (k0 == 0 ? 1 : 0);
     if constexpr (C::PART != kAllKeys)
       if (whole)
-        slot = 2 * (int64_t)gridDim.x +
+        slot = 2 * (int64_t)ws.n_wg +
                part_tile<C::PART>(a, ws, b, h, rt, C::MT);
     float* part_o = ws.o + slot * C::MT * C::DP;
     float2* part_ml = ws.ml + slot * C::MT;
@@ -290,9 +303,16 @@ __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
       }
     }
     __syncthreads();
-    run.u += pc.k1 - pc.k0;
+    run.u += pc.k1 - pc.k0 + (k1 == rq.KT ? C::EXTRA : 0);
   }
   if (tid == 0 && ws.row_tiles == 0) store_meta(ws, run.run, join);
+}
+
+template <class C>
+__global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
+    AttendArgs a, AttendWs ws) {
+  __shared__ RowsLds<C> mem;
+  attend_rows<C>(a, ws, blockIdx.x, mem);
 }
 
 }  // namespace pct

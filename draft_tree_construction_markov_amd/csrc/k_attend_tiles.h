@@ -57,6 +57,7 @@ struct TilesCfg {
   static constexpr int TPV = 64 / GPS;      // tiles whose pages fit a wave
   static constexpr int OCC = DP <= 128 ? 2 : 1;  // workgroups per CU
   static constexpr int FEW = kTilesFew, LEAST = tiles_least(MT);  // of a run
+  static constexpr int EXTRA = PART == kAllKeys ? 0 : kTilesExtra;
   static __device__ __forceinline__ int swizzle_k(int r) {
     return SL == 8 ? (r >> 1) & 7 : r & 15;
   }
@@ -422,7 +423,7 @@ __device__ __forceinline__ void tiles_piece(
   int64_t to_slot = slot;
   if constexpr (C::PART != kAllKeys)
     if (whole)
-      to_slot = 2 * (int64_t)gridDim.x +
+      to_slot = 2 * (int64_t)ws.n_wg +
                 part_tile<C::PART>(a, ws, b, h, (m0 - 16 * NT * wave) / C::MT,
                                    C::MT);
 #pragma unroll
@@ -461,15 +462,22 @@ __device__ __forceinline__ void tiles_piece(
 }
 
 template <class C>
-__global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
-    AttendArgs a, AttendWs ws) {
+struct TilesLds {
+  __align__(16) uint4 tiles[4 * C::KB * C::SL];
+  uint64_t odd_s[2][C::W];
+};
+
+template <class C>
+__device__ __forceinline__ void attend_tiles(const AttendArgs& a,
+                                             const AttendWs& ws, int block,
+                                             uint4* tiles,
+                                             uint64_t (*odd_s)[C::W]) {
   constexpr int KB = C::KB, SL = C::SL, MT = C::MT;
-  __shared__ __align__(16) uint4 tiles[4 * KB * SL];
-  __shared__ uint64_t odd_s[2][C::W];
 
   AttendRun run;
   AttendReq rq;
-  if (!attend_schedule<MT, KB, C::FEW, C::LEAST, C::PART>(a, ws, run, rq))
+  if (!attend_schedule<MT, KB, C::FEW, C::LEAST, C::PART, C::EXTRA>(
+          a, ws, block, run, rq))
     return;
   i32x4 join = {0, 0, 0, -1};
   if ((a.g.D >> 3) < SL) {
@@ -479,9 +487,13 @@ __global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
       tiles[i] = zero;
   }
   while (run.u < run.end) {
-    next_request<MT, KB, C::PART>(a, run, rq);
+    next_request<MT, KB, C::PART, C::EXTRA>(a, run, rq);
     const int b = run.b;
-    const AttendPiece pc = attend_piece(rq, run);
+    const AttendPiece pc = attend_piece<C::EXTRA>(rq, run);
+    if (C::EXTRA > 0 && pc.k0 >= rq.KT) {
+      run.u = pc.s0 + rq.KT + C::EXTRA;
+      continue;
+    }
     // (the same in every lane, which the compiler cannot see)
     const int h = __builtin_amdgcn_readfirstlane(pc.h);
     const int m0 = __builtin_amdgcn_readfirstlane(pc.rt * MT);
@@ -490,7 +502,49 @@ __global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
     tiles_piece<C>(a, ws, rq, b, h, m0, k0, k1, 2 * run.run + (k0 == 0),
                    tiles, odd_s);
     note_piece<C::PART, MT>(a, ws, run, rq, pc, join);
-    run.u += pc.k1 - pc.k0;
+    run.u += pc.k1 - pc.k0 + (k1 == rq.KT ? C::EXTRA : 0);
+  }
+  if (threadIdx.x == 0 && ws.row_tiles == 0) store_meta(ws, run.run, join);
+}
+
+// (attend_tiles written out once more: as a call the kernel of 128 rows keeps
+// other values in registers, 32 trees of 257 rows 625 -> 638 .. 650 us)
+template <class C>
+__global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
+    AttendArgs a, AttendWs ws) {
+  constexpr int KB = C::KB, SL = C::SL, MT = C::MT;
+  __shared__ __align__(16) uint4 tiles[4 * KB * SL];
+  __shared__ uint64_t odd_s[2][C::W];
+
+  AttendRun run;
+  AttendReq rq;
+  if (!attend_schedule<MT, KB, C::FEW, C::LEAST, C::PART, C::EXTRA>(
+          a, ws, blockIdx.x, run, rq))
+    return;
+  i32x4 join = {0, 0, 0, -1};
+  if ((a.g.D >> 3) < SL) {
+    // slots past the head size are read and never loaded
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 4 * KB * SL; i += 64 * C::W)
+      tiles[i] = zero;
+  }
+  while (run.u < run.end) {
+    next_request<MT, KB, C::PART, C::EXTRA>(a, run, rq);
+    const int b = run.b;
+    const AttendPiece pc = attend_piece<C::EXTRA>(rq, run);
+    if (C::EXTRA > 0 && pc.k0 >= rq.KT) {
+      run.u = pc.s0 + rq.KT + C::EXTRA;
+      continue;
+    }
+    // (the same in every lane, which the compiler cannot see)
+    const int h = __builtin_amdgcn_readfirstlane(pc.h);
+    const int m0 = __builtin_amdgcn_readfirstlane(pc.rt * MT);
+    const int k0 = __builtin_amdgcn_readfirstlane(pc.k0);
+    const int k1 = __builtin_amdgcn_readfirstlane(pc.k1);
+    tiles_piece<C>(a, ws, rq, b, h, m0, k0, k1, 2 * run.run + (k0 == 0),
+                   tiles, odd_s);
+    note_piece<C::PART, MT>(a, ws, run, rq, pc, join);
+    run.u += pc.k1 - pc.k0 + (k1 == rq.KT ? C::EXTRA : 0);
   }
   if (threadIdx.x == 0 && ws.row_tiles == 0) store_meta(ws, run.run, join);
 }

@@ -22,8 +22,8 @@ constexpr int kSmallPlaces = 64;      // places, that one workgroup goes through
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // A value that other waves of this workgroup may have written before a
-// barrier: read past the L1, as atomics write.  (The barrier waits for them; a
-// fence for the whole GPU in its place writes back the L2, 2 .. 5 us each.)
+// barrier: read past the L1, as atomics write.  (The barrier orders what one
+// workgroup does; fences for the whole GPU write back the L2, 2 .. 5 us each.)
 __device__ __forceinline__ int fresh(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }

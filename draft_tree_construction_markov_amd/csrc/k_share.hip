@@ -115,7 +115,7 @@ __device__ __forceinline__ int share_lead(const ShareArgs& a, int b) {
 // Results, and the rows packed by group: groups in the order of their
 // leaders, requests of a group in theirs.  One workgroup, a thread a request.
 __device__ __forceinline__ void share_pack(const ShareArgs& a, int* lead_s,
-                                           int* rows_s, int* at_s,
+                                           int* rows_s, int2* at_s,
                                            int2 (*wave_sum)) {
   const PageGeom& g = a.g;
   const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
@@ -157,7 +157,7 @@ __device__ __forceinline__ void share_pack(const ShareArgs& a, int* lead_s,
   const int group = head.x + sum.x - 1, first = head.y + sum.y - all;
   if (leads) {
     a.view.groups[group] = make_int4(b, (d + 1) << g.shift, all, first);
-    at_s[b] = group;
+    at_s[b] = make_int2(group, first);
   }
   // groups that are not there have no rows
   for (int x = groups + b; x < g.batch; x += kPackThreads)
@@ -165,23 +165,23 @@ __device__ __forceinline__ void share_pack(const ShareArgs& a, int* lead_s,
   __syncthreads();
   if (in)
     a.view.req[b] = make_int4(len.x, len.y, d + 1, lead >= 0 ? before : -1);
-  if (in) a.view.group_of[b] = lead >= 0 ? at_s[lead] : -1;
+  if (in) a.view.group_of[b] = lead >= 0 ? at_s[lead] : make_int2(-1, 0);
 }
 
 // Rows i = t, t + threads .. of request b into the packed order.
 __device__ __forceinline__ void share_rows(const ShareArgs& a, int b, int t,
                                            int threads) {
-  const int at = fresh(a.view.group_of + b);
-  if (at < 0) return;
+  const int32_t* at = reinterpret_cast<const int32_t*>(a.view.group_of + b);
+  if (fresh(at) < 0) return;
   const int R = a.g.N + 1;
   const int n = share_lengths(a, b).y;
-  const int to = fresh(&a.view.groups[at].w) + fresh(&a.view.req[b].w);
+  const int to = fresh(at + 1) + fresh(&a.view.req[b].w);
   for (int i = t; i <= n; i += threads) a.view.rows[to + i] = b * R + i;
 }
 
 struct PackLds {
-  int lead[kPackThreads], rows[kPackThreads], at[kPackThreads];
-  int2 wave_sum[kPackThreads / kWave];
+  int lead[kPackThreads], rows[kPackThreads];
+  int2 at[kPackThreads], wave_sum[kPackThreads / kWave];
 };
 
 __global__ __launch_bounds__(256) void share_clear_kernel(ShareArgs a) {

@@ -26,8 +26,7 @@ struct RowSums {
 
 __device__ __forceinline__ RowSums row_sums(const AttendWs& ws,
                                             const AttendPlan& p, int64_t tile,
-                                            int row) {
-  const int4 meta = ws.meta[tile];
+                                            const int4& meta, int row) {
   RowSums r{ws.o, ws.ml, 0, 2, 1, p.mt, row};
   if (meta.y < 0) {
     r.first = 2 * (int64_t)p.n_wg + tile;
@@ -47,6 +46,7 @@ __global__ __launch_bounds__(kJoinThreads) void shared_join_kernel(
   const PageGeom& g = a.g;
   const int b = blockIdx.x / g.Hkv, h = blockIdx.x - b * g.Hkv;
   const int4 rq = a.share.req[b];
+  const int2 group = a.share.group_of[b];
   const int m = blockIdx.y * ROWS + threadIdx.x / LR, c = threadIdx.x % LR;
   if (m >= (rq.y + 1) * a.G || 4 * c >= g.D) return;
   JoinSum s{neg_inf(), 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -83,19 +83,17 @@ __global__ __launch_bounds__(kJoinThreads) void shared_join_kernel(
         add_slots(std::integral_constant<int, kInFlight>{}, r, dp, x0);
     }
   };
-  if (rq.w >= 0) {
-    const int at = a.share.group_of[b];
-    const int first = a.share.groups[at].w;
-    const int pm = rq.w * a.G + m, rt = pm / ps.mt;
-    add(row_sums(ws, ps,
-                 (int64_t)h * ws.row_tiles + first * a.G / ps.mt + at + rt,
-                 pm - rt * ps.mt),
-        ps.dp);
-  }
+  // (both row tiles' notes on their way before either's sums)
   const int rt = m / po.mt;
-  add(row_sums(wo, po, ((int64_t)b * g.Hkv + h) * wo.row_tiles + rt,
-               m - rt * po.mt),
-      po.dp);
+  const int64_t own = ((int64_t)b * g.Hkv + h) * wo.row_tiles + rt;
+  const int4 own_meta = wo.meta[own];
+  if (group.x >= 0) {
+    const int pm = rq.w * a.G + m, prt = pm / ps.mt;
+    const int64_t tile = (int64_t)h * ws.row_tiles +
+                         group.y * a.G / ps.mt + group.x + prt;
+    add(row_sums(ws, ps, tile, ws.meta[tile], pm - prt * ps.mt), ps.dp);
+  }
+  add(row_sums(wo, po, own, own_meta, m - rt * po.mt), po.dp);
   const int i = m / a.G;
   const int64_t row =
       ((int64_t)b * (g.N + 1) + i) * a.Hq + h * a.G + (m - i * a.G);
@@ -163,18 +161,8 @@ Parts parts_of(int batch, int N, int64_t cap, int G, int Hkv, int D) {
 AttendWs workspace_of(const Part& x, char* base) {
   return AttendWs{reinterpret_cast<float*>(base + x.o),
                   reinterpret_cast<float2*>(base + x.ml),
-                  reinterpret_cast<int4*>(base + x.meta), x.row_tiles};
-}
-
-hipError_t launch_part(const AttendArgs& a, const Part& x, const AttendWs& ws,
-                       int part, hipStream_t s) {
-  switch (x.plan.dp) {
-    case 64: return launch_share_d64(a, x.plan, ws, part, s);
-    case 96: return launch_share_d96(a, x.plan, ws, part, s);
-    case 128: return launch_share_d128(a, x.plan, ws, part, s);
-    case 192: return launch_share_d192(a, x.plan, ws, part, s);
-    default: return launch_share_d256(a, x.plan, ws, part, s);
-  }
+                  reinterpret_cast<int4*>(base + x.meta), x.row_tiles,
+                  x.plan.n_wg};
 }
 
 }  // namespace
@@ -191,21 +179,24 @@ hipError_t launch_shared_attention(const AttendArgs& a, void* workspace,
   const Parts x = parts_of(g.batch, g.N, (int64_t)g.max_pages << g.shift, a.G,
                            g.Hkv, g.D);
   char* base = static_cast<char*>(workspace);
-  const AttendWs ws = workspace_of(x.shared, base);
-  const AttendWs wo = workspace_of(x.own, base);
+  AttendParts parts{{a, a},
+                    {x.shared.plan, x.own.plan},
+                    {workspace_of(x.shared, base), workspace_of(x.own, base)}};
+  parts.a[0].mask = nullptr;
+  parts.a[0].g.batch = g.batch / 2;  // groups at most
+  if (g.batch == 1) parts.p[0].n_wg = parts.ws[0].n_wg = 0;
+  const AttendWs &ws = parts.ws[0], &wo = parts.ws[1];
   const int64_t rows = (int64_t)g.batch * (g.N + 1);
   hipError_t e;
-  if (g.batch > 1) {
-    AttendArgs shared = a;
-    shared.mask = nullptr;
-    shared.g.batch = g.batch / 2;  // groups at most
-    ProfScope prof(PROF_ATTEND, rows, s);
-    e = launch_part(shared, x.shared, ws, kSharedKeys, s);
-    if (e != hipSuccess) return e;
-  }
   {
     ProfScope prof(PROF_ATTEND, rows, s);
-    e = launch_part(a, x.own, wo, kOwnKeys, s);
+    switch (x.own.plan.dp) {
+      case 64: e = launch_parts_d64(parts, s); break;
+      case 96: e = launch_parts_d96(parts, s); break;
+      case 128: e = launch_parts_d128(parts, s); break;
+      case 192: e = launch_parts_d192(parts, s); break;
+      default: e = launch_parts_d256(parts, s); break;
+    }
   }
   if (e != hipSuccess) return e;
   ProfScope prof(PROF_JOIN, rows, s);

@@ -1,11 +1,9 @@
 // k_shared_d64.hip -- attention in two parts (shared and own keys) for heads
 // padded to 64 elements.
-#include "k_attend_launch.h"
+#include "k_shared_launch.h"
 
 namespace pct {
-hipError_t launch_share_d64(const AttendArgs& a, const AttendPlan& p,
-                            const AttendWs& ws, int part, hipStream_t s) {
-  return part == kSharedKeys ? launch_attend_dp<64, kSharedKeys>(a, p, ws, s)
-                             : launch_attend_dp<64, kOwnKeys>(a, p, ws, s);
+hipError_t launch_parts_d64(const AttendParts& x, hipStream_t s) {
+  return launch_parts_dp<64>(x, s);
 }
 }  // namespace pct

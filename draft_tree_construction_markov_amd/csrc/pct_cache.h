@@ -112,7 +112,7 @@ struct ShareView {
                       // its group before its own, or -1: no group}
   int4* groups;       // [batch] {leader, shared positions, rows (0: no such
                       // group), first packed row}
-  int32_t* group_of;  // [batch] or -1
+  int2* group_of;     // [batch] {group or -1, its first packed row}
   int32_t* rows;      // [batch * (N + 1)] row of each packed row
 };
 struct ShareArgs {
@@ -173,6 +173,13 @@ constexpr int kHalfUnits = 6144;
 constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
 constexpr int tiles_least(int mt) { return mt == 64 ? 8 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X
+// In two parts (below) a row tile counts as so many steps more than it has, for
+// its beginning and its end, or runs of many short row tiles would end last:
+// 123 requests of one token over 64 .. 4096 own keys each and two shared
+// prefixes 255 us without, 16 requests of 65 rows 218; with 1 / 1 step of keys
+// per wave / of shared tiles 216 and 210, with 1 / 3 209 and 202, with 2 / 2
+// 213 and 204, with 1 / 6 210 and 208.
+constexpr int kRowsExtra = 1, kTilesExtra = 3;
 // fp16 holds probabilities times 2^kLift (k_attend_impl.h has the reason).
 template <bool BF16>
 constexpr float kLift = BF16 ? 0.f : 7.f;
@@ -192,6 +199,7 @@ struct AttendWs {
   float2* ml;  // [2 n_wg (+ tiles)][mt] {m, sum}
   int4* meta;  // [n_wg] or [tiles]
   int row_tiles;  // of a request at most (shared keys: of all groups)
+  int n_wg;
 };
 hipError_t launch_attend_d64(const AttendArgs&, const AttendPlan&,
                              const AttendWs&, hipStream_t);
@@ -203,16 +211,18 @@ hipError_t launch_attend_d192(const AttendArgs&, const AttendPlan&,
                               const AttendWs&, hipStream_t);
 hipError_t launch_attend_d256(const AttendArgs&, const AttendPlan&,
                               const AttendWs&, hipStream_t);
-hipError_t launch_share_d64(const AttendArgs&, const AttendPlan&,
-                            const AttendWs&, int part, hipStream_t);
-hipError_t launch_share_d96(const AttendArgs&, const AttendPlan&,
-                            const AttendWs&, int part, hipStream_t);
-hipError_t launch_share_d128(const AttendArgs&, const AttendPlan&,
-                            const AttendWs&, int part, hipStream_t);
-hipError_t launch_share_d192(const AttendArgs&, const AttendPlan&,
-                            const AttendWs&, int part, hipStream_t);
-hipError_t launch_share_d256(const AttendArgs&, const AttendPlan&,
-                            const AttendWs&, int part, hipStream_t);
+// The two parts of a call: arguments, tiles and workspaces of the shared keys
+// (no workgroups: no part) and of the own ones.
+struct AttendParts {
+  AttendArgs a[2];
+  AttendPlan p[2];
+  AttendWs ws[2];
+};
+hipError_t launch_parts_d64(const AttendParts&, hipStream_t);
+hipError_t launch_parts_d96(const AttendParts&, hipStream_t);
+hipError_t launch_parts_d128(const AttendParts&, hipStream_t);
+hipError_t launch_parts_d192(const AttendParts&, hipStream_t);
+hipError_t launch_parts_d256(const AttendParts&, hipStream_t);
 hipError_t launch_tree_attention(const AttendArgs& a, void* ws,
                                  hipStream_t s);
 size_t tree_attention_workspace(const pct_cache_shape& sh);
