@@ -40,7 +40,8 @@ size_t share_size(const pct_cache_shape* sh) {
 }
 
 size_t share_workspace(const pct_cache_shape* sh) {
-  return ((size_t)2 * sh->n_pages + (size_t)3 * sh->batch) * sizeof(int32_t);
+  return (size_t)sh->batch * ((size_t)share_blocks(*sh) * sizeof(uint64_t) +
+                              2 * sizeof(int32_t));
 }
 
 }  // namespace
@@ -83,11 +84,11 @@ pct_status pct_cache_share(const pct_cache_shape* shape, int32_t least,
   ShareArgs a{};
   a.g = geom(shape, block_table, ctx_len, n_nodes);
   a.least = least;
-  a.count = static_cast<int32_t*>(workspace);
-  a.lead = a.count + shape->n_pages;
-  a.place = a.lead + shape->n_pages;
-  a.size = a.place + shape->batch;
-  a.joined = a.size + shape->batch;
+  a.best = static_cast<uint64_t*>(workspace);
+  a.blocks = share_blocks(*shape);
+  a.place =
+      reinterpret_cast<int32_t*>(a.best + (size_t)a.blocks * shape->batch);
+  a.joined = a.place + shape->batch;
   a.leader = leader;
   a.shared = shared;
   a.view = view_of(shape, share);

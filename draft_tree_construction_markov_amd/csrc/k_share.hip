@@ -1,14 +1,19 @@
 // k_share.hip -- which requests of a round share a prefix, found from their
 // block tables, and their rows packed by group for shared attention.
 //
-// A page in the contexts of c requests at place j of their tables stands for
-// (j + 1) pages that c - 1 of them need not read again, if what precedes it is
-// the same in all: gain_b(j) = (j + 1) (c(table[b][j]) - 1).  Each request
-// picks its page of most gain (the first such), so that it joins the requests
-// it has the most in common with, whoever else shares less.  Requests of one
-// pick whose tables agree up to it are a group.  A table is compared with the
-// leader's entry by entry: c only decides what is tried, so tables in which a
-// page stands at several places or after other pages cost speed at most.
+// A page that c requests have at place j of their tables, all within their
+// contexts, stands for (j + 1) pages that c - 1 of them need not read again,
+// if what precedes it is the same in all: gain = (j + 1) (c - 1).  Each
+// request picks its place of most gain (the first such), so that it joins the
+// requests it has the most in common with, whoever else shares less.  Requests
+// of one page and place are a group as far as their tables agree up to it,
+// entry by entry, with the first one's: c only decides what is tried.
+//
+// columns: workgroups of 4 places hold the tables' columns in LDS and
+// count by comparison (pages counted by atomics took 12 us for 128 tables of
+// up to 1281 pages, at 40 holders a page); pick: the best of all columns;
+// join: leaders, and the comparison with them; pack: one workgroup.  Each is
+// a few dependent loads; small tables go through all of it in one workgroup.
 #include "pct_cache.h"
 #include "pct_device.h"
 
@@ -16,8 +21,9 @@ namespace pct {
 
 namespace {
 
-constexpr int kShareThreads = 256;   // of a request
+constexpr int kShareThreads = 256;   // of a request, of columns
 constexpr int kPackThreads = 1024;
+constexpr int kWide = 2;             // log2 of the places of columns
 static_assert(kMaxShareBatch == kPackThreads, "a thread per request");
 
 __device__ __forceinline__ int2 share_lengths(const ShareArgs& a, int b) {
@@ -35,62 +41,80 @@ __device__ __forceinline__ int share_pages(const ShareArgs& a, int b) {
 }
 
 // A value that other waves of this workgroup may have written before a
-// barrier: read past the L1, as atomics write.
+// barrier: read past the L1.
 __device__ __forceinline__ int fresh(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__device__ __forceinline__ void share_count(const ShareArgs& a, int b, int t,
-                                            int threads) {
-  const int full = share_pages(a, b);
-  const int32_t* table = a.g.table + (int64_t)b * a.g.max_pages;
-  for (int j = t; j < full; j += threads) {
-    const int p = table[j];
-    if ((unsigned)p < (unsigned)a.g.n_pages) atomicAdd(&a.count[p], 1);
-  }
+// Gain and place in one number, larger for more gain, then for an earlier
+// place.  Gains are below 2^41 (2^30 places, 2^10 requests), of which a
+// place's bits leave 33: past them they count as alike.
+__device__ __forceinline__ uint64_t pick_key(int j, int c) {
+  const uint64_t gain = (uint64_t)(j + 1) * (uint64_t)(c - 1);
+  const uint64_t top = gain < (1ull << 33) ? gain : (1ull << 33) - 1;
+  return top == 0 ? 0 : top << 31 | (uint32_t)(0x7fffffff - j);
 }
 
-// A wave's part of request b's pick: gains and places in one number, larger
-// for more gain, then for an earlier place.  Gains are below 2^41 (2^30
-// places, 2^10 requests), of which a place's bits leave 33: past them they
-// count as alike.
-__device__ __forceinline__ uint64_t share_best(const ShareArgs& a, int b,
-                                               int t, int threads) {
-  const int full = share_pages(a, b);
-  const int32_t* table = a.g.table + (int64_t)b * a.g.max_pages;
-  uint64_t best = 0;
-  for (int j = t; j < full; j += threads) {
-    const int p = table[j];
-    if ((unsigned)p >= (unsigned)a.g.n_pages) continue;
-    const int c = fresh(a.count + p);
-    const uint64_t gain = (uint64_t)(j + 1) * (uint64_t)(c - 1);
-    const uint64_t top = gain < (1ull << 33) ? gain : (1ull << 33) - 1;
-    const uint64_t key = top << 31 | (uint32_t)(0x7fffffff - j);
-    if (gain > 0 && key > best) best = key;
-  }
-  return best;
-}
-
-__device__ __forceinline__ uint64_t wave_max64(uint64_t x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint64_t y = __shfl_xor((unsigned long long)x, d, kWave);
-    x = y > x ? y : x;
-  }
-  return x;
-}
-
-// Request b picks: its page and the place there, or none (-1).  One lane.
-__device__ __forceinline__ void share_pick(const ShareArgs& a, int b,
-                                           uint64_t best) {
+// Places j0 .. j0 + 2^wide - 1 of all tables, by the whole workgroup (of a
+// multiple of so many threads): entries to col [batch][2^wide] (-1: none),
+// then the best key of each request to best_s.  full_s: whole pages of the
+// requests.  A thread's entries are all at one place, so that a column's
+// entry is read once for kMine comparisons.
+template <int kMine>
+__device__ __forceinline__ void share_columns(const ShareArgs& a, int j0,
+                                              int wide, const int* full_s,
+                                              int* col,
+                                              unsigned long long* best_s) {
   const PageGeom& g = a.g;
-  int d = -1;
-  if (best != 0 && (int64_t)(best >> 31) << g.shift >= a.least) {
-    d = 0x7fffffff - (int)(best & 0x7fffffff);
-    atomicMin(&a.lead[g.table[(int64_t)b * g.max_pages + d]], b);
+  const int w = threadIdx.x & ((1 << wide) - 1), j = j0 + w;
+  const int first = threadIdx.x >> wide, step = blockDim.x >> wide;
+  const int at = min(j, g.max_pages - 1);
+  __syncthreads();
+  for (int b0 = first; b0 < g.batch; b0 += kMine * step) {
+    int p[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+      p[k] = g.table[(int64_t)min(b0 + k * step, g.batch - 1) * g.max_pages +
+                     at];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int b = b0 + k * step;
+      if (b < g.batch)
+        col[b << wide | w] =
+            j < full_s[b] && (unsigned)p[k] < (unsigned)g.n_pages ? p[k] : -1;
+    }
   }
-  a.place[b] = d;
-  a.size[b] = 0;
+  __syncthreads();
+  for (int b0 = first; b0 < g.batch; b0 += kMine * step) {
+    int mine[kMine], count[kMine];
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int b = b0 + k * step;
+      mine[k] = b < g.batch ? col[b << wide | w] : -1;
+      any = any || mine[k] >= 0;
+      count[k] = 0;
+    }
+    if (!any) continue;
+#pragma unroll 8
+    for (int x = 0; x < g.batch; ++x) {
+      const int p = col[x << wide | w];
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) count[k] += p == mine[k] ? 1 : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const uint64_t key = mine[k] < 0 ? 0 : pick_key(j, count[k]);
+      if (key != 0) atomicMax(&best_s[b0 + k * step], key);
+    }
+  }
+}
+
+// Request b's place by its best key, or none (-1).
+__device__ __forceinline__ int share_place(const ShareArgs& a, uint64_t best) {
+  return best != 0 && (int64_t)(best >> 31) << a.g.shift >= a.least
+             ? 0x7fffffff - (int)(best & 0x7fffffff)
+             : -1;
 }
 
 // Whether thread t's entries of request b agree with its leader's.
@@ -104,206 +128,246 @@ __device__ __forceinline__ bool share_agrees(const ShareArgs& a, int b,
   return same;
 }
 
-// Leader of request b by its pick, or -1.
-__device__ __forceinline__ int share_lead(const ShareArgs& a, int b) {
-  const int d = fresh(a.place + b);
-  if (d < 0) return -1;
-  const int lead = fresh(a.lead + a.g.table[(int64_t)b * a.g.max_pages + d]);
-  return fresh(a.place + lead) == d ? lead : -1;
+// Lowest of thread t's requests that picked the page of request b, place d.
+__device__ __forceinline__ int share_lead(const ShareArgs& a, int b, int d,
+                                          const int* place, int t,
+                                          int threads) {
+  const int32_t* at = a.g.table + d;
+  const int page = at[(int64_t)b * a.g.max_pages];
+  int lead = b;
+  for (int x = t; x < b; x += threads)
+    if (place[x] == d && at[(int64_t)x * a.g.max_pages] == page)
+      lead = min(lead, x);
+  return lead;
 }
 
 // Results, and the rows packed by group: groups in the order of their
 // leaders, requests of a group in theirs.  One workgroup, a thread a request.
-__device__ __forceinline__ void share_pack(const ShareArgs& a, int* lead_s,
-                                           int* rows_s, int2* at_s,
-                                           int2 (*wave_sum)) {
+struct PackLds {
+  int2 lead[kPackThreads];  // leader or -1, rows in a group
+  int to[kPackThreads], size[kPackThreads];
+  int2 group[kPackThreads], wave_sum[kPackThreads / kWave];
+};
+__device__ __forceinline__ void share_pack(const ShareArgs& a, PackLds& s,
+                                           bool with_rows) {
   const PageGeom& g = a.g;
   const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
   const bool in = b < g.batch;
   int2 len = make_int2(0, -1);
   int lead = -1, d = -1;
+  s.size[b] = 0;
   if (in) {
     len = share_lengths(a, b);
     lead = fresh(a.joined + b);
-    if (lead >= 0 && fresh(a.size + lead) < 2) lead = -1;
-    d = lead >= 0 ? fresh(a.place + b) : -1;
-    a.leader[b] = lead >= 0 ? lead : b;
-    a.shared[b] = (d + 1) << g.shift;
+    d = fresh(a.place + b);
   }
-  lead_s[b] = lead;
-  rows_s[b] = in && lead >= 0 ? len.y + 1 : 0;
+  __syncthreads();
+  if (lead >= 0) atomicAdd(&s.size[lead], 1);
+  __syncthreads();
+  if (lead >= 0 && s.size[lead] < 2) lead = -1;
+  if (lead < 0) d = -1;
+  s.lead[b] = make_int2(lead, lead >= 0 ? len.y + 1 : 0);
   __syncthreads();
   // rows of the group, and those before this request's
   int before = 0, all = 0;
-  for (int x = 0; x < g.batch; ++x) {
-    const int r = lead_s[x] == lead && lead >= 0 ? rows_s[x] : 0;
-    all += r;
-    before += x < b ? r : 0;
+  if (lead >= 0) {
+#pragma unroll 8
+    for (int x = 0; x < g.batch; ++x) {
+      const int2 y = s.lead[x];
+      const int r = y.x == lead ? y.y : 0;
+      all += r;
+      before += x < b ? r : 0;
+    }
   }
   // groups and their rows before this one's, at the leaders
   const bool leads = in && lead == b;
   int2 sum = make_int2(leads ? 1 : 0, leads ? all : 0);
-  for (int s = 1; s < kWave; s <<= 1) {
-    const int x = __shfl_up(sum.x, s, kWave), y = __shfl_up(sum.y, s, kWave);
-    if (lane >= s) sum.x += x, sum.y += y;
+  for (int k = 1; k < kWave; k <<= 1) {
+    const int x = __shfl_up(sum.x, k, kWave), y = __shfl_up(sum.y, k, kWave);
+    if (lane >= k) sum.x += x, sum.y += y;
   }
-  if (lane == kWave - 1) wave_sum[wave] = sum;
+  if (lane == kWave - 1) s.wave_sum[wave] = sum;
   __syncthreads();
   int2 head = make_int2(0, 0);
-  for (int w = 0; w < wave; ++w)
-    head.x += wave_sum[w].x, head.y += wave_sum[w].y;
   int groups = 0;
-  for (int w = 0; w < kPackThreads / kWave; ++w) groups += wave_sum[w].x;
-  const int group = head.x + sum.x - 1, first = head.y + sum.y - all;
+  for (int w = 0; w < kPackThreads / kWave; ++w) {
+    const int2 x = s.wave_sum[w];
+    groups += x.x;
+    if (w < wave) head.x += x.x, head.y += x.y;
+  }
   if (leads) {
-    a.view.groups[group] = make_int4(b, (d + 1) << g.shift, all, first);
-    at_s[b] = make_int2(group, first);
+    const int2 group = make_int2(head.x + sum.x - 1, head.y + sum.y - all);
+    a.view.groups[group.x] = make_int4(b, (d + 1) << g.shift, all, group.y);
+    s.group[b] = group;
   }
   // groups that are not there have no rows
-  for (int x = groups + b; x < g.batch; x += kPackThreads)
-    a.view.groups[x] = make_int4(0, 0, 0, 0);
+  if (groups + b < g.batch) a.view.groups[groups + b] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  if (in)
+  if (in) {
+    const int2 group = lead >= 0 ? s.group[lead] : make_int2(-1, 0);
+    a.leader[b] = lead >= 0 ? lead : b;
+    a.shared[b] = (d + 1) << g.shift;
     a.view.req[b] = make_int4(len.x, len.y, d + 1, lead >= 0 ? before : -1);
-  if (in) a.view.group_of[b] = lead >= 0 ? at_s[lead] : make_int2(-1, 0);
-}
-
-// Rows i = t, t + threads .. of request b into the packed order.
-__device__ __forceinline__ void share_rows(const ShareArgs& a, int b, int t,
-                                           int threads) {
-  const int32_t* at = reinterpret_cast<const int32_t*>(a.view.group_of + b);
-  if (fresh(at) < 0) return;
-  const int R = a.g.N + 1;
-  const int n = share_lengths(a, b).y;
-  const int to = fresh(at + 1) + fresh(&a.view.req[b].w);
-  for (int i = t; i <= n; i += threads) a.view.rows[to + i] = b * R + i;
-}
-
-struct PackLds {
-  int lead[kPackThreads], rows[kPackThreads];
-  int2 at[kPackThreads], wave_sum[kPackThreads / kWave];
-};
-
-__global__ __launch_bounds__(256) void share_clear_kernel(ShareArgs a) {
-  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (p < a.g.n_pages) {
-    a.count[p] = 0;
-    a.lead[p] = 0x7fffffff;
+    a.view.group_of[b] = group;
+    s.to[b] = group.y + before;
+  }
+  if (!with_rows) return;
+  __syncthreads();
+  const int R = g.N + 1;
+  for (int x = b; x < g.batch * R; x += kPackThreads) {
+    const int q = x / R, i = x - q * R;
+    if (i < s.lead[q].y) a.view.rows[s.to[q] + i] = x;
   }
 }
 
-__global__ __launch_bounds__(kShareThreads) void share_count_kernel(
+template <int kMine>
+__global__ __launch_bounds__(kShareThreads) void share_columns_kernel(
     ShareArgs a) {
-  share_count(a, blockIdx.x, threadIdx.x, kShareThreads);
+  extern __shared__ unsigned long long dyn[];
+  unsigned long long* best_s = dyn;
+  int* full_s = reinterpret_cast<int*>(best_s + a.g.batch);
+  int* col = full_s + a.g.batch;
+  __shared__ int most;
+  if (threadIdx.x == 0) most = 0;
+  __syncthreads();
+  int here = 0;
+  for (int b = threadIdx.x; b < a.g.batch; b += kShareThreads) {
+    const int full = share_pages(a, b);
+    best_s[b] = 0;
+    full_s[b] = full;
+    here = max(here, full);
+  }
+  here = wave_max(here);
+  if ((threadIdx.x & 63) == 0) atomicMax(&most, here);
+  __syncthreads();
+  const int end = most;
+  for (int j0 = blockIdx.x << kWide; j0 < end; j0 += gridDim.x << kWide)
+    share_columns<kMine>(a, j0, kWide, full_s, col, best_s);
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.g.batch; b += kShareThreads)
+    a.best[(int64_t)blockIdx.x * a.g.batch + b] = best_s[b];
 }
 
-__global__ __launch_bounds__(kShareThreads) void share_pick_kernel(
-    ShareArgs a) {
-  __shared__ uint64_t best_s[kShareThreads / kWave];
+__global__ __launch_bounds__(kWave) void share_pick_kernel(ShareArgs a,
+                                                           int columns) {
   const int b = blockIdx.x;
-  const uint64_t best =
-      wave_max64(share_best(a, b, threadIdx.x, kShareThreads));
-  if ((threadIdx.x & 63) == 0) best_s[threadIdx.x >> 6] = best;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  uint64_t top = 0;
-  for (int w = 0; w < kShareThreads / kWave; ++w)
-    top = best_s[w] > top ? best_s[w] : top;
-  share_pick(a, b, top);
+  unsigned long long best = 0;
+  for (int w = threadIdx.x; w < columns; w += kWave)
+    best = max(best, (unsigned long long)a.best[(int64_t)w * a.g.batch + b]);
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) best = max(best, __shfl_xor(best, k, kWave));
+  if (threadIdx.x == 0) a.place[b] = share_place(a, best);
 }
 
 __global__ __launch_bounds__(kShareThreads) void share_join_kernel(
     ShareArgs a) {
-  const int b = blockIdx.x;
-  int lead = share_lead(a, b);
-  bool same = true;
-  if (lead >= 0)
-    same = share_agrees(a, b, lead, a.place[b], threadIdx.x, kShareThreads);
-  if (__syncthreads_or(same ? 0 : 1)) lead = -1;
-  if (threadIdx.x == 0) {
+  __shared__ int lead_s;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int d = a.place[b];
+  if (d < 0) {
+    if (tid == 0) a.joined[b] = -1;
+    return;
+  }
+  if (tid == 0) lead_s = b;
+  __syncthreads();
+  const int mine = share_lead(a, b, d, a.place, tid, kShareThreads);
+  if (mine < b) atomicMin(&lead_s, mine);
+  __syncthreads();
+  const int lead = lead_s;
+  const bool same = share_agrees(a, b, lead, d, tid, kShareThreads);
+  if (__syncthreads_or(same ? 0 : 1)) {
+    if (tid == 0) a.joined[b] = -1;
+  } else if (tid == 0) {
     a.joined[b] = lead;
-    if (lead >= 0) atomicAdd(&a.size[lead], 1);
   }
 }
 
 __global__ __launch_bounds__(kPackThreads) void share_pack_kernel(
     ShareArgs a, int with_rows) {
   __shared__ PackLds s;
-  share_pack(a, s.lead, s.rows, s.at, s.wave_sum);
-  if (!with_rows) return;
-  __syncthreads();
-  for (int b = threadIdx.x >> 6; b < a.g.batch; b += kPackThreads / kWave)
-    share_rows(a, b, threadIdx.x & 63, kWave);
+  share_pack(a, s, with_rows != 0);
 }
 
 __global__ __launch_bounds__(256) void share_rows_kernel(ShareArgs a) {
-  share_rows(a, blockIdx.x, blockIdx.y * 256 + threadIdx.x, 256 * gridDim.y);
+  const int b = blockIdx.x, i = blockIdx.y * 256 + threadIdx.x;
+  const int2 group = a.view.group_of[b];
+  const int4 rq = a.view.req[b];
+  if (group.x >= 0 && i <= rq.y)
+    a.view.rows[group.y + rq.w + i] = b * (a.g.N + 1) + i;
 }
 
-// Small batches and caches: one workgroup does all of it, a wave a request.
+// Small tables: one workgroup does all of it, then a wave a request.
+constexpr int kSmallBatch = 64;
+constexpr int kSmallTable = 16384;   // table entries, and
+constexpr int kPackRows = 16384;     // rows that one workgroup goes through
+
 __global__ __launch_bounds__(kPackThreads) void share_small_kernel(
     ShareArgs a) {
   __shared__ PackLds s;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kWaves = kPackThreads / kWave;
-  for (int p = threadIdx.x; p < a.g.n_pages; p += kPackThreads) {
-    a.count[p] = 0;
-    a.lead[p] = 0x7fffffff;
+  __shared__ unsigned long long best_s[kSmallBatch];
+  __shared__ int full_s[kSmallBatch], place_s[kSmallBatch];
+  __shared__ int col[kSmallTable];
+  const int tid = threadIdx.x, lane = tid & 63;
+  int most = 0;
+  if (tid < a.g.batch) {
+    best_s[tid] = 0;
+    full_s[tid] = most = share_pages(a, tid);
   }
   __syncthreads();
-  for (int b = wave; b < a.g.batch; b += kWaves)
-    share_count(a, b, lane, kWave);
+  for (int b = 0; b < a.g.batch; ++b) most = max(most, full_s[b]);
+  // all places at once, or as many as there is room and threads for
+  int wide = 0;
+  while (1 << wide < most && 2 << wide <= kPackThreads &&
+         a.g.batch << (wide + 1) <= kSmallTable)
+    ++wide;
+  for (int j0 = 0; j0 < most; j0 += 1 << wide)
+    share_columns<2>(a, j0, wide, full_s, col, best_s);
   __syncthreads();
-  for (int b = wave; b < a.g.batch; b += kWaves) {
-    const uint64_t best = wave_max64(share_best(a, b, lane, kWave));
-    if (lane == 0) share_pick(a, b, best);
-  }
+  if (tid < a.g.batch) a.place[tid] = place_s[tid] = share_place(a, best_s[tid]);
   __syncthreads();
-  for (int b = wave; b < a.g.batch; b += kWaves) {
-    int lead = share_lead(a, b);
-    bool same = true;
-    if (lead >= 0)
-      same = share_agrees(a, b, lead, fresh(a.place + b), lane, kWave);
-    if (__ballot(!same)) lead = -1;
-    if (lane == 0) {
-      a.joined[b] = lead;
-      if (lead >= 0) atomicAdd(&a.size[lead], 1);
+  for (int b = tid >> 6; b < a.g.batch; b += kPackThreads / kWave) {
+    const int d = place_s[b];
+    int lead = -1;
+    if (d >= 0) {
+      lead = share_lead(a, b, d, place_s, lane, kWave);
+      lead = -wave_max(-lead);
+      if (__ballot(!share_agrees(a, b, lead, d, lane, kWave))) lead = -1;
     }
+    if (lane == 0) a.joined[b] = lead;
   }
   __syncthreads();
-  share_pack(a, s.lead, s.rows, s.at, s.wave_sum);
-  __syncthreads();
-  for (int b = wave; b < a.g.batch; b += kWaves) share_rows(a, b, lane, kWave);
+  share_pack(a, s, true);
 }
 
-constexpr int kSmallTable = 32768;   // table entries,
-constexpr int kSmallPages = 16384;   // pages and
-constexpr int kPackRows = 16384;     // rows that one workgroup goes through
-
 }  // namespace
+
+int share_blocks(const pct_cache_shape& sh) {
+  const int64_t x = ((int64_t)sh.max_pages + (1 << kWide) - 1) >> kWide;
+  return (int)(x < kShareBlocks ? x : kShareBlocks);
+}
 
 hipError_t launch_share(const ShareArgs& a, hipStream_t s) {
   const PageGeom& g = a.g;
   const int64_t rows = (int64_t)g.batch * (g.N + 1);
-  if ((int64_t)g.batch * g.max_pages <= kSmallTable &&
-      g.n_pages <= kSmallPages && rows <= kPackRows) {
+  if (g.batch <= kSmallBatch && (int64_t)g.batch * g.max_pages <= kSmallTable &&
+      rows <= kPackRows) {
     hipLaunchKernelGGL(share_small_kernel, dim3(1), dim3(kPackThreads), 0, s,
                        a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(share_clear_kernel,
-                     dim3((unsigned)(((int64_t)g.n_pages + 255) / 256)),
-                     dim3(256), 0, s, a);
+  const size_t lds = (size_t)g.batch * (12 + (4 << kWide));
+  // (few requests: two entries of a thread)
+  const bool few = g.batch <= 2 * (kShareThreads >> kWide);
+  const auto kernel = few ? share_columns_kernel<2> : share_columns_kernel<8>;
+  hipLaunchKernelGGL(kernel, dim3(a.blocks), dim3(kShareThreads), lds, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 each(g.batch), block(kShareThreads);
-  hipLaunchKernelGGL(share_count_kernel, each, block, 0, s, a);
+  hipLaunchKernelGGL(share_pick_kernel, dim3(g.batch), dim3(kWave), 0, s, a,
+                     a.blocks);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(share_pick_kernel, each, block, 0, s, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(share_join_kernel, each, block, 0, s, a);
+  hipLaunchKernelGGL(share_join_kernel, dim3(g.batch), dim3(kShareThreads), 0,
+                     s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(share_pack_kernel, dim3(1), dim3(kPackThreads), 0, s, a,

@@ -118,11 +118,14 @@ struct ShareView {
 struct ShareArgs {
   PageGeom g;
   int least;                      // positions that a group must save
-  int32_t *count, *lead;          // [n_pages]
-  int32_t *place, *size, *joined; // [batch]
+  uint64_t* best;            // [blocks][batch] picks of groups of places
+  int blocks;
+  int32_t *place, *joined;   // [batch]
   int32_t *leader, *shared;       // [batch]
   ShareView view;
 };
+constexpr int kShareBlocks = 512;
+int share_blocks(const pct_cache_shape& sh);
 hipError_t launch_share(const ShareArgs& a, hipStream_t s);
 
 struct AttendArgs {

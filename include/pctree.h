@@ -671,9 +671,9 @@ pct_status pct_cache_compact(const pct_cache_shape* shape /*host*/,
 /* ------------------------------------------------------------------------
  * pct_cache_share -- which requests of a round share a prefix, found from
  * their tables.  With full_b the whole pages of request b's context (none if
- * n_nodes = -1; its root's page is never among them) and c(p) the number of
- * table entries j < full_b, over all b, that are page p, each request picks
- * its entry j of largest gain (j + 1) (c(block_table[b][j]) - 1), the first
+ * n_nodes = -1; its root's page is never among them) and c_j(p) the number of
+ * requests with j < full_b whose entry j is page p, each request picks
+ * its entry j of largest gain (j + 1) (c_j(block_table[b][j]) - 1), the first
  * such (gains from 2^33 on count as alike), or none if gain * page_size <
  * least.  Requests that picked the same page at the same j, and whose
  * tables agree in the entries 0..j with those of the lowest of them, are a

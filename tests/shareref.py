@@ -16,16 +16,16 @@ def share(ctx, n, table, n_pages, page, least):
             for b in range(batch)]
     count = {}
     for b in range(batch):
-        for p in table[b, :full[b]]:
+        for j, p in enumerate(table[b, :full[b]].tolist()):
             if 0 <= p < n_pages:
-                count[int(p)] = count.get(int(p), 0) + 1
+                count[j, p] = count.get((j, p), 0) + 1
     pick = {}
     for b in range(batch):
         best, at = 0, -1
         for j in range(full[b]):
             p = int(table[b, j])
             if 0 <= p < n_pages:
-                gain = (j + 1) * (count[p] - 1)
+                gain = (j + 1) * (count[j, p] - 1)
                 if gain > best:
                     best, at = gain, j
         if at >= 0 and best * page >= least:
@@ -33,12 +33,12 @@ def share(ctx, n, table, n_pages, page, least):
     leader, shared = np.arange(batch), np.zeros(batch, np.int64)
     groups = {}
     for b in sorted(pick):
-        groups.setdefault(int(table[b, pick[b]]), []).append(b)
+        groups.setdefault((pick[b], int(table[b, pick[b]])), []).append(b)
     for members in groups.values():
         lead = members[0]
         d = pick[lead]
-        on = [b for b in members if pick[b] == d and
-              np.array_equal(table[b, :d + 1], table[lead, :d + 1])]
+        on = [b for b in members
+              if np.array_equal(table[b, :d + 1], table[lead, :d + 1])]
         if len(on) > 1:
             leader[on] = lead
             shared[on] = (d + 1) * page
