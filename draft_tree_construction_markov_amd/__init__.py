@@ -1028,18 +1028,33 @@ def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
     return out
 
 
-@dataclass
+@dataclass(frozen=True)
 class PageState:
     """The state of a cache's pages, int32: ctx_len [batch], block_table
     [batch][max_pages], n_held [batch], ring [n_pages] and ring_state [2] as
-    CachePlan has them, extra [n_pages]: holders of a page beyond the
-    first."""
+    CachePlan has them, extra [n_pages]: holders of a page beyond the first.
+    The tensors are checked once, here; calls change what they hold."""
     ctx_len: torch.Tensor
     block_table: torch.Tensor
     n_held: torch.Tensor
     ring: torch.Tensor
     ring_state: torch.Tensor
     extra: torch.Tensor
+
+    def __post_init__(self):
+        batch, width = self.block_table.shape
+        n_pages, dev = self.ring.numel(), self.ring.get_device()
+        if dev < 0:
+            raise ValueError("libpctree needs device tensors")
+        shapes = ((batch,), (batch, width), (batch,), (n_pages,), (2,),
+                  (n_pages,))
+        names = ("ctx_len", "block_table", "n_held", "ring", "ring_state",
+                 "extra")
+        state = _PageState(*(
+            _want(name, getattr(self, name), torch.int32, shape, dev)
+            for name, shape in zip(names, shapes)))
+        object.__setattr__(self, "_ref", C.byref(state))
+        object.__setattr__(self, "_key", (batch, width, n_pages, dev))
 
 
 class CachePages:
@@ -1065,15 +1080,14 @@ class CachePages:
             L.pct_cache_fork_workspace(self._ref, batch)), dev)
         self._layer = n_pages * Hkv * page_size * D
         self._cache = (layers, n_pages, Hkv, page_size, D)
-        self._shapes = dict(ctx_len=(batch,), block_table=(batch, max_pages),
-                            n_held=(batch,), ring=(n_pages,), ring_state=(2,),
-                            extra=(n_pages,))
+        self._key = (batch, max_pages, n_pages, dev.index)
+        self._tail = (C.c_void_p(self.ws.data_ptr()), self.ws.numel())
 
     def _state(self, state: PageState):
-        dev, i32 = self.device.index, torch.int32
-        return C.byref(_PageState(*(
-            _want(name, getattr(state, name), i32, shape, dev)
-            for name, shape in self._shapes.items())))
+        if state._key != self._key:
+            raise ValueError("the state's (batch, max_pages, n_pages, device) "
+                             f"are {state._key}, not {self._key}")
+        return state._ref
 
     def _caches(self, k_cache, v_cache):
         dev, cache = self.device.index, self._cache
@@ -1088,7 +1102,7 @@ class CachePages:
         dev = self.device.index
         _enqueue(lib().pct_cache_free, dev, self._ref, places.numel(),
                  _want("places", places, torch.int32, (places.numel(),), dev),
-                 self._state(state), self.ws.data_ptr(), self.ws.numel())
+                 self._state(state), *self._tail)
 
     def trim(self, state: PageState, n_nodes=None):
         """Every request keeps the pages of its ctx_len + n_nodes + 1
@@ -1098,8 +1112,8 @@ class CachePages:
         _enqueue(lib().pct_cache_trim, dev, self._ref,
                  None if n_nodes is None else
                  _want("n_nodes", n_nodes, torch.int32,
-                       self._shapes["n_held"], dev),
-                 self._state(state), self.ws.data_ptr(), self.ws.numel())
+                       (self.shape.batch,), dev),
+                 self._state(state), *self._tail)
 
     def fork(self, state: PageState, src, dst, k_cache, v_cache, length=None,
              out=None):
@@ -1110,8 +1124,8 @@ class CachePages:
         where a pair is left out, since dst holds pages, src lacks some, or
         the ring has none left."""
         dev, i32, m = self.device.index, torch.int32, src.numel()
-        if m > self.shape.batch:
-            raise PCTError(1, f"{m} pairs for {self.shape.batch} places")
+        if m > self._key[0]:
+            raise PCTError(1, f"{m} pairs for {self._key[0]} places")
         if out is None:
             out = torch.empty(m, dtype=i32, device=src.device)
         kp, vp = self._caches(k_cache, v_cache)
@@ -1121,7 +1135,7 @@ class CachePages:
                  None if length is None else
                  _want("length", length, i32, (m,), dev),
                  self._state(state), kp, vp, _want("out", out, i32, (m,), dev),
-                 self.ws.data_ptr(), self.ws.numel())
+                 *self._tail)
         return out
 
     def compact(self, state: PageState, k_cache, v_cache, out=None):
@@ -1134,8 +1148,8 @@ class CachePages:
         dev = self.device.index
         _enqueue(lib().pct_cache_compact, dev, self._ref, self.layers,
                  self._layer, self._state(state),
-                 _want("out", table, torch.int32, self._shapes["block_table"],
-                       dev), kp, vp, self.ws.data_ptr(), self.ws.numel())
+                 _want("out", table, torch.int32, self._key[:2], dev), kp, vp,
+                 *self._tail)
         return table
 
 

@@ -16,8 +16,7 @@ namespace {
 
 constexpr int kThreads = 1024;        // of the kernels of one workgroup
 constexpr int kSeg = 16 * kThreads;   // pages of a workgroup of a scan
-constexpr int kSmallPages = 2 * kSeg; // pages, and
-constexpr int kSmallPlaces = 64;      // places, that one workgroup goes through
+constexpr int kSmallPlaces = 64;      // places that one workgroup goes through
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -64,6 +63,61 @@ __device__ __forceinline__ int block_prefix(int x, int* wave_sum, int& total) {
   return before + incl - x;
 }
 
+// Pages of a segment as bits: wave w has the pages from w * 1024 on, bit `lane`
+// of word e is page 64 e + lane of them.  USED: pages that are held (extra not
+// below zero), else those that are not.
+struct Bits {
+  uint64_t word[16];
+  int count;  // of the wave
+};
+__device__ __forceinline__ int wave_page(int seg) {
+  return seg * kSeg +
+         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (16 * kWave);
+}
+template <bool USED, typename Read>
+__device__ __forceinline__ Bits segment_bits(const PagesArgs& a, int seg,
+                                             Read read) {
+  const int lane = threadIdx.x & 63, P = a.g.n_pages, p0 = wave_page(seg);
+  Bits x;
+  x.count = 0;
+  int v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    v[e] = read(min(p0 + e * kWave + lane, P - 1));
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int p = p0 + e * kWave + lane;
+    x.word[e] = __ballot(p < P && (USED ? v[e] >= 0 : v[e] < 0));
+    x.count += __popcll(x.word[e]);
+  }
+  return x;
+}
+template <bool USED>
+__device__ __forceinline__ Bits segment_bits(const PagesArgs& a, int seg) {
+  return segment_bits<USED>(a, seg, [&](int p) { return fresh(a.extra + p); });
+}
+// set bits of a word below this lane's
+__device__ __forceinline__ int bits_before(uint64_t word) {
+  return __builtin_amdgcn_mbcnt_hi(
+      (uint32_t)(word >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)word, 0));
+}
+
+// Sum of the waves' x before this one, and of all.
+__device__ __forceinline__ int waves_prefix(int x, int* wave_sum, int& total) {
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) wave_sum[wave] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+  for (int w = 0; w < kThreads / kWave; ++w) {
+    const int y = wave_sum[w];
+    before += w < wave ? y : 0;
+    total += y;
+  }
+  return before;
+}
+
 // The pages [keep, held) of request b let go, by `threads` threads.
 __device__ __forceinline__ void let_go(const PagesArgs& a, int b, int keep,
                                        int held, int t, int threads) {
@@ -103,19 +157,20 @@ __device__ __forceinline__ int place_of(const PagesArgs& a, int i, int& keep,
 __device__ __forceinline__ int append_segment(const PagesArgs& a, int seg,
                                               int2 ring, int before,
                                               int* wave_sum) {
-  const int P = a.g.n_pages;
-  const int p0 = seg * kSeg + threadIdx.x * 16;
-  uint32_t gone = 0;
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (p0 + e < P && fresh(a.extra + p0 + e) < 0) gone |= 1u << e;
+  const Bits gone = segment_bits<false>(a, seg);
+  const int lane = threadIdx.x & 63, p0 = wave_page(seg);
   int total;
-  int at = before + block_prefix(__popc(gone), wave_sum, total);
-  while (gone) {
-    const int e = __builtin_ctz(gone);
-    gone &= gone - 1;
-    a.ring[wrap((int64_t)ring.x + ring.y + at++, P)] = p0 + e;
-    a.extra[p0 + e] = 0;
+  int at = before + waves_prefix(gone.count, wave_sum, total);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    if (gone.word[e] == 0) continue;
+    if ((gone.word[e] >> lane) & 1) {
+      const int p = p0 + e * kWave + lane;
+      a.ring[wrap((int64_t)ring.x + ring.y + at + bits_before(gone.word[e]),
+                  a.g.n_pages)] = p;
+      a.extra[p] = 0;
+    }
+    at += __popcll(gone.word[e]);
   }
   return total;
 }
@@ -134,10 +189,7 @@ __global__ __launch_bounds__(kThreads) void release_small_kernel(PagesArgs a) {
   }
   const int2 ring = ring_now(a);
   __syncthreads();
-  int more = 0;
-  for (int seg = 0; seg * kSeg < a.g.n_pages; ++seg)
-    more += append_segment(a, seg, ring, more, wave_sum);
-  __syncthreads();
+  const int more = append_segment(a, 0, ring, 0, wave_sum);
   if (threadIdx.x == 0) {
     a.ring_state[0] = ring.x;
     a.ring_state[1] = min(ring.y + more, a.g.n_pages);
@@ -156,12 +208,8 @@ __global__ __launch_bounds__(256) void release_kernel(PagesArgs a) {
 __global__ __launch_bounds__(kThreads) void released_count_kernel(PagesArgs a,
                                                                   int segs) {
   __shared__ int wave_sum[kThreads / kWave];
-  const int p0 = blockIdx.x * kSeg + threadIdx.x * 16;
-  int n = 0, total;
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (p0 + e < a.g.n_pages && a.extra[p0 + e] < 0) ++n;
-  block_prefix(n, wave_sum, total);
+  int total;
+  waves_prefix(segment_bits<false>(a, blockIdx.x).count, wave_sum, total);
   if (threadIdx.x != 0) return;
   a.count[blockIdx.x] = total;
   if (blockIdx.x == 0) {
@@ -184,7 +232,9 @@ __global__ __launch_bounds__(kThreads) void released_append_kernel(
     PagesArgs a, int segs) {
   __shared__ int wave_sum[kThreads / kWave];
   const int seg = blockIdx.x;
-  const int2 ring = make_int2(a.count[segs], a.count[segs + 1]);
+  // (one segment: nothing was counted, nobody else reads the state)
+  const int2 ring = segs == 1 ? ring_now(a)
+                              : make_int2(a.count[segs], a.count[segs + 1]);
   const int before = sum_counts(a.count, 0, seg, wave_sum);
   const int mine = append_segment(a, seg, ring, before, wave_sum);
   if (seg == segs - 1 && threadIdx.x == 0) {
@@ -315,43 +365,39 @@ __global__ __launch_bounds__(256) void fork_apply_kernel(ForkArgs f,
 // use.  The used pages from T on, in ascending order, move to the unused ones
 // below T, in ascending order: as many of the one as of the other, and no
 // page is both read and written.
-__device__ __forceinline__ void count_pages(const PagesArgs& a, int b, int t,
-                                            int threads) {
+// extra: a.extra, or a copy in LDS
+__device__ __forceinline__ void count_pages(const PagesArgs& a, int32_t* extra,
+                                            int b, int t, int threads) {
   const int held = clamp_held(a.held[b], a.g.max_pages);
   const int32_t* table = a.table + (int64_t)b * a.g.max_pages;
   for (int j = t; j < held; j += threads) {
     const int p = table[j];
-    if ((unsigned)p < (unsigned)a.g.n_pages) atomicAdd(&a.extra[p], 1);
+    if ((unsigned)p < (unsigned)a.g.n_pages) atomicAdd(&extra[p], 1);
   }
-}
-
-__device__ __forceinline__ uint32_t used_bits(const PagesArgs& a, int p0) {
-  uint32_t used = 0;
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (p0 + e < a.g.n_pages && fresh(a.extra + p0 + e) >= 0) used |= 1u << e;
-  return used;
 }
 
 // Lists the moves of a segment: `before` used pages precede it, `total` are
 // in use, of which `low` below page `total`.
-__device__ __forceinline__ void list_moves(const CompactArgs& c, int seg,
+__device__ __forceinline__ void list_moves(const CompactArgs& c,
+                                           const Bits& used, int seg,
                                            int before, int total, int low,
                                            int* wave_sum) {
   const PagesArgs& a = c.a;
-  const int p0 = seg * kSeg + threadIdx.x * 16;
-  const uint32_t used = used_bits(a, p0);
+  const int lane = threadIdx.x & 63, p0 = wave_page(seg);
   int sum;
-  int u = before + block_prefix(__popc(used), wave_sum, sum);
-  for (int e = 0; e < 16 && p0 + e < a.g.n_pages; ++e) {
-    const int p = p0 + e;
-    const bool on = (used >> e) & 1;
+  int at = before + waves_prefix(used.count, wave_sum, sum);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int p = p0 + e * kWave + lane;
+    const int u = at + bits_before(used.word[e]);
+    at += __popcll(used.word[e]);
+    if (p >= a.g.n_pages) continue;
+    const bool on = (used.word[e] >> lane) & 1;
     if (!on && p < total) c.hole[p - u] = p;
     if (on && p >= total) {
       c.high[u - low] = p;
       c.rank[p] = u - low;
     }
-    u += on ? 1 : 0;
     // the ring: the pages behind those in use
     a.ring[p] = wrap((int64_t)total + p, a.g.n_pages);
   }
@@ -364,36 +410,38 @@ __device__ __forceinline__ void list_moves(const CompactArgs& c, int seg,
 }
 
 // used pages of a segment below page `end`
-__device__ __forceinline__ int used_below(const PagesArgs& a, int seg, int end,
+__device__ __forceinline__ int used_below(const Bits& used, int seg, int end,
                                           int* wave_sum) {
-  const int p0 = seg * kSeg + threadIdx.x * 16;
-  uint32_t used = used_bits(a, p0);
-  const int n = end - p0;
-  used = n <= 0 ? 0 : n >= 16 ? used : used & ((1u << n) - 1);
-  int sum;
-  block_prefix(__popc(used), wave_sum, sum);
+  const int p0 = wave_page(seg);
+  int n = 0, sum;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int left = end - p0 - e * kWave;
+    const uint64_t mask =
+        left <= 0 ? 0 : left >= 64 ? ~0ull : (1ull << left) - 1;
+    n += __popcll(used.word[e] & mask);
+  }
+  waves_prefix(n, wave_sum, sum);
   return sum;
 }
 
 __global__ __launch_bounds__(kThreads) void compact_small_kernel(
     CompactArgs c) {
   __shared__ int wave_sum[kThreads / kWave];
+  __shared__ int32_t extra[kSeg];
   const PagesArgs& a = c.a;
   const int P = a.g.n_pages;
-  for (int p = threadIdx.x; p < P; p += kThreads) a.extra[p] = -1;
+  for (int p = threadIdx.x; p < P; p += kThreads) extra[p] = -1;
   __syncthreads();
   for (int b = threadIdx.x >> 6; b < a.g.batch; b += kThreads / kWave)
-    count_pages(a, b, threadIdx.x & 63, kWave);
+    count_pages(a, extra, b, threadIdx.x & 63, kWave);
   __syncthreads();
-  int total = 0, low = 0;
-  for (int seg = 0; seg * kSeg < P; ++seg)
-    total += used_below(a, seg, P, wave_sum);
-  for (int seg = 0; seg * kSeg < total; ++seg)
-    low += used_below(a, seg, total, wave_sum);
-  for (int seg = 0, before = 0; seg * kSeg < P; ++seg) {
-    list_moves(c, seg, before, total, low, wave_sum);
-    before += used_below(a, seg, P, wave_sum);
-  }
+  const Bits used =
+      segment_bits<true>(a, 0, [&](int p) { return extra[p]; });
+  const int total = used_below(used, 0, P, wave_sum);
+  const int low = used_below(used, 0, total, wave_sum);
+  list_moves(c, used, 0, 0, total, low, wave_sum);
+  for (int p = threadIdx.x; p < P; p += kThreads) a.extra[p] = extra[p];
 }
 
 __global__ __launch_bounds__(256) void compact_clear_kernel(PagesArgs a) {
@@ -402,13 +450,14 @@ __global__ __launch_bounds__(256) void compact_clear_kernel(PagesArgs a) {
 }
 
 __global__ __launch_bounds__(256) void compact_holders_kernel(PagesArgs a) {
-  count_pages(a, blockIdx.x, threadIdx.x, 256);
+  count_pages(a, a.extra, blockIdx.x, threadIdx.x, 256);
 }
 
 __global__ __launch_bounds__(kThreads) void compact_count_kernel(
     CompactArgs c) {
   __shared__ int wave_sum[kThreads / kWave];
-  const int n = used_below(c.a, blockIdx.x, c.a.g.n_pages, wave_sum);
+  const int n = used_below(segment_bits<true>(c.a, blockIdx.x), blockIdx.x,
+                           c.a.g.n_pages, wave_sum);
   if (threadIdx.x == 0) c.a.count[blockIdx.x] = n;
 }
 
@@ -418,9 +467,11 @@ __global__ __launch_bounds__(kThreads) void compact_list_kernel(CompactArgs c) {
   const int total = sum_counts(c.a.count, 0, segs, wave_sum);
   const int edge = min(total / kSeg, segs - 1);  // its segment of page `total`
   const int low = sum_counts(c.a.count, 0, edge, wave_sum) +
-                  used_below(c.a, edge, total, wave_sum);
+                  used_below(segment_bits<true>(c.a, edge), edge, total,
+                             wave_sum);
   const int before = sum_counts(c.a.count, 0, seg, wave_sum);
-  list_moves(c, seg, before, total, low, wave_sum);
+  list_moves(c, segment_bits<true>(c.a, seg), seg, before, total, low,
+             wave_sum);
 }
 
 // Tables, holders and the pages themselves.  The first workgroups rewrite a
@@ -485,7 +536,7 @@ size_t release_workspace(const pct_cache_shape& sh) {
 }
 
 hipError_t launch_release(const PagesArgs& a, hipStream_t s) {
-  if (a.m <= kSmallPlaces && a.g.n_pages <= kSmallPages) {
+  if (a.m <= kSmallPlaces && a.g.n_pages <= kSeg) {
     hipLaunchKernelGGL(release_small_kernel, dim3(1), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
@@ -493,10 +544,12 @@ hipError_t launch_release(const PagesArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(release_kernel, dim3(a.m), dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(released_count_kernel, dim3(segs), dim3(kThreads), 0, s, a,
-                     segs);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (segs > 1) {
+    hipLaunchKernelGGL(released_count_kernel, dim3(segs), dim3(kThreads), 0, s,
+                       a, segs);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(released_append_kernel, dim3(segs), dim3(kThreads), 0, s,
                      a, segs);
   return hipGetLastError();
@@ -524,7 +577,7 @@ hipError_t launch_compact(const CompactArgs& c, hipStream_t s) {
   const PagesArgs& a = c.a;
   const PageGeom& g = a.g;
   hipError_t e;
-  if (g.batch <= kSmallPlaces && g.n_pages <= kSmallPages) {
+  if (g.batch <= kSmallPlaces && g.n_pages <= kSeg) {
     hipLaunchKernelGGL(compact_small_kernel, dim3(1), dim3(kThreads), 0, s, c);
     e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -1,5 +1,7 @@
 """GPU checks of free, trim, fork and compact against plain definitions, equal
 in every value."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -71,7 +73,7 @@ class Both:
         got = self.h.compact(self.d, self.k, self.v, out=to)
         if out:
             assert got is to and torch.equal(was, self.d.block_table)
-            self.d.block_table = to
+            self.d = dataclasses.replace(self.d, block_table=to)
         self.s.compact()
         self.same()
 
@@ -267,8 +269,14 @@ def test_binding_refuses():
         t.h.compact(t.d, t.k, t.v, out=t.d.block_table[:2])
     with pytest.raises(pct.PCTError):      # more pairs than places
         t.h.fork(t.d, dev_i32([0] * 9), dev_i32([1] * 9), t.k, t.v)
-    bad = pct.PageState(**{**t.d.__dict__, "extra": t.d.ring})
+    bad = dataclasses.replace(t.d, extra=t.d.ring)
     with pytest.raises(pct.PCTError):
         t.h.trim(bad)
+    for kw in (dict(extra=t.d.extra.long()), dict(ring=t.d.ring[:5]),
+               dict(n_held=t.d.n_held.cpu()), dict(ctx_len=t.d.ctx_len[:3])):
+        with pytest.raises(ValueError):
+            dataclasses.replace(t.d, **kw)
+    with pytest.raises(ValueError):
+        pct.CachePages(4, 10, 4, 2, 1, 16).trim(t.d)
     with pytest.raises(pct.PCTError):
         pct.CachePages(0, 10, 4, 3, 1, 16)
