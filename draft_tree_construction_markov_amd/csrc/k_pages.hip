@@ -248,23 +248,37 @@ __global__ __launch_bounds__(kThreads) void released_append_kernel(
 // gives out the pages for the parts of pages, in the order of the pairs;
 // then a workgroup per pair writes its table row and counts, and others copy
 // the rows of its last page.
+constexpr int kClaims = 4096;  // places whose claims are kept in LDS
+
 __global__ __launch_bounds__(kThreads) void fork_plan_kernel(ForkArgs f) {
   __shared__ int wave_sum[kThreads / kWave];
-  __shared__ int s_taken;
+  __shared__ int s_taken, claim_s[kClaims];
   const PagesArgs& a = f.a;
   const PageGeom& g = a.g;
   const int tid = threadIdx.x, P = g.n_pages;
+  const bool in_lds = g.batch <= kClaims;
+  const auto place = [&](int b) { return b >= 0 && b < g.batch; };
   const int2 ring = ring_now(a);
   if (tid == 0) s_taken = 0;
   // the first pair that names a place has it
   for (int i = tid; i < a.m; i += kThreads) {
     const int d = f.dst[i];
-    if (d >= 0 && d < g.batch) f.claim[d] = a.m;
+    if (place(d)) {
+      if (in_lds)
+        claim_s[d] = a.m;
+      else
+        f.claim[d] = a.m;
+    }
   }
   __syncthreads();
   for (int i = tid; i < a.m; i += kThreads) {
     const int d = f.dst[i];
-    if (d >= 0 && d < g.batch) atomicMin(&f.claim[d], i);
+    if (place(d)) {
+      if (in_lds)
+        atomicMin(&claim_s[d], i);
+      else
+        atomicMin(&f.claim[d], i);
+    }
   }
   __syncthreads();
   int base = 0;
@@ -275,15 +289,15 @@ __global__ __launch_bounds__(kThreads) void fork_plan_kernel(ForkArgs f) {
     if (i < a.m) {
       s = f.src[i];
       d = f.dst[i];
-      ok = s >= 0 && s < g.batch && d >= 0 && d < g.batch && s != d;
+      ok = place(s) && place(d) && s != d;
     }
     if (ok) {
       len = clamp_ctx(a.ctx[s]);
       if (f.length) len = min(len, max(f.length[i], 0));
       rest = len & ((1 << g.shift) - 1);
       need = (len >> g.shift) + (rest > 0 ? 1 : 0);
-      ok = fresh(f.claim + d) == i && a.held[d] <= 0 &&
-           need <= clamp_held(a.held[s], g.max_pages);
+      ok = (in_lds ? claim_s[d] : fresh(f.claim + d)) == i &&
+           a.held[d] <= 0 && need <= clamp_held(a.held[s], g.max_pages);
       if (ok && rest > 0)
         ok = (unsigned)a.table[(int64_t)s * g.max_pages + need - 1] <
              (unsigned)P;

@@ -88,6 +88,7 @@ SHAPES = [
     (5, 12, 1024, 3, 1, 128, 2, 2500),
     (10, 33000, 2, 900, 1, 16, 1, 1700),   # more pages than one workgroup's
     (1100, 3500, 4, 6, 1, 16, 1, 20),      # more pairs than a workgroup
+    (4500, 9000, 4, 4, 1, 16, 1, 12),      # more places than LDS holds
 ]
 
 
