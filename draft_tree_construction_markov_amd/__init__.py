@@ -896,10 +896,14 @@ class SharePlan:
     """Plan of the prefixes that requests of a round share, found from their
     block tables; fixed shape, with its workspace and outputs allocated once;
     run() only enqueues kernels.  least: positions that a group must save to
-    be one."""
+    be one.  (Attention with and without groups, 32 heads of 128 over 400 ..
+    600 own positions: 8 tokens that save 1792 positions 16.0 and 16.2 us, 7168
+    17.5 and 19.9; 64 tokens, 4032 32.9 and 33.0, 16 k 34.7 and 38.0; 16 x 16
+    rows, 3840 26.0 and 25.3, 61 k 54 and 56; 4 x 65 rows, 3072 40 and 31,
+    12 k 56 and 52.)"""
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
-                 max_pages: int, least: int = 128, device="cuda"):
+                 max_pages: int, least: int = 4096, device="cuda"):
         self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, 1, 1,
                                 16, PCT_BF16)
         self.device = dev = _device(device)
@@ -1167,11 +1171,19 @@ class PagedCache:
     not attended, and commit leaves its length and its cache as they are
     whatever tau and accept_node say.  It keeps its root for a later round.
     n_nodes is what the last plan was given, n_served what was served of it.
+
+    share: requests may hold the same pages (extra counts their holders).
+    fork() makes a place a copy of another's context, free() empties places,
+    compact() moves the pages in use to the front, all between a commit and
+    the next plan (until then nothing is written, attended or kept), and
+    attend reads what requests share once for all of them, if that saves at
+    least `least` positions.  batch is at most 1024 then.
     """
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
                  max_pages: int, Hq: int, Hkv: int, D: int, layers: int = 1,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, share: bool = False, least: int = 4096,
+                 device="cuda"):
         dev = _device(device)
         i32 = dict(dtype=torch.int32, device=dev)
         self.k = torch.zeros(layers, n_pages, Hkv, page_size, D, dtype=dtype,
@@ -1186,14 +1198,66 @@ class PagedCache:
                                device=dev)
         self.n_nodes = None
         self.n_served = self._plan.out.n_served
-        self._attend = TreeAttention(batch, N, Hq, Hkv, D, n_pages, page_size,
-                                     max_pages, dtype=dtype, device=dev)
+        sizes = (batch, N, Hq, Hkv, D, n_pages, page_size, max_pages)
+        self.share = None
+        if share:
+            self.extra = torch.zeros(n_pages, **i32)
+            self._pages = CachePages(batch, n_pages, page_size, max_pages,
+                                     Hkv, D, layers=layers, dtype=dtype, N=N,
+                                     device=dev)
+            self._share = SharePlan(batch, N, n_pages, page_size, max_pages,
+                                    least=least, device=dev)
+            self.share = self._share.out
+            self._no_share = self.share.plan.clone()
+            self._attend = SharedAttention(*sizes, dtype=dtype, device=dev)
+        else:
+            self._attend = TreeAttention(*sizes, dtype=dtype, device=dev)
+
+    def _state(self) -> PageState:
+        if self.share is None:
+            raise ValueError("the cache was made without share=True")
+        return PageState(self.ctx_len, self.block_table, self.n_held,
+                         self.ring, self.ring_state, self.extra)
+
+    def _void(self):
+        """Until the next plan there are no rows."""
+        self._plan.out.slot.fill_(-1)
+        self.n_served.fill_(-1)
+        self.share.plan.copy_(self._no_share)
+
+    def fork(self, src, dst, length=None):
+        """Place dst[i] becomes a copy of the first length[i] (default: all)
+        positions of src[i]'s context (CachePages.fork); returns done [m]."""
+        state = self._state()
+        done = self._pages.fork(state, src, dst, self.k, self.v,
+                                length=length)
+        self._void()
+        return done
+
+    def free(self, places):
+        """Empty places [m] int32; entries outside the batch are left out."""
+        state = self._state()
+        self._pages.free(state, places)
+        self._void()
+
+    def compact(self):
+        """Move the pages in use to the first ones of the cache; there are
+        n_pages - ring_state[1] of them."""
+        state = self._state()
+        self._pages.compact(state, self.k, self.v)
+        self._void()
 
     def plan(self, n_nodes=None, depth=None) -> CacheRows:
         self.n_nodes = n_nodes
-        return self._plan.run(self.ctx_len, n_nodes, self.block_table,
+        if self.share is not None:
+            # (pages that others hold must not go back to the ring)
+            self._pages.trim(self._state(), n_nodes)
+        rows = self._plan.run(self.ctx_len, n_nodes, self.block_table,
                               self.n_held, self.ring, self.ring_state,
                               depth=depth)
+        if self.share is not None:
+            self._share.run(self.ctx_len, self.n_served, self.block_table)
+        return rows
 
     def write(self, layer: int, k, v):
         cache_write(k, v, self._plan.out.slot, self.k[layer], self.v[layer])
@@ -1214,9 +1278,11 @@ class PagedCache:
         """The layer's attention, in `out` when given, else in a tensor that
         every call without `out` writes, whatever its layer.  Unused rows,
         and those of requests that wait, are left as they were there."""
+        of = ((self.ctx_len, self.n_served) if self.share is None
+              else (self.share,))
         return self._attend.run(q, self.k[layer], self.v[layer],
-                                self.block_table, self.ctx_len, self.n_served,
-                                mask=mask, scale=scale, out=out)[0]
+                                self.block_table, *of, mask=mask, scale=scale,
+                                out=out)[0]
 
     def commit(self, tau, accept_node):
         return cache_commit(tau, accept_node, self.ctx_len, self.n_served,
