@@ -13,6 +13,9 @@ struct Span {
 };
 
 pct_status check_state(const pct_cache_shape* sh, const pct_page_state* st) {
+  // (pages are counted in 32 bits, past the last one of a scan)
+  if (sh->n_pages > 1 << 30)
+    return fail(PCT_ERR_UNSUPPORTED, "n_pages = %d exceeds 2^30", sh->n_pages);
   if (!st) return fail(PCT_ERR_INVALID_ARG, "state is NULL");
   const Span all[] = {{st->ctx_len, sh->batch},
                       {st->block_table, (int64_t)sh->batch * sh->max_pages},

@@ -352,25 +352,28 @@ __global__ __launch_bounds__(256) void fork_apply_kernel(ForkArgs f,
     if (rest > 0 && tid == 0) to[full] = rq.w;
   }
   if (rest == 0 || (unsigned)rq.w >= (unsigned)g.n_pages) return;
-  const int run = blockIdx.y * 4 + (tid >> 6);
-  if (run >= runs) return;
   const int hc = g.D / 8;
-  const int h = run % g.Hkv, lk = run / g.Hkv;
-  uint4* cache = ((lk & 1) ? a.vc : a.kc) + (int64_t)(lk >> 1) * a.layer_stride;
   const int64_t page_chunks = ((int64_t)g.Hkv << g.shift) * hc;
-  const int64_t head = ((int64_t)h << g.shift) * hc;
-  const u32x4* src =
-      reinterpret_cast<const u32x4*>(cache + from[full] * page_chunks + head);
-  u32x4* dst = reinterpret_cast<u32x4*>(cache + rq.w * page_chunks + head);
   const int n = rest * hc, step = 64 * gridDim.z;
-  for (int i = blockIdx.z * 64 + (tid & 63); i < n; i += 4 * step) {
-    u32x4 x[4];
+  const int64_t from_page = from[full];
+  for (int run = blockIdx.y * 4 + (tid >> 6); run < runs;
+       run += 4 * gridDim.y) {
+    const int h = run % g.Hkv, lk = run / g.Hkv;
+    uint4* cache = ((lk & 1) ? a.vc : a.kc) +
+                   (int64_t)(lk >> 1) * a.layer_stride +
+                   ((int64_t)h << g.shift) * hc;
+    const u32x4* src =
+        reinterpret_cast<const u32x4*>(cache + from_page * page_chunks);
+    u32x4* dst = reinterpret_cast<u32x4*>(cache + rq.w * page_chunks);
+    for (int i = blockIdx.z * 64 + (tid & 63); i < n; i += 4 * step) {
+      u32x4 x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e * step < n) x[e] = src[i + e * step];
+      for (int e = 0; e < 4; ++e)
+        if (i + e * step < n) x[e] = src[i + e * step];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e * step < n) dst[i + e * step] = x[e];
+      for (int e = 0; e < 4; ++e)
+        if (i + e * step < n) dst[i + e * step] = x[e];
+    }
   }
 }
 
@@ -577,8 +580,9 @@ hipError_t launch_fork(const ForkArgs& f, hipStream_t s) {
   const int runs = f.a.layers * 2 * g.Hkv;
   const int chunks = (g.D / 8) << g.shift;
   const int z = chunks <= 512 ? 1 : chunks / 512 < 16 ? chunks / 512 : 16;
-  hipLaunchKernelGGL(fork_apply_kernel, dim3(f.a.m, (runs + 3) / 4, z),
-                     dim3(256), 0, s, f, runs);
+  const int y = runs < 4 * 65535 ? (runs + 3) / 4 : 65535;
+  hipLaunchKernelGGL(fork_apply_kernel, dim3(f.a.m, y, z), dim3(256), 0, s, f,
+                     runs);
   return hipGetLastError();
 }
 

@@ -109,6 +109,20 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
+// Sum of the squares of a lane's elements.
+__device__ __forceinline__ float squares(const float (&x)[4],
+                                         const float (&y)[4]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    sum = __builtin_fmaf(y[e], y[e], __builtin_fmaf(x[e], x[e], sum));
+  return sum;
+}
+// Below kTiny a sum may have lost squares; elements times kDown have squares
+// within the range if they themselves had none (2^128 2^-70 squared, times 256
+// elements), and those times 1 / kDown if theirs were too small.
+constexpr float kTiny = 0x1p-90f, kDown = 0x1p-70f;
+
 // x or y, as values: a conditional expression of two variables is one of their
 // addresses, which keeps both in memory.
 template <typename T>
@@ -250,14 +264,18 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(
       uint4 y = mine[x];
       if (!in) y = make_uint4(0, 0, 0, 0);
       unpack_pairs<BF16, LAYOUT>(y, x0, x1);
-      float inv = 1.f;
       if (pick(kind == 0, q_norm, k_norm)) {
-        float sum = 0.f;
+        float sum = head_sum<LH>(squares(x0, x1)), eps = a.eps;
+        // squares out of fp32's range: elements and eps by powers of two
+        const bool big = !(sum < pos_inf()), small = sum < kTiny && eps < kTiny;
+        if (__ballot(big || small)) {
+          const float f = big ? kDown : small ? 1.f / kDown : 1.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sum = __builtin_fmaf(x1[e], x1[e], __builtin_fmaf(x0[e], x0[e], sum));
-        sum = head_sum<LH>(sum);
-        inv = 1.f / __builtin_sqrtf(sum / (float)D + a.eps);
+          for (int e = 0; e < 4; ++e) x0[e] *= f, x1[e] *= f;
+          sum = head_sum<LH>(squares(x0, x1));
+          eps = eps * f * f;
+        }
+        const float inv = 1.f / __builtin_sqrtf(sum / (float)D + eps);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x0[e] *= inv * pick(kind == 0, w[0][e], w[1][e]);

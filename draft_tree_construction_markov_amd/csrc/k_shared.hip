@@ -38,17 +38,14 @@ __device__ __forceinline__ RowSums row_sums(const AttendWs& ws,
   return r;
 }
 
-// A workgroup adds up ROWS rows, LR threads each (4 elements a thread).
-template <bool BF16, int LR>
-__global__ __launch_bounds__(kJoinThreads) void shared_join_kernel(
-    AttendArgs a, AttendPlan ps, AttendPlan po, AttendWs ws, AttendWs wo) {
-  constexpr int ROWS = kJoinThreads / LR;
+// Row m of request b's packed rows of head h, elements 4 c ..: adds up what
+// the runs of both parts left.
+template <bool BF16>
+__device__ __forceinline__ void join_row(
+    const AttendArgs& a, const AttendPlan& ps, const AttendPlan& po,
+    const AttendWs& ws, const AttendWs& wo, const int4& rq, const int2& group,
+    int b, int h, int m, int c) {
   const PageGeom& g = a.g;
-  const int b = blockIdx.x / g.Hkv, h = blockIdx.x - b * g.Hkv;
-  const int4 rq = a.share.req[b];
-  const int2 group = a.share.group_of[b];
-  const int m = blockIdx.y * ROWS + threadIdx.x / LR, c = threadIdx.x % LR;
-  if (m >= (rq.y + 1) * a.G || 4 * c >= g.D) return;
   JoinSum s{neg_inf(), 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   auto add_slots = [&](auto count, const RowSums& r, int dp, int x0)
       __attribute__((always_inline)) {
@@ -108,14 +105,30 @@ __global__ __launch_bounds__(kJoinThreads) void shared_join_kernel(
                                   (float)kLn2;
 }
 
+// A workgroup adds up ROWS rows, LR threads each (4 elements a thread).
+template <bool BF16, int LR>
+__global__ __launch_bounds__(kJoinThreads) void shared_join_kernel(
+    AttendArgs a, AttendPlan ps, AttendPlan po, AttendWs ws, AttendWs wo) {
+  constexpr int ROWS = kJoinThreads / LR;
+  const PageGeom& g = a.g;
+  const int b = blockIdx.x / g.Hkv, h = blockIdx.x - b * g.Hkv;
+  const int4 rq = a.share.req[b];
+  const int2 group = a.share.group_of[b];
+  const int M = (rq.y + 1) * a.G, c = threadIdx.x % LR;
+  if (4 * c >= g.D) return;
+  for (int m = blockIdx.y * ROWS + threadIdx.x / LR; m < M;
+       m += gridDim.y * ROWS)
+    join_row<BF16>(a, ps, po, ws, wo, rq, group, b, h, m, c);
+}
+
 template <bool BF16, int LR>
 hipError_t launch_join(const AttendArgs& a, const AttendPlan& ps,
                        const AttendPlan& po, const AttendWs& ws,
                        const AttendWs& wo, hipStream_t s) {
   constexpr int ROWS = kJoinThreads / LR;
-  const int64_t M = (int64_t)(a.g.N + 1) * a.G;
+  const int64_t y = ((int64_t)(a.g.N + 1) * a.G + ROWS - 1) / ROWS;
   hipLaunchKernelGGL((shared_join_kernel<BF16, LR>),
-                     dim3(a.g.batch * a.g.Hkv, (unsigned)((M + ROWS - 1) / ROWS)),
+                     dim3(a.g.batch * a.g.Hkv, (unsigned)(y < 65535 ? y : 65535)),
                      dim3(kJoinThreads), 0, s, a, ps, po, ws, wo);
   return hipGetLastError();
 }

@@ -459,7 +459,7 @@ pct_status pct_cache_write(const pct_cache_shape* shape /*host*/,
  *                              the pair (rounded up) that makes `low`
  *           PCT_ROTARY_BANDS   the same with w = (turns of pair i over
  *                              `original` positions - low) / (high - low)
- *           w is taken as at least 0 and at most 1
+ *           (the pairs of a ramp are kept within 0 .. rot - 1, w within 0 .. 1)
  *  amplitude  factor of the rotated elements (1: none)
  *
  * pct_rotary_table -- frequencies of a description.
@@ -608,7 +608,8 @@ typedef struct {
  * positions and lets go of the rest in the same way (n_nodes NULL = N).
  * Only batch, N (trim), n_pages, page_size and max_pages are read.
  * Errors: PCT_ERR_INVALID_ARG for sizes, m < 0, null pointers, arrays that
- * overlap; PCT_ERR_UNSUPPORTED for batch or m > 65535; PCT_ERR_WORKSPACE. */
+ * overlap; PCT_ERR_UNSUPPORTED for batch or m > 65535 or n_pages > 2^30;
+ * PCT_ERR_WORKSPACE. */
 size_t pct_cache_free_workspace(const pct_cache_shape* shape /*host*/);
 pct_status pct_cache_free(const pct_cache_shape* shape /*host*/, int32_t m,
                           const int32_t* places,

@@ -281,3 +281,26 @@ def test_binding_refuses():
         pct.CachePages(4, 10, 4, 2, 1, 16).trim(t.d)
     with pytest.raises(pct.PCTError):
         pct.CachePages(0, 10, 4, 3, 1, 16)
+
+
+def test_fork_of_many_layers_and_heads():
+    # more (layer, head) runs than a grid has rows of workgroups
+    rng = np.random.default_rng(9)
+    P, layers, Hkv = 4, 1024, 1024
+    h = pct.CachePages(3, P, 2, 2, Hkv, 16, layers=layers)
+    s = Pages(3, P, 2, 2)
+    s.grow(0, 3)
+    d = pct.PageState(*(dev_i32(x) for x in (s.ctx, s.table, s.held, s.ring,
+                                             s.state, s.extra)))
+    k = torch.randint(-99, 99, (layers, P, Hkv, 2, 16),
+                      dtype=torch.int16, device="cuda").view(torch.bfloat16)
+    v = k.flip(0).contiguous()
+    want = [x.view(torch.int16).clone() for x in (k, v)]
+    announce("fork, many layers and heads")
+    assert h.fork(d, dev_i32([0]), dev_i32([2]), k, v).tolist() == [1]
+    assert s.fork([0], [2]).tolist() == [1]
+    assert np.array_equal(d.block_table.cpu().numpy(), s.table)
+    a, b = int(s.table[0, 1]), int(s.table[2, 1])
+    for x, got in zip(want, (k, v)):
+        x[:, b, :, :1] = x[:, a, :, :1]
+        assert torch.equal(got.view(torch.int16), x)

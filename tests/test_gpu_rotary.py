@@ -285,3 +285,18 @@ def test_a_round_of_the_cache():
                     err = np.abs(got(b, i).float().cpu().numpy() - y[b, i])
                     assert (err <= tol[b, i]).all()
     assert not out[1, 3].any() and not c.k[0].any()
+
+
+@pytest.mark.parametrize("power", [-100, -60, 45, 100])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_squares_past_the_range_of_fp32(power, eps):
+    c = Case(2, 5, 4, 2, 80, 16, 80, "half", "none", True, BF, unused=False)
+    c.qkv.mul_(2.0 ** power)
+    c.qkv[0, 1] = 1.0
+    c.eps = eps
+    q, k, v = c.q.clone(), c.k.clone(), c.v.clone()
+    announce("rotary, powers", power, eps)
+    got = c.call()
+    torch.cuda.synchronize()
+    c.check_q(got, c.was, q)
+    c.check_cache(k, v)

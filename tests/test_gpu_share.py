@@ -335,3 +335,38 @@ def test_binding_refuses():
             pct.SharePlan(**d)
         with pytest.raises(pct.PCTError):
             pct.SharedAttention(Hq=2, Hkv=2, D=64, **d)
+
+
+def test_more_rows_than_a_grid_has():
+    # one key-value head for 128 query heads, and as many rows as there are
+    N, Hq, page = 8192, 128, 16
+    R = N + 1
+    table = np.tile(np.arange(514, dtype=np.int32), (2, 1))
+    table[1, 1:] += 513
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn(1030, 1, page, 16, generator=g, device="cuda").to(BF)
+            for _ in range(2))
+    q = torch.randn(2, R, Hq, 16, generator=g, device="cuda").to(BF)
+    ctx, n, tab = dev_i32([16, 21]), dev_i32([N, 700]), dev_i32(table)
+    plan = pct.SharePlan(2, N, 1030, page, 514, least=1)
+    h = pct.SharedAttention(2, N, Hq, 1, 16, 1030, page, 514, lse=True)
+    announce("shared attention, many rows")
+    s = plan.run(ctx, n, tab)
+    got, lse = h.run(q, k, v, tab, s)
+    assert s.shared.tolist() == [16, 16] and s.leader.tolist() == [0, 0]
+    # rows here and there against the definition in 64 bits
+    kd, vd = k.double(), v.double()
+    for b, i in ((0, 0), (0, 1), (0, 4095), (0, 8192), (0, 8191), (1, 700),
+                 (1, 13)):
+        t = torch.arange(int(ctx[b]) + i + 1, device="cuda")
+        at, off = tab[b].long()[t // page], t % page
+        K, V = kd[at, 0, off], vd[at, 0, off]
+        z = q[b, i].double() @ K.T * 0.25
+        w = torch.softmax(z, -1)
+        o, A = w @ V, w @ V.abs()
+        ds = (q[b, i].double().abs() @ K.abs().T).max() * 0.25 * 19 * 2 ** -24
+        tol = A * (2 * 2 ** -8 + 2 * ds + (2 * len(t) + 64) * 2 ** -24)
+        assert ((got[b, i].double() - o).abs() <= tol).all(), (b, i)
+        assert ((lse[b, i].double() - torch.logsumexp(z, -1)).abs() <=
+                ds + (2 * len(t) + 128) * 2 ** -24).all()
+    assert not got[1, 701:].any()

@@ -77,6 +77,8 @@ def test_refuses(call):
         other = 4096 if name != "ctx_len" else 8192
         assert call(shape(), st=state(**{name: other})) == 1, name
     assert call(shape(batch=65536)) == 2
+    assert call(shape(n_pages=(1 << 30) + 1), **(
+        dict(stride=1 << 50) if call in (fork, compact) else {})) == 2
     assert call(shape(), ws=None) == 3
     assert call(shape(), nbytes=7) == 3
     assert call(shape(), ws=ODD) == 1
