@@ -896,18 +896,19 @@ class SharePlan:
     """Plan of the prefixes that requests of a round share, found from their
     block tables; fixed shape, with its workspace and outputs allocated once;
     run() only enqueues kernels.  least: positions that a group must save to
-    be one.  (Attention with and without groups, 32 heads of 128 over 400 ..
+    be one (default: 4096, times the rows of a request up to 8).  (Attention with and without groups, 32 heads of 128 over 400 ..
     600 own positions: 8 tokens that save 1792 positions 16.0 and 16.2 us, 7168
     17.5 and 19.9; 64 tokens, 4032 32.9 and 33.0, 16 k 34.7 and 38.0; 16 x 16
     rows, 3840 26.0 and 25.3, 61 k 54 and 56; 4 x 65 rows, 3072 40 and 31,
     12 k 56 and 52.)"""
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
-                 max_pages: int, least: int = 4096, device="cuda"):
+                 max_pages: int, least: int | None = None,
+                 device="cuda"):
         self.shape = CacheShape(batch, N, n_pages, page_size, max_pages, 1, 1,
                                 16, PCT_BF16)
         self.device = dev = _device(device)
-        self.least = least
+        self.least = 4096 * min(N + 1, 8) if least is None else least
         self._fn, self._ref = lib().pct_cache_share, C.byref(self.shape)
         size = lib().pct_cache_share_size(self._ref)
         if size == 0:
@@ -1177,13 +1178,13 @@ class PagedCache:
     compact() moves the pages in use to the front, all between a commit and
     the next plan (until then nothing is written, attended or kept), and
     attend reads what requests share once for all of them, if that saves at
-    least `least` positions.  batch is at most 1024 then.
+    least `least` positions (SharePlan).  batch is at most 1024 then.
     """
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
                  max_pages: int, Hq: int, Hkv: int, D: int, layers: int = 1,
-                 dtype=torch.bfloat16, share: bool = False, least: int = 4096,
-                 device="cuda"):
+                 dtype=torch.bfloat16, share: bool = False,
+                 least: int | None = None, device="cuda"):
         dev = _device(device)
         i32 = dict(dtype=torch.int32, device=dev)
         self.k = torch.zeros(layers, n_pages, Hkv, page_size, D, dtype=dtype,

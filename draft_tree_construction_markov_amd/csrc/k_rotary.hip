@@ -132,6 +132,7 @@ __device__ __forceinline__ T pick(bool c, T x, T y) {
 
 constexpr int kRotaryThreads = 256;
 constexpr int kAhead = 4;  // heads of a lane that are loaded together
+constexpr int kResident = 5120;  // waves on the chip
 
 template <int LH, bool BF16, int LAYOUT>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(
@@ -314,7 +315,7 @@ hipError_t launch_rotary_lh(const RotaryArgs& a, hipStream_t s) {
   const int units = (a.q ? (a.Hq + HW - 1) / HW : 0) +
                     (a.k ? 2 * ((a.Hkv + HW - 1) / HW) : 0);
   // a wave per row, or several while these are few
-  int64_t splits = 16384 / a.rows;
+  int64_t splits = kResident / a.rows;
   splits = splits < 1 ? 1 : splits > units ? units : splits;
   const int per = (int)((units + splits - 1) / splits);
   splits = (units + per - 1) / per;

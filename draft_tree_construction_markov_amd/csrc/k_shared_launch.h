@@ -1,6 +1,6 @@
 // k_shared_launch.h -- the launch of attention in two parts for one padded head
-// size.  Heads up to 128: one launch for both.  Larger heads: a launch for each (their tiles of
-// 128 rows have 8 waves, those of 16 rows 4).
+// size: one for both, or a launch for each where a wide head has tiles of 128
+// rows (which have 8 waves, the others 4).
 #pragma once
 #include "k_attend_rows.h"
 #include "k_attend_tiles.h"
@@ -34,7 +34,8 @@ struct PartKernel<DP, 16, BF16, PART> {
 // 196, 60, 64 us; shared keys first 220, 191, 68, 69; by turns 245, 303, 64,
 // 71; two launches 209, 202, 65, 74.  4 x 6 rows: 13.4, two launches 21.)
 template <class X, class Y>
-__global__ __launch_bounds__(256, 2) void attend_parts_kernel(AttendParts x) {
+__global__ __launch_bounds__(256, Y::C::OCC) void attend_parts_kernel(
+    AttendParts x) {
   __shared__ union {
     typename X::Lds shared;
     typename Y::Lds own;
@@ -94,9 +95,21 @@ hipError_t launch_part_type(const AttendArgs& a, const AttendPlan& p,
   return hipGetLastError();
 }
 
-// one part after the other
+// Wide heads: one launch unless there are row tiles of 128 rows.
+template <int DP, bool BF16>
+hipError_t launch_parts_small(const AttendParts& x, hipStream_t s) {
+  using Rows = PartKernel<DP, 16, BF16, kOwnKeys>;
+  using Tiles = PartKernel<DP, 64, BF16, kOwnKeys>;
+  using Shared = PartKernel<DP, 64, BF16, kSharedKeys>;
+  if (x.p[1].mt > 16) return launch_both<Shared, Tiles>(x, s);
+  if (x.p[0].mt > 16) return launch_both<Shared, Rows>(x, s);
+  return launch_both<PartKernel<DP, 16, BF16, kSharedKeys>, Rows>(x, s);
+}
 template <int DP>
 hipError_t launch_parts_wide(const AttendParts& x, hipStream_t s) {
+  if (x.p[0].mt <= 64 && x.p[1].mt <= 64)
+    return x.a[0].bf16 ? launch_parts_small<DP, true>(x, s)
+                       : launch_parts_small<DP, false>(x, s);
   hipError_t e =
       x.a[0].bf16
           ? launch_part_type<DP, true, kSharedKeys>(x.a[0], x.p[0], x.ws[0], s)
