@@ -1033,7 +1033,7 @@ def cache_commit(tau, accept_node, ctx_len, n_nodes, block_table, k_cache,
     return out
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class PageState:
     """The state of a cache's pages, int32: ctx_len [batch], block_table
     [batch][max_pages], n_held [batch], ring [n_pages] and ring_state [2] as

@@ -65,7 +65,8 @@ def forked_tables(rng, batch, width, page, P, prompts, depth):
     (33, 40, 8, 3000, 4, 38, 0), (64, 500, 16, 9000, 3, 400, 20),
     (128, 300, 16, 20000, 3, 290, 2), (130, 40, 1024, 500, 9, 40, 0),
     (1024, 20, 4, 5000, 40, 18, 1), (1000, 70, 2, 20000, 6, 60, 20),
-    (12, 3000, 16, 30000, 2, 2900, 5), (70, 30, 8, 20, 5, 28, 1)])
+    (12, 3000, 16, 30000, 2, 2900, 5), (70, 30, 8, 20, 5, 28, 1),
+    (16, 300, 16, 5000, 3, 290, 2), (8, 2000, 16, 9000, 2, 1900, 0)])
 def test_plan(batch, width, page, P, prompts, depth, N):
     rng = np.random.default_rng(batch + width)
     groups = 0
@@ -170,6 +171,24 @@ def test_many_groups():
                    [i % 40 for i in range(60)], 1, 4, 2, 64, 16)
     got = run(c)
     assert len(set(got[2].leader[got[2].shared > 0].tolist())) == 11
+    check(c, got)
+
+
+@pytest.mark.parametrize("D", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("batch,N,Hq", [(20, 0, 16), (6, 15, 8), (5, 31, 6)])
+def test_wide_tables(D, dtype, batch, N, Hq):
+    # a block table for long requests: shared row tiles of 128 rows
+    of = [i % 2 if i < batch - 1 else -1 for i in range(batch)]
+    n = [N - i % (N // 2 + 1) for i in range(batch)]
+    c = SharedCase(D + batch, of, [130, 210], [3 + 17 * i % 90 for i in
+                                              range(batch)], N, Hq, 2, D, 16,
+                   n=n, dtype=dtype)
+    wide = np.full((batch, 7000), -1, np.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    got = run(c)
+    assert (got[2].shared > 0).sum() == batch - 1
     check(c, got)
 
 
