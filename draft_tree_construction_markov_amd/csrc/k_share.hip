@@ -13,7 +13,9 @@
 // count by comparison (pages counted by atomics took 12 us for 128 tables of
 // up to 1281 pages, at 40 holders a page); pick: the best of all columns;
 // join: leaders, and the comparison with them; pack: one workgroup.  Each is
-// a few dependent loads; small tables go through all of it in one workgroup.
+// a few dependent loads (128 tables of up to 1281 pages: 6.4, 4.0, 4.4 and 5.6
+// us); small tables go through all of it in one workgroup (8 tables of up to 82
+// pages 6.9 us).
 #include "pct_cache.h"
 #include "pct_device.h"
 

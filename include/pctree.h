@@ -344,6 +344,10 @@ pct_status pct_build_tree_noalloc(const pct_tree_shape* shape /*host*/,
  *   { pct_cache_write, pct_tree_attention } -> pct_verify_accept or
  *   pct_verify_sample -> pct_cache_commit -> the next round
  *
+ * With rotary positions pct_cache_write_rotary takes pct_cache_write's place.
+ * Where requests share pages (pct_cache_fork), pct_cache_trim comes before the
+ * plan, and pct_cache_share after it with pct_shared_attention in the layers.
+ *
  * Positions of a request: its ctx_len committed tokens, then the root (the
  * last token the target supplied, not yet in the cache) at position
  * ctx_len, then node i at position ctx_len + 1 + i.  Rows: row 0 of a
