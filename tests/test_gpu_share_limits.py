@@ -1,0 +1,142 @@
+"""GPU checks of rotary writes, forks, compaction and shared attention in a
+cache whose offsets pass 32 bits, and of calls with small or odd arguments."""
+import numpy as np
+import pytest
+import torch
+
+import draft_tree_construction_markov_amd as pct
+from cacheref import attention
+from gpu_util import announce, dev_i32
+from pagesref import Pages
+from rotaryref import rotate, tolerance
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def test_offsets_past_32_bits():
+    # pages of 4 MB, 1300 of them: 5.4 GB for the keys, as much for the values
+    P, Hkv, page, D = 1300, 8, 1024, 256
+    k = torch.empty(1, P, Hkv, page, D, dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    s = Pages(4, P, page, 4)
+    s.ring[:] = np.roll(np.arange(P)[::-1], 0)     # the last pages first
+    s.grow(0, 1030)
+    d = pct.PageState(*(dev_i32(x) for x in (s.ctx, s.table, s.held, s.ring,
+                                             s.state, s.extra)))
+    assert s.table[0, :2].tolist() == [1299, 1298]
+    # rows rotated into the context's last positions
+    r = pct.Rotary(D)
+    R = 31
+    torch.manual_seed(0)
+    qkv = torch.randn(1, R, 4 * Hkv, D, device="cuda").to(BF)
+    q, kk, vv = qkv[:, :, :2 * Hkv], qkv[:, :, 2 * Hkv:3 * Hkv], \
+        qkv[:, :, 3 * Hkv:]
+    pos = np.arange(1000, 1000 + R)[None]
+    slot = s.table[0][pos // page].astype(np.int64) * page + pos % page
+    announce("rotary past 32 bits")
+    rq = pct.cache_write_rotary(r, q, kk, vv, dev_i32(pos),
+                                torch.from_numpy(slot).cuda(), k[0], v[0])
+    torch.cuda.synchronize()
+    f = [int(x) % (1 << 64) for x in r.table.tolist()]
+    y, mag = rotate(kk.float().cpu().numpy(), pos, f, D, "half")
+    tol = tolerance(y, mag, BF)
+    for i in range(R):
+        p, o = divmod(int(slot[0, i]), page)
+        got = k[0, p, :, o].float().cpu().numpy()
+        assert (np.abs(got - y[0, i]) <= tol[0, i]).all()
+        assert torch.equal(v[0, p, :, o], vv[0, i])
+    # the earlier positions, then two samples
+    for x in (k, v):
+        x[0, 1299, :, :1000] = torch.randn(Hkv, 1000, D, device="cuda").to(BF)
+    h = pct.CachePages(4, P, page, 4, Hkv, D)
+    announce("fork past 32 bits")
+    assert h.fork(d, dev_i32([0, 0]), dev_i32([1, 3]), k, v).tolist() == [1, 1]
+    s.fork([0, 0], [1, 3])
+    assert np.array_equal(d.block_table.cpu().numpy(), s.table)
+    for b in (1, 3):
+        for x in (k, v):
+            assert torch.equal(x[0, int(s.table[b, 1]), :, :6],
+                               x[0, 1298, :, :6])
+    # attention of all three before and after they moved to the front
+    plan = pct.SharePlan(4, 0, P, page, 4, least=1)
+    att = pct.SharedAttention(4, 0, 2 * Hkv, Hkv, D, P, page, 4, lse=True)
+    ctx, n = dev_i32([1029, 1029, 0, 1029]), dev_i32([0, 0, -1, 0])
+    rows = rq[:, 7:11].reshape(4, 1, 2 * Hkv, D).contiguous()
+
+    def attend():
+        announce("shared attention past 32 bits")
+        sh = plan.run(ctx, n, d.block_table)
+        out, lse = att.run(rows, k[0], v[0], d.block_table, sh)
+        torch.cuda.synchronize()
+        assert sh.shared.tolist() == [1024, 1024, 0, 1024]
+        return out.clone(), lse.clone()
+
+    out, lse = attend()
+    table = s.table
+    low = torch.from_numpy(np.unique(table[[0, 1, 3], :2])).cuda()
+    small = np.searchsorted(low.cpu().numpy(), table).astype(np.int32)
+    o, z, tol, tol_z = attention(
+        rows.double().cpu().numpy(), k[0][low.long()].double().cpu().numpy(),
+        v[0][low.long()].double().cpu().numpy(), small,
+        [1029, 1029, 0, 1029], [0, 0, -1, 0], None, D ** -0.5, BF)
+    on = [0, 1, 3]
+    assert (np.abs(out.double().cpu().numpy() - o)[on] <= tol[on]).all()
+    assert (np.abs(lse.double().cpu().numpy() - z)[on] <= tol_z[on]).all()
+    announce("compaction past 32 bits")
+    h.compact(d, k, v)
+    s.k = s.v = None
+    s.compact()
+    assert np.array_equal(d.block_table.cpu().numpy(), s.table)
+    assert s.table.max() == 3
+    again, lse2 = attend()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_pages_of_one_position_and_one_request():
+    k = torch.randn(1, 9, 1, 1, 16, device="cuda").to(BF)
+    v = torch.randn(1, 9, 1, 1, 16, device="cuda").to(BF)
+    h = pct.CachePages(1, 9, 1, 3, 1, 16)
+    s = Pages(1, 9, 1, 3, head=4)
+    s.grow(0, 3)
+    d = pct.PageState(*(dev_i32(x) for x in (s.ctx, s.table, s.held, s.ring,
+                                             s.state, s.extra)))
+    announce("pages of one position")
+    assert h.fork(d, dev_i32([0]), dev_i32([0]), k, v).tolist() == [0]
+    before = k[0, torch.from_numpy(s.table[0].astype(np.int64)).cuda()].clone()
+    h.compact(d, k, v)
+    assert d.block_table.tolist() == [[0, 1, 2]]
+    assert torch.equal(k[0, :3], before)
+    assert d.ring_state.tolist() == [0, 6]
+    h.free(d, dev_i32([0, 0, 0]))
+    assert d.ring_state.tolist() == [0, 9] and not d.ctx_len.any()
+    assert sorted(d.ring.tolist()) == list(range(9))
+
+
+def test_places_on_other_streams_of_one_state():
+    # calls on one stream after the other, in the order of their events
+    P = 40
+    h = pct.CachePages(4, P, 4, 6, 1, 16)
+    k = torch.randn(1, P, 1, 4, 16, device="cuda").to(BF)
+    v = torch.randn_like(k)
+    s = Pages(4, P, 4, 6)
+    s.grow(0, 17)
+    d = pct.PageState(*(dev_i32(x) for x in (s.ctx, s.table, s.held, s.ring,
+                                             s.state, s.extra)))
+    src, dst = dev_i32([0, 0]), dev_i32([1, 2])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    streams[0].wait_stream(torch.cuda.current_stream())
+    announce("pages, two streams")
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            h.fork(d, src, dst, k, v)
+            h.free(d, dst)
+        streams[(i + 1) % 2].wait_stream(streams[i % 2])
+    torch.cuda.synchronize()
+    for _ in range(6):
+        s.fork([0, 0], [1, 2])
+        s.free([1, 2])
+    for got, want in ((d.ring, s.ring), (d.ring_state, s.state),
+                      (d.extra, s.extra), (d.block_table, s.table)):
+        assert np.array_equal(got.cpu().numpy(), want)
