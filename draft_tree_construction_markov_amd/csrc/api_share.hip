@@ -30,12 +30,14 @@ ShareView view_of(const pct_cache_shape* sh, const void* share) {
   v.req = static_cast<int4*>(const_cast<void*>(share));
   v.groups = v.req + sh->batch;
   v.group_of = reinterpret_cast<int2*>(v.groups + sh->batch);
-  v.rows = reinterpret_cast<int32_t*>(v.group_of + sh->batch);
+  v.totals = reinterpret_cast<float*>(v.group_of + sh->batch);
+  v.rows = reinterpret_cast<int32_t*>(v.totals + 4);
   return v;
 }
 
 size_t share_size(const pct_cache_shape* sh) {
-  return (size_t)sh->batch * (2 * sizeof(int4) + sizeof(int2)) +
+  return 4 * sizeof(float) +
+         (size_t)sh->batch * (2 * sizeof(int4) + sizeof(int2)) +
          (size_t)sh->batch * (sh->N + 1) * sizeof(int32_t);
 }
 

@@ -284,7 +284,7 @@ __device__ __forceinline__ void next_request(const AttendArgs& a,
   }
 }
 
-// Fills in the run of workgroup `block` of n_wg; false when it has none (its
+// Fills in the run of workgroup `block` of `blocks`; false when it has none (its
 // entry of the join is then empty).  Every wave does this by itself: lane l goes
 // through requests l per .. (l + 1) per - 1, and the sums over lanes need no
 // LDS.
@@ -292,7 +292,8 @@ template <int MT, int KS, int FEW, int LEAST, int PART = kAllKeys,
           int EXTRA = 0>
 __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
                                                 const AttendWs& ws, int block,
-                                                AttendRun& r, AttendReq& rq) {
+                                                int blocks, AttendRun& r,
+                                                AttendReq& rq) {
   const PageGeom& g = a.g;
   const int lane = threadIdx.x & 63;
   const int per = (g.batch + 63) / 64;
@@ -332,7 +333,7 @@ __device__ __forceinline__ bool attend_schedule(const AttendArgs& a,
   const bool same = __ballot(least != 0x7fffffff && least != RT) == 0;
   if (PART == kAllKeys) block = blockIdx.x;
   const int xcd = block & 7, at = block >> 3;
-  const int n_wg = PART == kAllKeys ? (int)gridDim.x : ws.n_wg;
+  const int n_wg = PART == kAllKeys ? (int)gridDim.x : blocks;
   const int per_xcd = n_wg >> 3;
   // levels, if they keep at least 4 of 5 workgroups busy
   int bx = RT > 0 ? per_xcd / RT : 0;  // blocks of an XCD

@@ -58,7 +58,7 @@ struct RowsLds {
 template <class C>
 __device__ __forceinline__ void attend_rows(const AttendArgs& a,
                                             const AttendWs& ws, int block,
-                                            RowsLds<C>& mem) {
+                                            int blocks, RowsLds<C>& mem) {
   constexpr int NT = C::NT, KB = C::KB, CH = C::CH, NL = C::NL;
   constexpr int DT = C::DT, KSTEP = C::KSTEP;
   uint4* const lds = mem.tiles;
@@ -73,7 +73,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a,
   AttendRun run;
   AttendReq rq;
   if (!attend_schedule<C::MT, C::KS, C::FEW, C::LEAST, C::PART, C::EXTRA>(
-          a, ws, block, run, rq))
+          a, ws, block, blocks, run, rq))
     return;
   i32x4 join = {0, 0, 0, -1};
 
@@ -312,7 +312,7 @@ template <class C>
 __global__ __launch_bounds__(256, C::OCC) void attend_rows_kernel(
     AttendArgs a, AttendWs ws) {
   __shared__ RowsLds<C> mem;
-  attend_rows<C>(a, ws, blockIdx.x, mem);
+  attend_rows<C>(a, ws, blockIdx.x, gridDim.x, mem);
 }
 
 }  // namespace pct

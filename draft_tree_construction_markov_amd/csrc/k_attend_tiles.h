@@ -470,14 +470,14 @@ struct TilesLds {
 template <class C>
 __device__ __forceinline__ void attend_tiles(const AttendArgs& a,
                                              const AttendWs& ws, int block,
-                                             uint4* tiles,
+                                             int blocks, uint4* tiles,
                                              uint64_t (*odd_s)[C::W]) {
   constexpr int KB = C::KB, SL = C::SL, MT = C::MT;
 
   AttendRun run;
   AttendReq rq;
   if (!attend_schedule<MT, KB, C::FEW, C::LEAST, C::PART, C::EXTRA>(
-          a, ws, block, run, rq))
+          a, ws, block, blocks, run, rq))
     return;
   i32x4 join = {0, 0, 0, -1};
   if ((a.g.D >> 3) < SL) {
@@ -519,7 +519,7 @@ __global__ __launch_bounds__(64 * C::W, C::OCC) void attend_tiles_kernel(
   AttendRun run;
   AttendReq rq;
   if (!attend_schedule<MT, KB, C::FEW, C::LEAST, C::PART, C::EXTRA>(
-          a, ws, blockIdx.x, run, rq))
+          a, ws, blockIdx.x, gridDim.x, run, rq))
     return;
   i32x4 join = {0, 0, 0, -1};
   if ((a.g.D >> 3) < SL) {

@@ -149,6 +149,7 @@ struct PackLds {
   int2 lead[kPackThreads];  // leader or -1, rows in a group
   int to[kPackThreads], size[kPackThreads];
   int2 group[kPackThreads], wave_sum[kPackThreads / kWave];
+  float totals[kPackThreads / kWave][3];
 };
 __device__ __forceinline__ void share_pack(const ShareArgs& a, PackLds& s,
                                            bool with_rows) {
@@ -213,8 +214,30 @@ __device__ __forceinline__ void share_pack(const ShareArgs& a, PackLds& s,
     a.view.group_of[b] = group;
     s.to[b] = group.y + before;
   }
-  if (!with_rows) return;
+  // (only how the attention divides its workgroups depends on these)
+  float own = 0.f, rows = 0.f;
+  if (len.y >= 0) {
+    const int cap = g.max_pages << g.shift, before_own = (d + 1) << g.shift;
+    own = (float)(min(min(len.x, cap - 1) + len.y + 1, cap) - before_own);
+    rows = (float)(len.y + 1) * (float)before_own;
+  }
+  if (wave * kWave < g.batch) {
+    own = wave_sum(own);
+    rows = wave_sum(rows);
+    const float requests = (float)__popcll(__ballot(len.y >= 0));
+    if (lane == 0) {
+      s.totals[wave][0] = own;
+      s.totals[wave][1] = requests;
+      s.totals[wave][2] = rows;
+    }
+  }
   __syncthreads();
+  if (b < 3) {
+    float sum = 0.f;
+    for (int w = 0; w * kWave < g.batch; ++w) sum += s.totals[w][b];
+    a.view.totals[b] = sum;
+  }
+  if (!with_rows) return;
   const int R = g.N + 1;
   for (int x = b; x < g.batch * R; x += kPackThreads) {
     const int q = x / R, i = x - q * R;

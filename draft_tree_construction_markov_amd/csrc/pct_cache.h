@@ -113,6 +113,8 @@ struct ShareView {
   int4* groups;       // [batch] {leader, shared positions, rows (0: no such
                       // group), first packed row}
   int2* group_of;     // [batch] {group or -1, its first packed row}
+  float* totals;      // positions of the own keys of all requests, requests
+                      // with rows, rows times shared positions, unused
   int32_t* rows;      // [batch * (N + 1)] row of each packed row
 };
 struct ShareArgs {

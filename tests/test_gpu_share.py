@@ -31,7 +31,7 @@ def check_plan(ctx, n, table, P, page, N, least, given=True):
     # the packed rows: each row of a group's requests once, group by group
     batch, R = len(ctx), N + 1
     plan = o.plan.cpu().numpy()
-    rows = plan[10 * batch:]
+    rows = plan[10 * batch + 4:]
     groups = plan[4 * batch:8 * batch].reshape(batch, 4)
     at, seen = 0, 0
     for g, lead in enumerate(x for x in range(batch)
