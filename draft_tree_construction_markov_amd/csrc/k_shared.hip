@@ -6,10 +6,9 @@
 // and the join adds them up: m = max(m_1, m_2 ..), O = sum_i 2^(m_i - m) O_i.
 // The shared keys are then read once for a group instead of once for each of
 // its requests, and the packed rows fill the row tiles.  One token of 128
-// requests over two prefixes of 16 k positions and 64 .. 4096 own ones 209 us
-// (tree attention 1259), 16 requests of 65 rows over 8 k 199 (238), 735
-// TFLOP/s.  The join is bound by the sums' read: 10 us for 35 MB there, 18 for
-// 60 MB.
+// requests over two prefixes of 16 k positions and 64 .. 4096 own ones 180 us
+// (tree attention 1259), 16 requests of 65 rows over 8 k 182 (238), 802
+// TFLOP/s.  The join is bound by the sums' read: 7 and 16 us of these.
 #include "k_attend_join.h"
 
 namespace pct {
@@ -264,7 +263,7 @@ hipError_t launch_shared_attention(const AttendArgs& a, void* workspace,
   ProfScope prof(PROF_JOIN, rows, s);
   // Groups where the shared row tiles are cut into many runs each (7 tokens
   // over 31 k shared positions, 2 heads, 256 runs: 53 us without, 30 with; 123
-  // tokens over 16 k, 8 heads, 13 runs: 209 and 211).
+  // tokens over 16 k, 8 heads, 512 runs of 40 row tiles: 209 and 211).
   const int64_t tiles =
       ((int64_t)g.batch * (g.N + 1) * a.G / x.shared.plan.mt + 1) * g.Hkv;
   const int groups = x.shared.plan.n_wg >= 16 * tiles ? 4 : 1;

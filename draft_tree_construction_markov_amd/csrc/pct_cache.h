@@ -179,11 +179,11 @@ constexpr int kWhole = 6;  // a row tile of so few steps stays in one run
 constexpr int tiles_least(int mt) { return mt == 64 ? 8 : 4; }
 constexpr int kCus = 256;  // compute units of an MI355X
 // In two parts (below) a row tile counts as so many steps more than it has, for
-// its beginning and its end, or runs of many short row tiles would end last:
-// 123 requests of one token over 64 .. 4096 own keys each and two shared
-// prefixes 255 us without, 16 requests of 65 rows 218; with 1 / 1 step of keys
-// per wave / of shared tiles 216 and 210, with 1 / 3 209 and 202, with 2 / 2
-// 213 and 204, with 1 / 6 210 and 208.
+// its beginning and its end, or runs of many short row tiles would end last.
+// (In two launches: 123 requests of one token over 64 .. 4096 own keys each and
+// two shared prefixes 255 us without, 16 requests of 65 rows 218; with 1 / 1
+// step of few rows / of shared tiles 216 and 210, with 1 / 3 209 and 202, with
+// 2 / 2 213 and 204, with 1 / 6 210 and 208.)
 constexpr int kRowsExtra = 1, kTilesExtra = 3;
 // fp16 holds probabilities times 2^kLift (k_attend_impl.h has the reason).
 template <bool BF16>
