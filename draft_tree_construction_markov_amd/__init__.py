@@ -909,6 +909,8 @@ class SharePlan:
                                 16, PCT_BF16)
         self.device = dev = _device(device)
         self.least = 4096 * min(N + 1, 8) if least is None else least
+        if not 1 <= self.least < 1 << 31:
+            raise ValueError(f"least = {least} is not in 1 .. 2^31 - 1")
         self._fn, self._ref = lib().pct_cache_share, C.byref(self.shape)
         size = lib().pct_cache_share_size(self._ref)
         if size == 0:

@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256, 2) void attend_split_kernel(AttendParts x) {
   n = max(min(n, x.ws[0].n_wg >> 3), places - (x.ws[1].n_wg >> 3));
   // half of them among the first places of the compute units, half among the
   // second ones
-  const int n0 = (n + 1) / 2, n1 = n / 2, k = at < h ? at : at - h;
+  const int n0 = min((n + 1) / 2, h), n1 = n - n0, k = at < h ? at : at - h;
   const bool shared = k < (at < h ? n0 : n1);
   if (shared)
     X::run(x.a[0], x.ws[0], 8 * (at < h ? k : n0 + k) + xcd, 8 * n,

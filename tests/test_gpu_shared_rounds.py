@@ -236,3 +236,121 @@ def test_caches_without_shares_refuse():
         c.free(dev_i32([0]))
     with pytest.raises(ValueError):
         c.compact()
+
+
+def test_captured_rounds_equal_eager_ones():
+    batch, n_pages, width = 5, 90, 12
+    torch.manual_seed(1)
+    rng = np.random.default_rng(4)
+    eager, graph = (pct.PagedCache(batch, N, n_pages, PAGE, width, HQ, HKV, D,
+                                   share=True, least=1) for _ in range(2))
+    rotary = pct.Rotary(D)
+    n = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    depth = torch.zeros(batch, N, dtype=torch.int32, device="cuda")
+    mask = torch.zeros(batch, N, 1, dtype=torch.int64, device="cuda")
+    qkv = torch.zeros(batch, N + 1, HQ + 2 * HKV, D, dtype=BF, device="cuda")
+    q, k, v = qkv[:, :, :HQ], qkv[:, :, HQ:HQ + HKV], qkv[:, :, HQ + HKV:]
+    tau = torch.ones(batch, dtype=torch.int32, device="cuda")
+    accept = torch.full((batch, N), -1, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(batch, N + 1, HQ, D, dtype=BF, device="cuda")
+            for _ in range(2)]
+    turned = [torch.zeros_like(x) for x in outs]
+
+    def step(c, i):
+        c.plan(n, depth)
+        c.write_rotary(0, rotary, q, k, v, out=turned[i])
+        c.attend(0, turned[i], mask, out=outs[i])
+        c.commit(tau, accept)
+
+    def inputs(nodes):
+        _, d, anc = random_trees(rng, batch, N, np.asarray(nodes))
+        n.copy_(dev_i32(nodes))
+        depth.copy_(dev_i32(d))
+        mask.copy_(torch.from_numpy(pack(anc)).cuda())
+        qkv.normal_()
+        for b in range(batch):
+            path = ([] if nodes[b] < 1 else
+                    np.nonzero(anc[b, rng.integers(nodes[b])])[0].tolist())
+            tau[b] = len(path) + 1
+            accept[b] = torch.tensor((path + [-1] * N)[:N])
+
+    inputs([5, 2, -1, -1, -1])
+    for i, c in enumerate((eager, graph)):
+        step(c, i)
+    g = torch.cuda.CUDAGraph()
+    announce("captured shared rounds")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    state = [x.clone() for x in (graph.ctx_len, graph.block_table,
+                                 graph.n_held, graph.ring, graph.ring_state)]
+    with torch.cuda.graph(g):
+        step(graph, 1)
+    for x, y in zip((graph.ctx_len, graph.block_table, graph.n_held,
+                     graph.ring, graph.ring_state), state):
+        assert torch.equal(x, y)         # a capture runs nothing
+    live = [5, 2, -1, -1, -1]
+    for turn in range(14):
+        inputs(live)
+        step(eager, 0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(*outs) and torch.equal(*turned)
+        for x in ("ctx_len", "block_table", "n_held", "ring", "ring_state",
+                  "extra", "k", "v"):
+            assert torch.equal(getattr(eager, x), getattr(graph, x)), x
+        assert torch.equal(eager.share.shared, graph.share.shared)
+        if turn == 5:
+            for c in (eager, graph):
+                assert c.fork(dev_i32([0, 0]), dev_i32([2, 4])).all()
+            live = [5, 2, 4, -1, 3]
+        if turn == 9:
+            for c in (eager, graph):
+                c.free(dev_i32([1, 2]))
+                c.fork(dev_i32([4]), dev_i32([3]))
+                c.compact()
+            live = [1, -1, -1, 5, 5]
+    assert (eager.share.shared > 0).sum() == 3
+
+
+def test_two_caches_on_two_streams():
+    torch.manual_seed(2)
+    caches = [pct.PagedCache(6, 0, 400, 16, 60, 8, 2, D, share=True, least=1)
+              for _ in range(2)]
+    rotary = pct.Rotary(D)
+    rows = [torch.randn(40, 6, 1, 12, D, device="cuda").to(BF)
+            for _ in range(2)]
+    outs = [[None] * 40, [None] * 40]
+    only = dev_i32([0, -1, -1, -1, -1, -1])
+    every = dev_i32([0] * 6)
+
+    def run(i, at):
+        c = caches[i]
+        x = rows[i][at]
+        c.plan(only if at < 20 else every)
+        r = c.write_rotary(0, rotary, x[:, :, :8], x[:, :, 8:10],
+                           x[:, :, 10:])
+        outs[i][at] = c.attend(0, r).clone()
+        c.commit(dev_i32([1] * 6), dev_i32(np.full((6, 1), -1)))
+        if at == 19:
+            c.fork(dev_i32([0] * 5), dev_i32([1, 2, 3, 4, 5]))
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    announce("two shared caches on two streams")
+    for at in range(40):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                run(i, at)
+    torch.cuda.synchronize()
+    both = [[x.clone() for x in y] for y in outs]
+    kept = [c.k.clone() for c in caches]
+    # the same, one after the other
+    caches = [pct.PagedCache(6, 0, 400, 16, 60, 8, 2, D, share=True, least=1)
+              for _ in range(2)]
+    for i in range(2):
+        for at in range(40):
+            run(i, at)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs[i], both[i]))
+        assert torch.equal(caches[i].k, kept[i])
