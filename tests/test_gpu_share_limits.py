@@ -109,6 +109,9 @@ def test_pages_of_one_position_and_one_request():
     assert d.block_table.tolist() == [[0, 1, 2]]
     assert torch.equal(k[0, :3], before)
     assert d.ring_state.tolist() == [0, 6]
+    # caches of one layer without that dimension
+    h.compact(d, k[0], v[0])
+    assert torch.equal(k[0, :3], before)
     h.free(d, dev_i32([0, 0, 0]))
     assert d.ring_state.tolist() == [0, 9] and not d.ctx_len.any()
     assert sorted(d.ring.tolist()) == list(range(9))
