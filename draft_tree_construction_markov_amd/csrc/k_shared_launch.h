@@ -135,21 +135,25 @@ hipError_t launch_parts_dp(const AttendParts& x, hipStream_t s) {
                      : launch_parts_type<DP, false>(x, s);
 }
 
+// One part of wide heads.  (Shared keys come here with tiles of 128 rows only.)
 template <int DP, bool BF16, int PART>
 hipError_t launch_part_type(const AttendArgs& a, const AttendPlan& p,
                             const AttendWs& ws, hipStream_t s) {
   if (p.n_wg == 0) return hipSuccess;
-  using Half = TilesCfg<DP, 64, BF16, PART>;
   using Full = TilesCfg<DP, 128, BF16, PART>;
-  if (p.mt == 64)
-    hipLaunchKernelGGL((attend_tiles_kernel<Half>), dim3(p.n_wg),
-                       dim3(64 * Half::W), 0, s, a, ws);
-  else if (p.mt == 128)
-    hipLaunchKernelGGL((attend_tiles_kernel<Full>), dim3(p.n_wg),
-                       dim3(64 * Full::W), 0, s, a, ws);
-  else
-    hipLaunchKernelGGL((attend_rows_kernel<RowsCfg<DP, BF16, PART>>),
-                       dim3(p.n_wg), dim3(256), 0, s, a, ws);
+  if constexpr (PART == kOwnKeys) {
+    using Half = TilesCfg<DP, 64, BF16, PART>;
+    using Rows = RowsCfg<DP, BF16, PART>;
+    if (p.mt == 64)
+      hipLaunchKernelGGL((attend_tiles_kernel<Half>), dim3(p.n_wg),
+                         dim3(64 * Half::W), 0, s, a, ws);
+    if (p.mt == 16)
+      hipLaunchKernelGGL((attend_rows_kernel<Rows>), dim3(p.n_wg), dim3(256),
+                         0, s, a, ws);
+    if (p.mt < 128) return hipGetLastError();
+  }
+  hipLaunchKernelGGL((attend_tiles_kernel<Full>), dim3(p.n_wg),
+                     dim3(64 * Full::W), 0, s, a, ws);
   return hipGetLastError();
 }
 
