@@ -918,15 +918,19 @@ class SharePlan:
                            lib().pct_last_error().decode())
         self.ws = _workspace(lib().pct_cache_share_workspace(self._ref), dev)
         i32 = dict(dtype=torch.int32, device=dev)
-        # no rows before the first run
-        plan = torch.zeros(size // 4, **i32)
+        # no rows and no groups before the first run (one buffer, so that one
+        # copy goes back to that)
+        self._all = torch.zeros(size // 4 + 2 * batch, **i32)
+        plan, leader, shared = self._all.split((size // 4, batch, batch))
         req = plan[:4 * batch].view(batch, 4)
         req[:, 1] = -1
         req[:, 3] = -1
         plan[8 * batch:10 * batch] = -1
+        torch.arange(batch, out=leader)
+        self._none = self._all.clone()
         self.out = CacheShare(
-            leader=torch.arange(batch, **i32), shared=torch.zeros(batch, **i32),
-            plan=plan, key=(batch, N, n_pages, page_size, max_pages))
+            leader=leader, shared=shared, plan=plan,
+            key=(batch, N, n_pages, page_size, max_pages))
         o = self.out
         self._tail = tuple(C.c_void_p(x.data_ptr()) for x in (
             o.leader, o.shared, o.plan, self.ws)) + (self.ws.numel(),)
@@ -943,6 +947,10 @@ class SharePlan:
                  _want("block_table", block_table, i32, (batch, width), dev),
                  *self._tail)
         return self.out
+
+    def clear(self):
+        """Outputs as before the first run: no rows and no groups."""
+        self._all.copy_(self._none)
 
 
 class SharedAttention:
@@ -1178,7 +1186,8 @@ class PagedCache:
     share: requests may hold the same pages (extra counts their holders).
     fork() makes a place a copy of another's context, free() empties places,
     compact() moves the pages in use to the front, all between a commit and
-    the next plan (until then nothing is written, attended or kept), and
+    the next plan (until then nothing is written, rotated, attended or kept,
+    and nobody shares), and
     attend reads what requests share once for all of them, if that saves at
     least `least` positions (SharePlan).  batch is at most 1024 then.
     """
@@ -1211,7 +1220,6 @@ class PagedCache:
             self._share = SharePlan(batch, N, n_pages, page_size, max_pages,
                                     least=least, device=dev)
             self.share = self._share.out
-            self._no_share = self.share.plan.clone()
             self._attend = SharedAttention(*sizes, dtype=dtype, device=dev)
         else:
             self._attend = TreeAttention(*sizes, dtype=dtype, device=dev)
@@ -1223,10 +1231,11 @@ class PagedCache:
                          self.ring, self.ring_state, self.extra)
 
     def _void(self):
-        """Until the next plan there are no rows."""
+        """Until the next plan there are no rows and no groups."""
         self._plan.out.slot.fill_(-1)
+        self._plan.out.pos.fill_(-1)
         self.n_served.fill_(-1)
-        self.share.plan.copy_(self._no_share)
+        self._share.clear()
 
     def fork(self, src, dst, length=None):
         """Place dst[i] becomes a copy of the first length[i] (default: all)

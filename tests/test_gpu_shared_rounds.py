@@ -354,3 +354,34 @@ def test_two_caches_on_two_streams():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(outs[i], both[i]))
         assert torch.equal(caches[i].k, kept[i])
+
+
+def test_no_rows_and_no_groups_until_the_next_plan():
+    r = Rounds(4, 60, 10, 3)
+    while r.lengths()[0] < 2 * PAGE:
+        r.round([5, 5, -1, -1])
+    assert r.fork([(0, 2)]).tolist() == [1]
+    c = r.c
+    for act in (lambda: c.fork(dev_i32([1]), dev_i32([3])),
+                lambda: c.free(dev_i32([3])), c.compact):
+        rows = c.plan(dev_i32([2, 2, 2, -1]), dev_i32(np.ones((4, N))))
+        assert (rows.pos[:3, :3] >= 0).all()
+        assert c.share.leader.tolist() == [0, 1, 0, 3]
+        assert (c.share.shared > 0).tolist() == [True, False, True, False]
+        announce("until the next plan")
+        act()
+        before = [x.clone() for x in (c.k, c.v)]
+        kv = torch.ones(4, N + 1, HKV, D, dtype=BF, device="cuda")
+        q = torch.ones(4, N + 1, HQ, D, dtype=BF, device="cuda")
+        out = torch.full_like(q, 3.0)
+        c.write_rotary(0, r.rotary, q, kv, kv, out=out)
+        torch.cuda.synchronize()
+        assert (out == 3.0).all()
+        for x, y in zip(before, (c.k, c.v)):
+            assert torch.equal(x, y)
+        assert c.share.leader.tolist() == [0, 1, 2, 3]
+        assert not c.share.shared.any()
+        assert (rows.pos == -1).all() and (rows.slot == -1).all()
+    # and the next plan brings them back
+    r.round([2, 2, 2, -1])
+    assert c.share.leader.tolist() == [0, 1, 0, 3]
