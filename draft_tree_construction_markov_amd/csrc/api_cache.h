@@ -24,10 +24,15 @@ inline pct_status hip_fail(hipError_t e, const char* what) {
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// arrays of n and m values that share memory (a null pointer has none)
-inline bool overlap(const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
+// memory of n bytes from x on and of m bytes from y on meet (a null pointer
+// has none)
+inline bool bytes_meet(const void* x, size_t n, const void* y, size_t m) {
   const uintptr_t p = (uintptr_t)x, q = (uintptr_t)y;
-  return x && y && p < q + 4 * (uintptr_t)m && q < p + 4 * (uintptr_t)n;
+  return x && y && p < q + m && q < p + n;
+}
+// arrays of n and m values that share memory
+inline bool overlap(const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
+  return bytes_meet(x, 4 * (size_t)n, y, 4 * (size_t)m);
 }
 
 inline int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }

@@ -68,14 +68,6 @@ pct_status pct_cache_share(const pct_cache_shape* shape, int32_t least,
   if (least < 1) return fail(PCT_ERR_INVALID_ARG, "least must be positive");
   if (!ctx_len || !block_table || !leader || !shared || !share)
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
-  const int64_t n = shape->batch, t = n * shape->max_pages;
-  const int32_t* out[2] = {leader, shared};
-  for (const int32_t* x : out)
-    if (overlap(x, n, ctx_len, n) || overlap(x, n, n_nodes, n) ||
-        overlap(x, n, block_table, t))
-      return fail(PCT_ERR_INVALID_ARG, "leader or shared overlap an input");
-  if (overlap(leader, n, shared, n))
-    return fail(PCT_ERR_INVALID_ARG, "leader overlaps shared");
   if (!aligned16(share))
     return fail(PCT_ERR_INVALID_ARG, "share must be 16-byte aligned");
   const size_t need = share_workspace(shape);
@@ -83,6 +75,24 @@ pct_status pct_cache_share(const pct_cache_shape* shape, int32_t least,
     return fail(PCT_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (!aligned16(workspace))
     return fail(PCT_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const size_t n = 4 * (size_t)shape->batch;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } all[] = {{leader, n},
+             {shared, n},
+             {share, share_size(shape)},
+             {workspace, need},
+             {ctx_len, n},
+             {n_nodes, n},
+             {block_table, n * shape->max_pages}};
+  // (the first four are written)
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (bytes_meet(all[i].p, all[i].bytes, all[j].p, all[j].bytes))
+        return fail(PCT_ERR_INVALID_ARG,
+                    "leader, shared, share or the workspace overlap each "
+                    "other or an input");
   ShareArgs a{};
   a.g = geom(shape, block_table, ctx_len, n_nodes);
   a.least = least;

@@ -691,9 +691,9 @@ pct_status pct_cache_compact(const pct_cache_shape* shape /*host*/,
  *          for pct_shared_attention, which holds the lengths too
  *  workspace  pct_cache_share_workspace(shape) bytes
  * Only batch, N, n_pages, page_size and max_pages of the shape are read.
- * Errors: PCT_ERR_INVALID_ARG for sizes, least < 1, null pointers, outputs
- * that overlap each other or an input; PCT_ERR_UNSUPPORTED for batch > 1024;
- * PCT_ERR_WORKSPACE. */
+ * Errors: PCT_ERR_INVALID_ARG for sizes, least < 1, null pointers, outputs or
+ * a workspace that overlap each other or an input; PCT_ERR_UNSUPPORTED for
+ * batch > 1024; PCT_ERR_WORKSPACE. */
 size_t pct_cache_share_size(const pct_cache_shape* shape /*host*/);
 size_t pct_cache_share_workspace(const pct_cache_shape* shape /*host*/);
 pct_status pct_cache_share(const pct_cache_shape* shape /*host*/,

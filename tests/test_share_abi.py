@@ -73,6 +73,23 @@ def test_plan_refuses():
     assert plan(shape(), ws=ODD) == 1
 
 
+def test_plan_refuses_a_share_or_workspace_that_overlaps():
+    L, sh = pct.lib(), shape()
+    size = L.pct_cache_share_size(C.byref(sh))
+    need = L.pct_cache_share_workspace(C.byref(sh))
+    # (the first address that is aligned and whose last bytes meet the array)
+    at = dict(ctx=256, n=512, table=4096, leader=8192, shared=12288)
+    for x in at.values():
+        for y in (x, ((x - size) // 16 + 1) * 16):
+            assert plan(sh, n=512, share=C.c_void_p(y)) == 1, (x, y)
+        for y in (x, ((x - need) // 16 + 1) * 16):
+            assert plan(sh, n=512, ws=C.c_void_p(y)) == 1, (x, y)
+    assert plan(sh, n=512, share=C.c_void_p(4096 + 16)) == 1   # within
+    for y in (WS.value, WS.value + (need - 1) // 16 * 16,
+              WS.value - (size - 1) // 16 * 16):
+        assert plan(sh, share=C.c_void_p(y)) == 1, y
+
+
 def test_attention_refuses():
     assert attend(None) == 1
     for name in ("q", "kc", "vc", "table", "share", "out"):
