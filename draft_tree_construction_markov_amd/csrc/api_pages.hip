@@ -6,49 +6,66 @@ using namespace pct;
 
 namespace {
 
-// Arrays of a page state, for the checks of overlap.
+// Arrays of a call, for the checks of overlap.
 struct Span {
   const int32_t* p;
   int64_t n;
 };
+
+struct StateSpans {
+  Span all[6];
+};
+StateSpans spans_of(const pct_cache_shape* sh, const pct_page_state* st) {
+  return {{{st->ctx_len, sh->batch},
+           {st->block_table, (int64_t)sh->batch * sh->max_pages},
+           {st->n_held, sh->batch},
+           {st->ring, sh->n_pages},
+           {st->ring_state, 2},
+           {st->extra, sh->n_pages}}};
+}
 
 pct_status check_state(const pct_cache_shape* sh, const pct_page_state* st) {
   // (pages are counted in 32 bits, past the last one of a scan)
   if (sh->n_pages > 1 << 30)
     return fail(PCT_ERR_UNSUPPORTED, "n_pages = %d exceeds 2^30", sh->n_pages);
   if (!st) return fail(PCT_ERR_INVALID_ARG, "state is NULL");
-  const Span all[] = {{st->ctx_len, sh->batch},
-                      {st->block_table, (int64_t)sh->batch * sh->max_pages},
-                      {st->n_held, sh->batch},
-                      {st->ring, sh->n_pages},
-                      {st->ring_state, 2},
-                      {st->extra, sh->n_pages}};
-  for (const Span& x : all)
-    if (!x.p) return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
+  const StateSpans x = spans_of(sh, st);
+  for (const Span& y : x.all)
+    if (!y.p) return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
   for (int i = 0; i < 6; ++i)
     for (int j = 0; j < i; ++j)
-      if (overlap(all[i].p, all[i].n, all[j].p, all[j].n))
+      if (overlap(x.all[i].p, x.all[i].n, x.all[j].p, x.all[j].n))
         return fail(PCT_ERR_INVALID_ARG, "arrays of the state overlap");
   return PCT_OK;
 }
 
-// whether x meets an array of the state
+// whether n values from x on meet an array of the state
 bool meets_state(const pct_cache_shape* sh, const pct_page_state* st,
                  const int32_t* x, int64_t n) {
-  return overlap(x, n, st->ctx_len, sh->batch) ||
-         overlap(x, n, st->block_table, (int64_t)sh->batch * sh->max_pages) ||
-         overlap(x, n, st->n_held, sh->batch) ||
-         overlap(x, n, st->ring, sh->n_pages) ||
-         overlap(x, n, st->ring_state, 2) ||
-         overlap(x, n, st->extra, sh->n_pages);
+  for (const Span& y : spans_of(sh, st).all)
+    if (overlap(x, n, y.p, y.n)) return true;
+  return false;
 }
 
-pct_status check_workspace(const void* ws, size_t have, size_t need) {
+// The workspace holds what kernels of a call leave for the next ones: it must
+// not meet the state, which the call changes, nor its other arrays.
+template <int N>
+pct_status check_workspace(const void* ws, size_t have, size_t need,
+                           const pct_cache_shape* sh, const pct_page_state* st,
+                           const Span (&more)[N]) {
   if (!ws || have < need)
     return fail(PCT_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (!aligned16(ws))
     return fail(PCT_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  return PCT_OK;
+  const auto meets = [&](const Span& y) {
+    return bytes_meet(ws, need, y.p, 4 * (size_t)y.n);
+  };
+  bool met = false;
+  for (const Span& y : spans_of(sh, st).all) met = met || meets(y);
+  for (const Span& y : more) met = met || meets(y);
+  return met ? fail(PCT_ERR_INVALID_ARG,
+                    "workspace overlaps the state or another array")
+             : PCT_OK;
 }
 
 pct_status check_caches(const pct_cache_shape* sh, int layers,
@@ -117,7 +134,9 @@ pct_status pct_cache_free(const pct_cache_shape* shape, int32_t m,
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
   if (meets_state(shape, state, places, m))
     return fail(PCT_ERR_INVALID_ARG, "places overlaps the state");
-  st = check_workspace(workspace, workspace_bytes, release_workspace(*shape));
+  const Span more[] = {{places, m}};
+  st = check_workspace(workspace, workspace_bytes, release_workspace(*shape),
+                       shape, state, more);
   if (st != PCT_OK || m == 0) return st;
   PagesArgs a = pages_args(shape, state, nullptr);
   a.m = m;
@@ -134,7 +153,9 @@ pct_status pct_cache_trim(const pct_cache_shape* shape, const int32_t* n_nodes,
   if ((st = check_state(shape, state)) != PCT_OK) return st;
   if (meets_state(shape, state, n_nodes, shape->batch))
     return fail(PCT_ERR_INVALID_ARG, "n_nodes overlaps the state");
-  st = check_workspace(workspace, workspace_bytes, release_workspace(*shape));
+  const Span more[] = {{n_nodes, shape->batch}};
+  st = check_workspace(workspace, workspace_bytes, release_workspace(*shape),
+                       shape, state, more);
   if (st != PCT_OK) return st;
   PagesArgs a = pages_args(shape, state, n_nodes);
   a.count = static_cast<int32_t*>(workspace);
@@ -169,8 +190,9 @@ pct_status pct_cache_fork(const pct_cache_shape* shape, int32_t layers,
       overlap(done, m, dst, m) || overlap(done, m, length, m))
     return fail(PCT_ERR_INVALID_ARG,
                 "src, dst, length or done overlap the state or each other");
+  const Span more[] = {{src, m}, {dst, m}, {length, m}, {done, m}};
   st = check_workspace(workspace, workspace_bytes,
-                       fork_workspace(shape->batch, m));
+                       fork_workspace(shape->batch, m), shape, state, more);
   if (st != PCT_OK || m == 0) return st;
   ForkArgs f{};
   f.a = pages_args(shape, state, nullptr);
@@ -216,7 +238,9 @@ pct_status pct_cache_compact(const pct_cache_shape* shape, int32_t layers,
       meets_state(shape, state, table_out,
                   (int64_t)shape->batch * shape->max_pages))
     return fail(PCT_ERR_INVALID_ARG, "table_out overlaps the state");
-  st = check_workspace(workspace, workspace_bytes, compact_workspace(*shape));
+  const Span more[] = {{table_out, (int64_t)shape->batch * shape->max_pages}};
+  st = check_workspace(workspace, workspace_bytes, compact_workspace(*shape),
+                       shape, state, more);
   if (st != PCT_OK) return st;
   CompactArgs c{};
   c.a = pages_args(shape, state, nullptr);

@@ -610,9 +610,10 @@ typedef struct {
  *  workspace  pct_cache_free_workspace(shape) bytes
  * pct_cache_trim -- every request keeps the pages of its ctx_len + n_nodes + 1
  * positions and lets go of the rest in the same way (n_nodes NULL = N).
- * Only batch, N (trim), n_pages, page_size and max_pages are read.
- * Errors: PCT_ERR_INVALID_ARG for sizes, m < 0, null pointers, arrays that
- * overlap; PCT_ERR_UNSUPPORTED for batch or m > 65535 or n_pages > 2^30;
+ * Only batch, N (trim), n_pages, page_size and max_pages are read (an N that
+ * is not has to be in its range too, here and for the calls below).
+ * Errors: PCT_ERR_INVALID_ARG for sizes, m < 0, null pointers, arrays or a
+ * workspace that overlap; PCT_ERR_UNSUPPORTED for batch or m > 65535 or n_pages > 2^30;
  * PCT_ERR_WORKSPACE. */
 size_t pct_cache_free_workspace(const pct_cache_shape* shape /*host*/);
 pct_status pct_cache_free(const pct_cache_shape* shape /*host*/, int32_t m,

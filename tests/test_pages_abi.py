@@ -84,6 +84,28 @@ def test_refuses(call):
     assert call(shape(), ws=ODD) == 1
 
 
+WORKSPACE = {free: lambda L, s: L.pct_cache_free_workspace(s),
+             trim: lambda L, s: L.pct_cache_free_workspace(s),
+             fork: lambda L, s: L.pct_cache_fork_workspace(s, 3),
+             compact: lambda L, s: L.pct_cache_compact_workspace(s)}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_workspace_that_overlaps_is_refused(call):
+    need = WORKSPACE[call](pct.lib(), ref(shape()))
+    kw = dict(n=256) if call is trim else {}
+    arrays = [4096 * (i + 1) for i in range(6)]
+    arrays += {free: [256], trim: [256], fork: [256, 512, 768],
+               compact: [1 << 20]}[call]
+    for x in arrays:
+        # the first address that is aligned and whose last bytes meet x
+        for y in (x, ((x - need) // 16 + 1) * 16):
+            assert y > 0
+            assert call(shape(), ws=C.c_void_p(y), **kw) == 1, (x, y)
+    if call is fork:
+        assert fork(shape(), length=1024, ws=C.c_void_p(1024)) == 1
+
+
 def test_free_and_trim_refuse():
     assert free(shape(), m=-1) == 1
     assert free(shape(), m=65536) == 2
