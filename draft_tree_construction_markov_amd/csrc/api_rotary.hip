@@ -105,16 +105,13 @@ pct_status pct_cache_write_rotary(
     int64_t k_row_stride, const void* v, int64_t v_row_stride,
     const int32_t* pos, const int64_t* slot, void* q_out,
     int64_t q_out_row_stride, void* k_cache, void* v_cache, void* stream) {
-  if (shape && (shape->max_pages < 1 || (!q && shape->Hq < 1))) {
+  pct_cache_shape sh;
+  if (shape) {
     // neither the block table nor, without queries, their heads are read
-    pct_cache_shape sh = *shape;
-    if (sh.max_pages < 1) sh.max_pages = 1;
-    if (!q && sh.Hq < 1) sh.Hq = sh.Hkv;
-    if (sh.Hq >= 1)
-      return pct_cache_write_rotary(&sh, rotary, table, eps, q_weight,
-                                    k_weight, q, q_row_stride, k, k_row_stride,
-                                    v, v_row_stride, pos, slot, q_out,
-                                    q_out_row_stride, k_cache, v_cache, stream);
+    sh = *shape;
+    sh.max_pages = 1;
+    if (!q) sh.Hq = sh.Hkv;
+    shape = &sh;
   }
   pct_status st = check_pages(shape);
   if (st != PCT_OK) return st;

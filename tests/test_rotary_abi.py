@@ -121,3 +121,13 @@ def test_write_refuses_an_output_that_overlaps():
     assert write(shape(), out=D, os=264) == 1
     assert write(shape(), out=C.c_void_p(FAR + 16)) == 1
     assert write(shape(), out=C.c_void_p(2 * FAR - 16)) == 1
+
+
+def test_write_does_not_read_the_table_width():
+    # a refusal that comes after the sizes' checks
+    for width in (0, -1, 1 << 27, 2 ** 31 - 1):
+        assert write(shape(max_pages=width), eps=-1.0) == 1
+        assert b"eps" in pct.lib().pct_last_error(), width
+    for heads in (0, -1, 5, 2 ** 31 - 1):
+        assert write(shape(Hq=heads), q=None, out=None, eps=-1.0) == 1
+        assert b"eps" in pct.lib().pct_last_error(), heads
