@@ -315,6 +315,10 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(
   }
 }
 
+// Rows of a launch at most: a grid has fewer than 2^32 threads, and a row here
+// 64 of them.
+constexpr int64_t kLaunchRows = 1 << 25;
+
 template <int LH, bool BF16>
 hipError_t launch_rotary_lh(const RotaryArgs& a, hipStream_t s) {
   constexpr int HW = kWave / LH;
@@ -348,9 +352,24 @@ hipError_t launch_rotary_type(const RotaryArgs& a, hipStream_t s) {
   return launch_rotary_lh<32, BF16>(a, s);
 }
 
-hipError_t launch_cache_rotary(const RotaryArgs& a, hipStream_t s) {
-  return a.bf16 ? launch_rotary_type<true>(a, s)
-                : launch_rotary_type<false>(a, s);
+hipError_t launch_cache_rotary(const RotaryArgs& all, hipStream_t s) {
+  for (int64_t row = 0; row < all.rows; row += kLaunchRows) {
+    RotaryArgs a = all;
+    a.rows = all.rows - row < kLaunchRows ? all.rows - row : kLaunchRows;
+    const auto from = [&](const void* x, int64_t stride) {
+      return x ? static_cast<const uint16_t*>(x) + row * stride : nullptr;
+    };
+    a.q = from(all.q, all.qs);
+    a.k = from(all.k, all.ks);
+    a.v = from(all.v, all.vs);
+    if (all.out) a.out = static_cast<uint16_t*>(all.out) + row * all.os;
+    a.pos = all.pos + row;
+    if (all.slot) a.slot = all.slot + row;
+    const hipError_t e = a.bf16 ? launch_rotary_type<true>(a, s)
+                                : launch_rotary_type<false>(a, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace pct

@@ -300,3 +300,36 @@ def test_squares_past_the_range_of_fp32(power, eps):
     torch.cuda.synchronize()
     c.check_q(got, c.was, q)
     c.check_cache(k, v)
+
+
+def test_more_rows_than_a_grid_has_threads_for():
+    # 2^26 + 8193 rows of one head of 16 elements, in place: rows on both sides
+    # of every 2^24th one, the first and the last against the definition
+    R, batch, D = 8193, 8193, 16
+    rows = R * batch
+    assert rows > 1 << 26
+    rotary = pct.Rotary(D)
+    cache = torch.zeros(1, 1, 1, D, dtype=BF, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn(rows, D, generator=g, device="cuda", dtype=BF)
+    q = q.view(batch, R, 1, D)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    pos[rows - 2] = -1
+    at = sorted({x for m in range(0, rows, 1 << 24) for x in (m, m - 1)
+                 if x >= 0} | {rows - 1, rows - 2, rows - 8193, 1 << 26})
+    was = q.view(rows, D)[at].float().cpu().numpy()
+    announce("rotary, rows past 2^26", rows)
+    out = pct.cache_write_rotary(rotary, q, None, None, pos.view(batch, R),
+                                 None, cache, cache, out=q)
+    torch.cuda.synchronize()
+    assert out is q
+    got = q.view(rows, D)[at].float().cpu().numpy()
+    f = [int(x) % (1 << 64) for x in rotary.table.cpu().tolist()]
+    y, mag = rotate(was[:, None], np.array(at), f, D, "half")
+    tol = tolerance(y, mag, BF)
+    for i, x in enumerate(at):
+        if x == rows - 2:
+            assert np.array_equal(got[i], was[i])
+        else:
+            assert (np.abs(got[i] - y[i, 0]) <= tol[i, 0]).all(), x
+            assert x == 0 or not np.array_equal(got[i], was[i]), x
