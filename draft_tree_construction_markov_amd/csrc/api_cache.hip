@@ -69,12 +69,12 @@ pct_status pct_cache_write(const pct_cache_shape* shape, const void* k,
                            int64_t k_row_stride, const void* v,
                            int64_t v_row_stride, const int64_t* slot,
                            void* k_cache, void* v_cache, void* stream) {
-  if (shape && shape->max_pages < 1) {
+  pct_cache_shape sh;
+  if (shape) {
     // the block table is not read: its width does not matter here
-    pct_cache_shape sh = *shape;
+    sh = *shape;
     sh.max_pages = 1;
-    return pct_cache_write(&sh, k, k_row_stride, v, v_row_stride, slot,
-                           k_cache, v_cache, stream);
+    shape = &sh;
   }
   pct_status st = check_pages(shape);
   if (st != PCT_OK) return st;

@@ -105,6 +105,13 @@ def test_plan_refuses():
     assert plan(shape(), ws=ODD) == 1
 
 
+def test_write_does_not_read_the_table_width():
+    # a refusal that comes after the sizes' checks
+    for width in (0, -1, 1 << 27, 2 ** 31 - 1):
+        assert write(shape(max_pages=width), ks=120) == 1
+        assert b"strides" in pct.lib().pct_last_error(), width
+
+
 def test_write_refuses():
     assert write(None) == 1
     for name in ("k", "v", "slot", "kc", "vc"):
