@@ -895,9 +895,11 @@ class CacheShare:
 class SharePlan:
     """Plan of the prefixes that requests of a round share, found from their
     block tables; fixed shape, with its workspace and outputs allocated once;
-    run() only enqueues kernels.  least: positions that a group must save to
-    be one (default: 4096, times the rows of a request up to 8).  (Attention with and without groups, 32 heads of 128 over 400 ..
-    600 own positions: 8 tokens that save 1792 positions 16.0 and 16.2 us, 7168
+    run() only enqueues kernels.  least: positions that a request's pick must
+    promise to save (default: 4096, times the rows of a request up to 8); the
+    promise counts all requests with that page at that place, and a group
+    that fewer of them form saves less.  (Attention with and without groups,
+    32 heads of 128 over 400 .. 600 own positions: 8 tokens that save 1792 positions 16.0 and 16.2 us, 7168
     17.5 and 19.9; 64 tokens, 4032 32.9 and 33.0, 16 k 34.7 and 38.0; 16 x 16
     rows, 3840 26.0 and 25.3, 61 k 54 and 56; 4 x 65 rows, 3072 40 and 31,
     12 k 56 and 52.)"""
@@ -1188,8 +1190,8 @@ class PagedCache:
     compact() moves the pages in use to the front, all between a commit and
     the next plan (until then nothing is written, rotated, attended or kept,
     and nobody shares), and
-    attend reads what requests share once for all of them, if that saves at
-    least `least` positions (SharePlan).  batch is at most 1024 then.
+    attend reads what requests share once for all of them, if that promises to
+    save `least` positions (SharePlan).  batch is at most 1024 then.
     """
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,

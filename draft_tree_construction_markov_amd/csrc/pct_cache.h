@@ -119,7 +119,7 @@ struct ShareView {
 };
 struct ShareArgs {
   PageGeom g;
-  int least;                      // positions that a group must save
+  int least;                 // positions that a pick must promise
   uint64_t* best;            // [blocks][batch] picks of groups of places
   int blocks;
   int32_t *place, *joined;   // [batch]

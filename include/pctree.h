@@ -684,7 +684,10 @@ pct_status pct_cache_compact(const pct_cache_shape* shape /*host*/,
  * least.  Requests that picked the same page at the same j, and whose
  * tables agree in the entries 0..j with those of the lowest of them, are a
  * group, if they are two or more.
- *  least   positions that a group must save to be one (>= 1)
+ *  least   positions that a pick must promise by its gain (>= 1).  The gain
+ *          counts all requests that have the page there; a group can be fewer
+ *          of them, where others pick another place or differ before it, and
+ *          then saves less
  *  ctx_len, n_nodes (NULL = N), block_table  as for pct_tree_attention
  *  leader  [batch] out: lowest request of the group, b itself without one
  *  shared  [batch] out: positions that the group shares, 0 without one

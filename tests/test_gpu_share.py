@@ -11,6 +11,7 @@ from cacheref import pack
 from gpu_util import announce, dev_i32
 from shareref import SharedCase, share
 from test_gpu_cache_attention import compare
+from test_share_abi import two_depths
 
 pytestmark = pytest.mark.gpu
 
@@ -389,3 +390,14 @@ def test_more_rows_than_a_grid_has():
         assert ((lse[b, i].double() - torch.logsumexp(z, -1)).abs() <=
                 ds + (2 * len(t) + 128) * 2 ** -24).all()
     assert not got[1, 701:].any()
+
+
+@pytest.mark.parametrize("least", [1, 250 * 8, 250 * 8 + 1])
+def test_a_pick_is_measured_by_its_gain(least):
+    # (once in one workgroup, once in four launches)
+    for wide in (46, 700):
+        table = np.full((26, wide), -1, np.int32)
+        table[:, :46] = two_depths()
+        _, shared = check_plan(np.full(26, 45 * 8), np.zeros(26, int), table,
+                               2000, 8, 0, least)
+        assert (shared > 0).sum() == (24 if least > 250 * 8 else 26)

@@ -13,6 +13,15 @@ from test_cache_abi import D, HEADS, ODD, PAGES, shape
 WS = C.c_void_p(1 << 24)
 
 
+def two_depths():
+    """Tables of 46 entries of 26 requests: 10 common pages, and 40 of the
+    last 24."""
+    table = 50 + np.arange(26 * 46, dtype=np.int32).reshape(26, 46)
+    table[:, :10] = np.arange(10)
+    table[2:, 10:40] = np.arange(10, 40)
+    return table
+
+
 def plan(sh, least=64, ws=WS, nbytes=1 << 20, **kw):
     a = dict(ctx=256, n=None, table=4096, leader=8192, shared=12288,
              share=C.c_void_p(1 << 20))
@@ -71,6 +80,21 @@ def test_plan_refuses():
     assert plan(shape(), nbytes=need - 1) == 3
     assert plan(shape(), ws=None) == 3
     assert plan(shape(), ws=ODD) == 1
+
+
+def test_a_pick_is_measured_by_its_gain():
+    """26 requests share 10 pages, 24 of them 40: these pick the deeper page,
+    and the other two, whose gain counts all 26, are a group that saves 10
+    pages."""
+    table = two_depths()
+    n, ctx = [0] * 26, [45 * 8] * 26
+    for least in (1, 250 * 8):
+        leader, shared = share(ctx, n, table, 2000, 8, least)
+        assert leader.tolist() == [0, 0] + [2] * 24
+        assert shared.tolist() == [80, 80] + [320] * 24
+    leader, shared = share(ctx, n, table, 2000, 8, 250 * 8 + 1)
+    assert leader.tolist() == [0, 1] + [2] * 24
+    assert shared.tolist() == [0, 0] + [320] * 24
 
 
 def test_plan_refuses_a_share_or_workspace_that_overlaps():
