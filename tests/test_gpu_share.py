@@ -401,3 +401,50 @@ def test_a_pick_is_measured_by_its_gain(least):
         _, shared = check_plan(np.full(26, 45 * 8), np.zeros(26, int), table,
                                2000, 8, 0, least)
         assert (shared > 0).sum() == (24 if least > 250 * 8 else 26)
+
+
+SIZES = [
+    # of, prefix, own, N, Hq, Hkv, D, page, dtype, table width (0: as needed)
+    ([0, 0, 0], [300], [40, 3, 64], 4, 4, 2, 64, 16, BF, 0),
+    ([0] * 8 + [1] * 5 + [-1], [5000, 3500], [1 + 40 * i for i in range(14)],
+     0, 8, 2, 128, 16, BF, 0),
+    ([0, 0, 1, 1, -1], [700, 64], [9, 300, 1, 70, 500], 64, 8, 2, 128, 32, HF,
+     0),
+    ([0, 0, -1], [250], [10, 90, 30], 256, 2, 1, 128, 16, BF, 0),
+    ([0, 0, 0, -1], [400], [5, 60, 7, 200], 40, 8, 2, 192, 16, BF, 0),
+    ([0, 0, 1, 1], [200, 130], [5, 60, 7, 33], 70, 8, 2, 128, 16, BF, 7000),
+    ([0, 0, 1, 1], [200, 130], [5, 60, 7, 33], 70, 8, 2, 256, 16, HF, 7000)]
+
+
+@pytest.mark.parametrize("shares", [True, False])
+@pytest.mark.parametrize("size", SIZES)
+def test_equals_tree_attention(size, shares):
+    of, prefix, own, N, Hq, Hkv, D, page, dtype, wide = size
+    batch = len(of)
+    n = [N - i % (N // 2 + 1) for i in range(batch)]
+    c = SharedCase(D + N, of, prefix, own, N, Hq, Hkv, D, page, n=n,
+                   dtype=dtype)
+    if wide:
+        table = np.full((batch, wide), -1, np.int32)
+        table[:, :c.table.shape[1]] = c.table
+        c.table = table
+    # (a promise that no call makes: nobody shares)
+    got = run(c, least=1 if shares else 2 ** 31 - 1)
+    assert (got[2].shared > 0).any() == shares
+    h = pct.TreeAttention(batch, N, Hq, Hkv, D, c.n_pages, page,
+                          c.table.shape[1], dtype=dtype, lse=True)
+    announce("tree attention of the same rows")
+    out, lse = h.run(
+        c.q.cuda(), c.k.cuda(), c.v.cuda(), dev_i32(c.table), dev_i32(c.ctx),
+        dev_i32(c.n), scale=c.scale,
+        mask=None if c.anc is None else torch.from_numpy(pack(c.anc)).cuda())
+    torch.cuda.synchronize()
+    want = c.want()
+    check(c, got, want)
+    # each is within its tolerance of the definition: both are within twice it
+    # of each other, and unused rows are as they were in both
+    used = np.arange(N + 1)[None] <= c.n[:, None]
+    for x, y, tol in ((got[0], out, want[2]), (got[1], lse, want[3])):
+        y = y.double().cpu().numpy()
+        assert (np.abs(x - y)[used] <= 2 * tol[used]).all()
+        assert not x[~used].any() and not y[~used].any()
