@@ -385,3 +385,66 @@ def test_no_rows_and_no_groups_until_the_next_plan():
     # and the next plan brings them back
     r.round([2, 2, 2, -1])
     assert c.share.leader.tolist() == [0, 1, 0, 3]
+
+
+def test_captured_forks_frees_and_compactions_equal_eager_ones():
+    batch, n_pages, width = 5, 80, 12
+    torch.manual_seed(3)
+    eager, graph = (pct.PagedCache(batch, 0, n_pages, PAGE, width, HQ, HKV, D,
+                                   layers=LAYERS, share=True, least=1)
+                    for _ in range(2))
+    src, dst, gone = dev_i32([0, 0]), dev_i32([2, 4]), dev_i32([-1, -1])
+    n = dev_i32([0, 0, -1, -1, -1])
+    names = ("ctx_len", "block_table", "n_held", "ring", "ring_state", "extra",
+             "k", "v", "n_served")
+
+    def move(c):
+        c.free(gone)
+        done = c.fork(src, dst)
+        c.compact()
+        return done
+
+    def grow(rounds):
+        for _ in range(rounds):
+            kv = torch.randn(2, batch, 1, HKV, D, device="cuda").to(BF)
+            q = torch.randn(batch, 1, HQ, D, device="cuda").to(BF)
+            outs = []
+            for c in (eager, graph):
+                c.plan(n)
+                for layer in range(LAYERS):
+                    c.write(layer, kv[0], kv[1] * (layer + 1))
+                outs.append(c.attend(LAYERS - 1, q))
+                c.commit(dev_i32([1] * batch), dev_i32([[-1]] * batch))
+            assert torch.equal(*outs)
+
+    def same():
+        torch.cuda.synchronize()
+        for x in names:
+            assert torch.equal(getattr(eager, x), getattr(graph, x)), x
+        for x in ("leader", "shared", "plan"):
+            assert torch.equal(getattr(eager.share, x), getattr(graph.share, x))
+        assert graph.share.leader.tolist() == list(range(batch))
+        assert not graph.share.shared.any()
+
+    grow(3 * PAGE + 2)
+    announce("captured forks, frees and compactions")
+    state = {x: getattr(graph, x).clone() for x in names}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        done = move(graph)
+    for x in names:
+        assert torch.equal(getattr(graph, x), state[x]), x  # nothing ran
+    for live, pairs, free in (
+            ([0, 0, 0, -1, 0], ([0, 0], [2, 4]), [-1, 9]),
+            ([0, 0, 0, 0, 0], ([2, 2], [3, 4]), [4, 1]),
+            ([0, -1, 0, 0, 0], ([1, 3], [0, 1]), [0, 0]),
+            ([-1, 0, 0, 0, 0], ([4, 1], [0, 1]), [1, 0])):
+        src.copy_(dev_i32(pairs[0]))
+        dst.copy_(dev_i32(pairs[1]))
+        gone.copy_(dev_i32(free))
+        want = move(eager)
+        g.replay()
+        assert torch.equal(want, done)
+        same()
+        n.copy_(dev_i32(live))
+        grow(PAGE - 1)
