@@ -899,10 +899,12 @@ class SharePlan:
     promise to save (default: 4096, times the rows of a request up to 8); the
     promise counts all requests with that page at that place, and a group
     that fewer of them form saves less.  (Attention with and without groups,
-    32 heads of 128 over 400 .. 600 own positions: 8 tokens that save 1792 positions 16.0 and 16.2 us, 7168
-    17.5 and 19.9; 64 tokens, 4032 32.9 and 33.0, 16 k 34.7 and 38.0; 16 x 16
-    rows, 3840 26.0 and 25.3, 61 k 54 and 56; 4 x 65 rows, 3072 40 and 31,
-    12 k 56 and 52.)"""
+    32 heads of 128 over 400 .. 600 own positions: 8 tokens that save 1792
+    positions 16.0 and 16.2 us, 7168 17.5 and 19.9; 64 tokens, 4032 32.9 and
+    33.0, 16 k 34.7 and 38.0; 16 x 16 rows, 3840 26.0 and 25.3, 61 k 54 and 56;
+    4 x 65 rows, 3072 40 and 31, 12 k 56 and 52; 8 x 257 rows, 57 k 377 and
+    709, 32 x 257, 63 k 669 and 756, where TreeAttention takes 374 and
+    482.)"""
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
                  max_pages: int, least: int | None = None,
@@ -958,7 +960,14 @@ class SharePlan:
 class SharedAttention:
     """TreeAttention that reads the keys a group of requests shares once for
     all of its rows: fixed shape, workspace and outputs allocated once; run()
-    only enqueues kernels.  Its outputs carry no gradient."""
+    only enqueues kernels.  Its outputs carry no gradient.
+
+    For few rows a request over long shared prefixes (16 x 65 rows over 8 k: 185
+    us, TreeAttention 242).  Every row's sums go through the workspace (ws; 145
+    MB there, 393 MB for 32 x 257 rows of 32 heads of 128, 2.4 GB for 128 x
+    513): trees of 257 rows gain nothing (8 x 257 over 8 k 377 and 374), and
+    without groups they are slower (32 x 257 over 1 k .. 4 k 811
+    and 495, 128 x 513 over 256 .. 2 k 5156 and 3167)."""
 
     def __init__(self, batch: int, N: int, Hq: int, Hkv: int, D: int,
                  n_pages: int, page_size: int, max_pages: int,
@@ -1191,7 +1200,9 @@ class PagedCache:
     the next plan (until then nothing is written, rotated, attended or kept,
     and nobody shares), and
     attend reads what requests share once for all of them, if that promises to
-    save `least` positions (SharePlan).  batch is at most 1024 then.
+    save `least` positions (SharePlan).  batch is at most 1024 then.  All
+    rounds attend by SharedAttention, with its workspace; large trees have
+    faster rows of a TreeAttention on block_table, ctx_len and n_served.
     """
 
     def __init__(self, batch: int, N: int, n_pages: int, page_size: int,
@@ -1281,7 +1292,8 @@ class PagedCache:
                      out=None):
         """write() of a layer whose queries and keys are normalised (with
         weights) and rotated to the rows' places on the way; returns the
-        rotated queries (cache_write_rotary)."""
+        rotated queries (cache_write_rotary), by default a new tensor of zeros
+        in each call: give `out` in the layers of a round."""
         o = self._plan.out
         return cache_write_rotary(rotary, q, k, v, o.pos, o.slot,
                                   self.k[layer], self.v[layer],

@@ -11,8 +11,8 @@
 // Small calls are chains of dependent loads: 4 places of 63 pages freed 3.8
 // us, forked again 4.1 (the plan) and 4.0 (table rows and the rows of 32
 // layers).  The copies are bound by memory: 64 forks of 31 rows at most in 16
-// layers 9.6 us for 43 MB; a compaction that moves 1.44 GB 533 us, 5.2 TB/s
-// (a copy of 1 GiB reaches 5.06).
+// layers 9.3 us for 43 MB; a compaction that moves 1.44 GB 529 us, 5.4 TB/s
+// read and written (a copy of 1 GiB reaches 5.06).
 #include "pct_cache.h"
 #include "pct_device.h"
 

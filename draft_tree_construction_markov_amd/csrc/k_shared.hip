@@ -5,10 +5,13 @@
 //   O = sum_t 2^(z_t - m) v_t, l = sum_t 2^(z_t - m),
 // and the join adds them up: m = max(m_1, m_2 ..), O = sum_i 2^(m_i - m) O_i.
 // The shared keys are then read once for a group instead of once for each of
-// its requests, and the packed rows fill the row tiles.  One token of 128
-// requests over two prefixes of 16 k positions and 64 .. 4096 own ones 180 us
-// (tree attention 1259), 16 requests of 65 rows over 8 k 182 (238), 802
-// TFLOP/s.  The join is bound by the sums' read: 7 and 16 us of these.
+// its requests, and the packed rows fill the row tiles.  On the same inputs
+// again and again, one token of 128 requests over two prefixes of 16 k
+// positions and 64 .. 4096 own ones 176 us (tree attention 1259), 16 requests
+// of 65 rows over 8 k 185 (242), 790 TFLOP/s.  The join is bound by the sums'
+// read: 6 and 16 us of these.  All rows leave sums, those of requests without
+// a group too: 32 x 257 rows over 1 k .. 4 k positions 811 us (495), over a
+// shared 8 k 1476 (1391).
 #include "k_attend_join.h"
 
 namespace pct {
