@@ -656,18 +656,21 @@ class CachePlan:
             o.slot, o.pos, o.missing, o.n_served, self.ws)) + (
                 self.ws.numel(),)
 
+    def _depth(self, depth):
+        nodes = self._shapes[1]
+        if nodes[1] == 0:
+            return None
+        if depth is None:
+            raise ValueError("depth is required when N > 0")
+        return _want("depth", depth, torch.int32, nodes, self.device.index)
+
     def run(self, ctx_len, n_nodes, block_table, n_held, ring, ring_state,
             depth=None) -> CacheRows:
         """n_nodes None = N everywhere; depth [batch][N] gives nodes their
         place in the sequence and is required unless N = 0."""
         dev, i32 = self.device.index, torch.int32
-        one, nodes, pages, free, state = self._shapes
-        if nodes[1] == 0:
-            dp = None
-        elif depth is None:
-            raise ValueError("depth is required when N > 0")
-        else:
-            dp = _want("depth", depth, i32, nodes, dev)
+        one, _, pages, free, state = self._shapes
+        dp = self._depth(depth)
         _enqueue(self._fn, dev, self._ref,
                  _want("ctx_len", ctx_len, i32, one, dev),
                  None if n_nodes is None else
@@ -1273,13 +1276,18 @@ class PagedCache:
         self._void()
 
     def plan(self, n_nodes=None, depth=None) -> CacheRows:
-        self.n_nodes = n_nodes
         if self.share is not None:
+            # (what the plan refuses is refused before pages are let go)
+            self._plan._depth(depth)
+            if n_nodes is not None and \
+                    n_nodes.data_ptr() == self.n_served.data_ptr():
+                raise PCTError(1, "n_served overlaps n_nodes or ctx_len")
             # (pages that others hold must not go back to the ring)
             self._pages.trim(self._state(), n_nodes)
         rows = self._plan.run(self.ctx_len, n_nodes, self.block_table,
                               self.n_held, self.ring, self.ring_state,
                               depth=depth)
+        self.n_nodes = n_nodes
         if self.share is not None:
             self._share.run(self.ctx_len, self.n_served, self.block_table)
         return rows

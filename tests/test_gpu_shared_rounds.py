@@ -448,3 +448,33 @@ def test_captured_forks_frees_and_compactions_equal_eager_ones():
         same()
         n.copy_(dev_i32(live))
         grow(PAGE - 1)
+
+
+def test_a_plan_that_is_refused_changes_nothing():
+    r = Rounds(3, 60, 10, 5)
+    while r.lengths()[0] < 2 * PAGE:
+        r.round([5, 5, -1])
+    r.fork([(0, 2)])
+    c = r.c
+    depth = dev_i32(np.ones((3, N)))
+    for n in ([5, 5, 5], [5, 5, -1]):
+        given = dev_i32(n)
+        rows = c.plan(given, depth)
+        names = ("ctx_len", "block_table", "n_held", "ring", "ring_state",
+                 "extra", "n_served")
+        before = [getattr(c, x).clone() for x in names]
+        slot = rows.slot.clone()
+        none = dev_i32([-1, -1, -1])
+        for bad in ((none, None), (none, depth[:, 1:]), (none, depth.long()),
+                    (none, depth.cpu()), (none[:2], depth),
+                    (none.long(), depth), (none.cpu(), depth),
+                    (c.n_served, depth)):
+            announce("refused plan")
+            with pytest.raises(pct.PCTError if bad[0] is c.n_served
+                               else ValueError):
+                c.plan(*bad)
+            torch.cuda.synchronize()
+            for x, y in zip(before, (getattr(c, x) for x in names)):
+                assert torch.equal(x, y)
+            assert torch.equal(slot, rows.slot) and c.n_nodes is given
+    r.round([5, 4, 3])
