@@ -16,32 +16,34 @@ static uint64_t splitmix64_host(uint64_t x) {
   return x ^ (x >> 31);
 }
 
-// One thread per (request, row, 64-bit word).  Ancestors have smaller
-// indices than their descendants (nodes are in key order), so the walk up
-// from row i can stop as soon as it leaves word w.
+// A thread per (request, row, 64-bit word), and more of them per thread only
+// where a grid would have 2^32 threads, which is cut without an error.
+// Ancestors have smaller indices than their descendants (nodes are in key
+// order), so the walk up from row i can stop as soon as it leaves word w.
 __global__ __launch_bounds__(256) void mask_kernel(int batch, int N,
                                                    int words,
                                                    const int32_t* parent,
                                                    const int32_t* n_nodes,
                                                    uint64_t* mask) {
-  const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t total = (int64_t)batch * N * words;
-  if (g >= total) return;
-  const int w = (int)(g % words);
-  const int i = (int)((g / words) % N);
-  const int q = (int)(g / ((int64_t)words * N));
-  uint64_t bits = 0;
-  if (i < n_nodes[q] && (i >> 6) >= w) {
-    const int32_t* par = parent + (int64_t)q * N;
-    int a = i;
-    while (a >= 0 && (a >> 6) >= w) {
-      if ((a >> 6) == w) bits |= (uint64_t)1 << (a & 63);
-      const int na = par[a];
-      if (na >= a) break;  // malformed input: parents must precede children
-      a = na;
+  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < total;
+       g += (int64_t)gridDim.x * 256) {
+    const int w = (int)(g % words);
+    const int i = (int)((g / words) % N);
+    const int q = (int)(g / ((int64_t)words * N));
+    uint64_t bits = 0;
+    if (i < n_nodes[q] && (i >> 6) >= w) {
+      const int32_t* par = parent + (int64_t)q * N;
+      int a = i;
+      while (a >= 0 && (a >> 6) >= w) {
+        if ((a >> 6) == w) bits |= (uint64_t)1 << (a & 63);
+        const int na = par[a];
+        if (na >= a) break;  // malformed input: parents must precede children
+        a = na;
+      }
     }
+    mask[g] = bits;
   }
-  mask[g] = bits;
 }
 
 // One wave per request.  Node i is accepted when its token equals the
@@ -325,7 +327,8 @@ hipError_t launch_mask(int batch, int N, const int32_t* parent,
                        const int32_t* n_nodes, uint64_t* mask, hipStream_t s) {
   const int words = (N + 63) / 64;
   const int64_t total = (int64_t)batch * N * words;
-  const int blocks = (int)((total + 255) / 256);
+  const int64_t need = (total + 255) / 256;
+  const unsigned blocks = (unsigned)(need < 1 << 23 ? need : 1 << 23);
   hipLaunchKernelGGL(mask_kernel, dim3(blocks), dim3(256), 0, s, batch, N,
                      words, parent, n_nodes, mask);
   return hipGetLastError();
