@@ -555,6 +555,11 @@ size_t carve_adaptive(int batch, int B, int V, int n_max, void* ws,
   w.cv = c.take<int32_t>(pieces * Kf);
   return c.off;
 }
+// A grid has fewer than 2^32 threads (a larger one is cut without an error).
+bool grid_holds(int64_t workgroups, int64_t threads) {
+  return workgroups * threads < (int64_t)1 << 32;
+}
+
 pct_status check_adaptive(int32_t batch, int32_t B, int32_t V, int32_t n_max) {
   if (batch < 1 || B < 1 || V < 1 || n_max < 1)
     return fail(PCT_ERR_INVALID_ARG, "need batch, B, V, n_max >= 1");
@@ -564,6 +569,9 @@ pct_status check_adaptive(int32_t batch, int32_t B, int32_t V, int32_t n_max) {
   if (n_max > kAdaptiveMaxNodes)
     return fail(PCT_ERR_UNSUPPORTED, "n_max = %d exceeds %d", n_max,
                 kAdaptiveMaxNodes);
+  if (!grid_holds((int64_t)batch * B, 1024))
+    return fail(PCT_ERR_UNSUPPORTED, "batch * B = %lld exceeds 2^22 - 1",
+                (long long)batch * B);
   return PCT_OK;
 }
 }  // namespace
@@ -718,6 +726,8 @@ pct_status pct_throughput_curve(int32_t batch, int32_t N, const float* score,
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
   pct_status st = check_cost(cost);
   if (st != PCT_OK) return st;
+  if (!grid_holds(batch, 64))
+    return fail(PCT_ERR_UNSUPPORTED, "batch = %d exceeds 2^26 - 1", batch);
   hipStream_t s = static_cast<hipStream_t>(stream);
   StopArgs a = stop_args(N, n_nodes, score, ctx_len, cost);
   a.f = f;
@@ -758,6 +768,8 @@ pct_status pct_verify_accept(int32_t batch, int32_t N, int32_t B,
   if (!tok || !parent || !depth || !n_nodes || !target || !tau ||
       !accept_node || !accept_tok)
     return fail(PCT_ERR_INVALID_ARG, "required pointer is NULL");
+  if (!grid_holds(batch, 64))
+    return fail(PCT_ERR_UNSUPPORTED, "batch = %d exceeds 2^26 - 1", batch);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
   {

@@ -166,8 +166,8 @@ size_t pct_build_tree_workspace(const pct_tree_shape* shape /*host*/);
  * two candidates (its next sibling and its first child), so the open set
  * stays below 2 n_max + 2 entries.
  * Errors: PCT_ERR_INVALID_ARG for n_max < 1, B < 1, V < 1, V >= 2^18,
- * batch < 1 or null pointers; PCT_ERR_UNSUPPORTED for n_max > 1024 or
- * B > 255; a cost model with negative c1, c2 or c_ell, or with
+ * batch < 1 or null pointers; PCT_ERR_UNSUPPORTED for n_max > 1024, B > 255
+ * or batch * B >= 2^22; a cost model with negative c1, c2 or c_ell, or with
  * C_d + c0 <= 0, is rejected (the stop rule is only the throughput optimum
  * for a positive, convex, increasing cost). */
 pct_status pct_build_tree_adaptive(int32_t batch, int32_t B, int32_t V,
@@ -229,7 +229,8 @@ size_t pct_build_tree_adaptive_pc_workspace(const pct_tree_shape* shape /*host*/
  *  f        [batch][N+1] out
  * Needs no workspace.
  * Errors: PCT_ERR_INVALID_ARG for batch < 1, N < 1, null required pointers
- * or a cost model that is not convex and increasing. */
+ * or a cost model that is not convex and increasing; PCT_ERR_UNSUPPORTED for
+ * batch >= 2^26. */
 pct_status pct_throughput_curve(int32_t batch, int32_t N, const float* score,
                                 const int32_t* n_nodes,
                                 const int32_t* ctx_len,
@@ -267,7 +268,7 @@ pct_status pct_tree_mask(int32_t batch, int32_t N, const int32_t* parent,
  *          -1 padded
  * Needs no workspace.
  * Errors: PCT_ERR_INVALID_ARG for batch < 1, N < 1, B < 1, N > 8192 or
- * null required pointers. */
+ * null required pointers; PCT_ERR_UNSUPPORTED for batch >= 2^26. */
 pct_status pct_verify_accept(int32_t batch, int32_t N, int32_t B,
                              const int32_t* tok, const int32_t* parent,
                              const int32_t* depth, const int32_t* n_nodes,

@@ -192,3 +192,17 @@ def test_verify_sample_workspace():
     assert lib.pct_verify_sample_workspace(32, 256, 151936) == 0
     assert lib.pct_verify_sample_workspace(1, 64, 1000) == 0
     assert lib.pct_verify_sample_workspace(0, 64, 1000) == 0
+
+
+def test_batches_that_no_grid_holds_are_unsupported():
+    lib = pct.lib()
+    d = C.c_void_p(256)
+    assert lib.pct_verify_accept(1 << 26, 1, 1, d, d, d, d, None, d, d, d, d,
+                                 None) == 2
+    assert lib.pct_throughput_curve(1 << 26, 1, d, d, d, None, d, None) == 2
+    for batch, B in ((1 << 22, 1), (1 << 15, 128)):
+        assert lib.pct_build_tree_adaptive_workspace(batch, B, 100, 4) == 0
+        assert lib.pct_build_tree_adaptive(
+            batch, B, 100, 4, d, d, None, d, d, d, d, d, d, d, None, d,
+            1 << 60, None) == 2
+    assert lib.pct_build_tree_adaptive_workspace((1 << 22) - 1, 1, 100, 4) > 0
