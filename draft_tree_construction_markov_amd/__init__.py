@@ -905,7 +905,7 @@ class SharePlan:
     32 heads of 128 over 400 .. 600 own positions: 8 tokens that save 1792
     positions 16.0 and 16.2 us, 7168 17.5 and 19.9; 64 tokens, 4032 32.9 and
     33.0, 16 k 34.7 and 38.0; 16 x 16 rows, 3840 26.0 and 25.3, 61 k 54 and 56;
-    4 x 65 rows, 3072 40 and 31, 12 k 56 and 52; 8 x 257 rows, 57 k 377 and
+    4 x 65 rows, 3 k 40 and 31, 12 k 56 and 52; 8 x 257 rows, 57 k 377 and
     709, 32 x 257, 63 k 669 and 756, where TreeAttention takes 374 and
     482.)"""
 
